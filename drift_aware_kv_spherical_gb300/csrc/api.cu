@@ -1,6 +1,7 @@
 // The C ABI of libpolestar: handle management, argument validation,
 // workspace sizing and dispatch to the kernels.  Declarations and the
 // meaning of every argument are in include/polestar.h.
+#include <cmath>
 #include <cstdio>
 #include <cstdint>
 #include <cstring>
@@ -97,6 +98,8 @@ void trace_clear(TraceSink* t) {
 constexpr int kMaxC = 256;
 constexpr int kMaxD = 8192;
 constexpr int kMaxDh = 256;
+
+bool kv4_dh_ok(int dh) { return dh == 64 || dh == 128 || dh == 256; }
 
 }  // namespace
 
@@ -208,7 +211,6 @@ ps_status ps_trace_get(ps_handle h, int i, const char** name, float* ms) {
 
 size_t ps_workspace_bytes(int op, int B, int N, int d, int C, int Hq, int Hkv,
                           int dh, int k, int P, int V) {
-  (void)k;
   if (B <= 0) return 0;
   switch (op) {
     case PS_OP_KMEANS: return (N > 0 && C > 0) ? kmeans_ws(B, N, d, C) : 0;
@@ -220,6 +222,12 @@ size_t ps_workspace_bytes(int op, int B, int N, int d, int C, int Hq, int Hkv,
     case PS_OP_REFRESH:
       return (N > 0 && d > 0 && Hkv > 0 && dh > 0) ? refresh_ws(B, N, d, Hkv, dh) : 0;
     case PS_OP_COMMIT: return (P > 0 && V > 0) ? commit_ws(B, P, V) : 0;
+    case PS_OP_KV4_ATTN:
+    case PS_OP_KV4_WEIGHT:
+      if (N <= 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || P <= 0 || !kv4_dh_ok(dh)) return 0;
+      return op == PS_OP_KV4_ATTN ? kv4_attn_ws(B, N, Hq, Hkv, dh, P)
+                                  : kv4_weight_ws(B, N, Hq, Hkv, dh, P);
+    case PS_OP_KV4_EVICT: return (Hkv > 0 && k > 0) ? kv4_evict_ws(B, Hkv, k) : 0;
   }
   return 0;
 }
@@ -496,4 +504,138 @@ extern "C" ps_status ps_nvfp4_fetch_dequant(ps_handle h, const void* store, cons
                                          k, mu, rho, tensor_scale, B, N, d, C,
                                          static_cast<__nv_bfloat16*>(Ht),
                                          static_cast<cudaStream_t>(stream)));
+}
+
+// ---- the 4-bit KV cache; see include/polestar.h
+namespace {
+
+// The shape, pointers and tensor scales of a cache.
+ps_status check_kv4(const ps_kv4_cache* c) {
+  PS_REQUIRE(c != nullptr && c->B >= 0 && c->Hkv >= 1 && c->Ncache >= 1 && kv4_dh_ok(c->dh));
+  PS_REQUIRE(c->B <= 65535 && (long)c->B * c->Hkv <= 65535);
+  PS_REQUIRE(std::isnormal(c->kmul) && c->kmul > 0.f && std::isnormal(c->vmul) && c->vmul > 0.f);
+  if (c->B > 0) {
+    PS_PTR(c->kcode); PS_PTR(c->kscale); PS_PTR(c->vcode); PS_PTR(c->vscale);
+  }
+  return PS_OK;
+}
+
+bool ld_ok(int64_t ld, long least, int dtype) {
+  return ld >= least && ld % (dtype == PS_F32 ? 4 : 8) == 0;
+}
+
+ps_status kv4_rows(ps_handle h, const ps_kv4_cache* c, const void* K, const void* V, int dtype,
+                   int R, int64_t ld, const int32_t* off, const int32_t* rows,
+                   const int32_t* cnt, bool load, void* stream) {
+  TraceScope trace_scope(h);
+  PS_REQUIRE(h != nullptr && dtype_ok(dtype) && R >= 0);
+  ps_status st = check_kv4(c);
+  if (st != PS_OK) return st;
+  if (c->B == 0 || R == 0) return PS_OK;
+  PS_REQUIRE(ld_ok(ld, (long)c->Hkv * c->dh, dtype));
+  PS_REQUIRE((long)R * c->Hkv <= INT32_MAX);
+  PS_PTR(K); PS_PTR(V);
+  Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)ld, off, rows, cnt,
+                c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul};
+  return launch_status(kv4_rows_run(a, load, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks a cache and a query and lays out the kernels' arguments; *none is set
+// where there is nothing to do.
+ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, Kv4AttnArgs* a,
+                    bool* none) {
+  PS_REQUIRE(h != nullptr && q != nullptr && dtype_ok(q->dtype) && q->T >= 0);
+  ps_status st = check_kv4(c);
+  if (st != PS_OK) return st;
+  PS_REQUIRE(q->Hq >= c->Hkv && q->Hq % c->Hkv == 0);
+  PS_REQUIRE(std::isfinite(q->scale) && std::isfinite(q->cap) && q->cap >= 0.f);
+  PS_REQUIRE((q->slope == nullptr) || (q->qpos != nullptr));
+  *none = c->B == 0 || q->T == 0;
+  if (*none) return PS_OK;
+  PS_REQUIRE((long)c->B * q->T * q->Hq <= INT32_MAX / 64);
+  PS_REQUIRE(ld_ok(q->q_ld, (long)q->Hq * c->dh, q->dtype));
+  PS_PTR(q->Q);
+  *a = Kv4AttnArgs{};
+  a->kcode = c->kcode; a->kscale = c->kscale; a->vcode = c->vcode; a->vscale = c->vscale;
+  a->Q = q->Q; a->dtype = q->dtype;
+  a->B = c->B; a->T = q->T; a->Hq = q->Hq; a->Hkv = c->Hkv;
+  a->G = q->Hq / c->Hkv; a->M = q->T * a->G;
+  a->Ncache = c->Ncache; a->dh = c->dh; a->q_ld = (long)q->q_ld;
+  a->len = q->len; a->span = q->span; a->kpos = q->kpos; a->qpos = q->qpos; a->slope = q->slope;
+  a->scale = q->scale * c->kmul; a->vmul = c->vmul;
+  a->cap = q->cap; a->inv_cap = q->cap > 0.f ? 1.f / q->cap : 0.f;
+  a->num_sms = h->num_sms; a->status = h->status;
+  return PS_OK;
+}
+
+}  // namespace
+
+extern "C" ps_status ps_kv4_store(ps_handle h, const ps_kv4_cache* c, const void* K,
+                                  const void* V, int dtype, int R, int64_t ld,
+                                  const int32_t* off, const int32_t* rows, const int32_t* cnt,
+                                  void* stream) {
+  return kv4_rows(h, c, K, V, dtype, R, ld, off, rows, cnt, false, stream);
+}
+
+extern "C" ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V, int dtype,
+                                 int R, int64_t ld, const int32_t* off, const int32_t* rows,
+                                 const int32_t* cnt, void* stream) {
+  return kv4_rows(h, c, K, V, dtype, R, ld, off, rows, cnt, true, stream);
+}
+
+extern "C" ps_status ps_kv4_attn(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,
+                                 void* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  TraceScope trace_scope(h);
+  Kv4AttnArgs a;
+  bool none;
+  ps_status st = kv4_query(h, c, q, &a, &none);
+  if (st != PS_OK || none) return st;
+  PS_PTR(O);
+  st = check_ws(kv4_attn_ws(a.B, a.Ncache, a.Hq, a.Hkv, a.dh, a.T), ws, ws_bytes);
+  if (st != PS_OK) return st;
+  a.O = O; a.lse = lse; a.ws = ws;
+  return launch_status(kv4_attn_run(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" ps_status ps_kv4_weight(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,
+                                   const float* lse, const float* w_in, float* w_out, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  TraceScope trace_scope(h);
+  Kv4AttnArgs a;
+  bool none;
+  ps_status st = kv4_query(h, c, q, &a, &none);
+  if (st != PS_OK || none) return st;
+  PS_NN(lse); PS_NN(w_out);
+  st = check_ws(kv4_weight_ws(a.B, a.Ncache, a.Hq, a.Hkv, a.dh, a.T), ws, ws_bytes);
+  if (st != PS_OK) return st;
+  a.lse_in = lse; a.w_in = w_in; a.w_out = w_out; a.ws = ws;
+  return launch_status(kv4_weight_run(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" ps_status ps_kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps_kv4_cache* dst,
+                                  const float* w, const int32_t* len, const int32_t* kpos,
+                                  int keep, int sink, int recent, float* w_dst,
+                                  int32_t* kpos_dst, int32_t* len_dst, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  TraceScope trace_scope(h);
+  PS_REQUIRE(h != nullptr);
+  ps_status st = check_kv4(src);
+  if (st == PS_OK) st = check_kv4(dst);
+  if (st != PS_OK) return st;
+  PS_REQUIRE(src->B == dst->B && src->Hkv == dst->Hkv && src->dh == dst->dh &&
+             src->kmul == dst->kmul && src->vmul == dst->vmul);
+  PS_REQUIRE(keep >= 1 && sink >= 0 && recent >= 0 && (long)sink + recent <= keep &&
+             keep <= dst->Ncache);
+  if (src->B == 0) return PS_OK;
+  PS_NN(w); PS_NN(w_dst); PS_NN(len_dst);
+  PS_REQUIRE(w != w_dst && (kpos == nullptr || kpos != kpos_dst) && len != len_dst);
+  PS_REQUIRE(src->kcode != dst->kcode && src->vcode != dst->vcode &&
+             src->kscale != dst->kscale && src->vscale != dst->vscale);
+  st = check_ws(kv4_evict_ws(src->B, src->Hkv, keep), ws, ws_bytes);
+  if (st != PS_OK) return st;
+  Kv4EvictArgs a{src->kcode, src->kscale, src->vcode, src->vscale,
+                 dst->kcode, dst->kscale, dst->vcode, dst->vscale,
+                 src->B, src->Hkv, src->Ncache, dst->Ncache, src->dh, keep, sink, recent,
+                 w, len, kpos, w_dst, kpos_dst, len_dst, ws};
+  return launch_status(kv4_evict_run(a, static_cast<cudaStream_t>(stream)));
 }

@@ -100,6 +100,43 @@ bool refresh_tc_ok(int dtype, int Hkv, int dh);
 size_t refresh_ws(int B, int N, int d, int Hkv, int dh);
 cudaError_t refresh_run(const RefreshArgs& a, cudaStream_t s);
 
+// the 4-bit KV cache (kv4_cache.cu, kv4_attn.cu, kv4_evict.cu); every array
+// pointer as in include/polestar.h
+struct Kv4RowsArgs {  // store: K, V -> cache; load: cache -> K, V
+  const void* K; const void* V; int dtype; int B, R, Hkv, Ncache, dh; long ld;
+  const int32_t* off; const int32_t* rows; const int32_t* cnt;
+  uint8_t* kcode; uint8_t* kscale; uint8_t* vcode; uint8_t* vscale;
+  float kmul, vmul;
+};
+cudaError_t kv4_rows_run(const Kv4RowsArgs& a, bool load, cudaStream_t s);
+
+struct Kv4AttnArgs {
+  const uint8_t* kcode; const uint8_t* kscale; const uint8_t* vcode; const uint8_t* vscale;
+  const void* Q; int dtype; int B, T, Hq, Hkv, G, M, Ncache, dh; long q_ld;
+  const int32_t* len; const int32_t* span; const int32_t* kpos; const int32_t* qpos;
+  const float* slope;
+  float scale;          // of a raw product: the caller's scale times kmul
+  float vmul, cap, inv_cap;
+  void* O; float* lse;                                    // attention
+  const float* lse_in; const float* w_in; float* w_out;   // weight
+  void* ws; int ntile, nsplit; float* po; float* pml;     // row tiles, shares, their partials
+  int num_sms; int* status;
+};
+size_t kv4_attn_ws(int B, int N, int Hq, int Hkv, int dh, int T);
+size_t kv4_weight_ws(int B, int N, int Hq, int Hkv, int dh, int T);
+cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s);
+cudaError_t kv4_weight_run(const Kv4AttnArgs& a, cudaStream_t s);
+
+struct Kv4EvictArgs {
+  const uint8_t* kcode; const uint8_t* kscale; const uint8_t* vcode; const uint8_t* vscale;
+  uint8_t* kcode_dst; uint8_t* kscale_dst; uint8_t* vcode_dst; uint8_t* vscale_dst;
+  int B, Hkv, Ncache, Ndst, dh, keep, sink, recent;
+  const float* w; const int32_t* len; const int32_t* kpos;
+  float* w_dst; int32_t* kpos_dst; int32_t* len_dst; void* ws;
+};
+size_t kv4_evict_ws(int B, int Hkv, int keep);
+cudaError_t kv4_evict_run(const Kv4EvictArgs& a, cudaStream_t s);
+
 struct CommitArgs {
   const void* logits; int dtype; int B, P, V; const uint8_t* role; uint8_t* undecided;
   const float* D; int d_ld; float* d_sum; int32_t* d_cnt; float* d_prev;

@@ -8,6 +8,7 @@ path: if the library is missing or a call fails, a PolestarError is raised.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -16,18 +17,21 @@ LIB_PATH = os.path.join(_HERE, "libpolestar.so")
 
 PS_OK, PS_ERR_ARG, PS_ERR_UNSUPPORTED, PS_ERR_WORKSPACE, PS_ERR_CUDA, PS_ERR_TIMEOUT = range(6)
 PS_F32, PS_BF16 = 0, 1
-OP_KMEANS, OP_NVFP4, OP_PROXY_KL, OP_TOPK, OP_REFRESH, OP_COMMIT = range(6)
+(OP_KMEANS, OP_NVFP4, OP_PROXY_KL, OP_TOPK, OP_REFRESH, OP_COMMIT, OP_KV4_ATTN,
+ OP_KV4_WEIGHT, OP_KV4_EVICT) = range(9)
 EXPORTED = ["ps_create", "ps_destroy", "ps_check", "ps_status_string", "ps_last_cuda_error",
             "ps_trace_enable", "ps_trace_count", "ps_trace_get",
             "ps_workspace_bytes", "ps_kmeans_spherical", "ps_nvfp4_residual",
             "ps_proxy_attn_kl", "ps_topk_drift", "ps_refresh_kv", "ps_commit",
             "ps_store_record_bytes", "ps_host_alloc", "ps_host_free",
             "ps_nvfp4_pack_clusters", "ps_nvfp4_fetch_dequant", "ps_schedule_step", "ps_drift_score",
-            "ps_block_progress"]
+            "ps_block_progress", "ps_kv4_store", "ps_kv4_load", "ps_kv4_attn",
+            "ps_kv4_weight", "ps_kv4_evict"]
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 
 class PolestarError(RuntimeError):
@@ -92,6 +96,11 @@ _SIGS = {
                            _i, _i, _p, _sz, _p]),
     "ps_commit": (_i, [_p, _p, _i, _i, _i, _i, _p, _p, _p, _i, _p, _p, _p, _p, _i,
                        CommitParams, _p, _p, _p, _p, _sz, _p]),
+    "ps_kv4_store": (_i, [_p, _p, _p, _p, _i, _i, _i64, _p, _p, _p, _p]),
+    "ps_kv4_load": (_i, [_p, _p, _p, _p, _i, _i, _i64, _p, _p, _p, _p]),
+    "ps_kv4_attn": (_i, [_p, _p, _p, _p, _p, _p, _sz, _p]),
+    "ps_kv4_weight": (_i, [_p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "ps_kv4_evict": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
 }
 
 
@@ -379,6 +388,148 @@ def ps_block_progress(commit, undecided, role, out, stream=None):
     st = lib.cdll.ps_block_progress(lib.handle(), _ptr(commit), _ptr(undecided), _ptr(role),
                                     B, P, _store_ptr(out), _stream(stream))
     _check(st, "ps_block_progress")
+
+
+# ---- the 4-bit KV cache (include/polestar.h)
+class Kv4Cache:
+    """A layer's 4-bit KV cache over caller-owned buffers: kcode, vcode
+    [B][Hkv][Ncache][dh/2] and kscale, vscale [B][Hkv][Ncache][dh/16] (uint8),
+    with the tensor scales of K and V."""
+
+    _pack = struct.Struct("4P4i2f")
+
+    def __init__(self, kcode, kscale, vcode, vscale, kmul=1.0, vmul=1.0):
+        self.B, self.Hkv, self.N, half = kcode.shape
+        self.dh = 2 * half
+        want = {2: (kcode, vcode), 16: (kscale, vscale)}
+        for div, ts in want.items():
+            for t in ts:
+                _plain(t, torch.uint8, (self.B, self.Hkv, self.N, self.dh // div))
+        self.buffers = (kcode, kscale, vcode, vscale)
+        self.kmul, self.vmul = float(kmul), float(vmul)
+        self.device = kcode.device
+        self._c = self._pack.pack(*(t.data_ptr() for t in self.buffers), self.B, self.Hkv,
+                                  self.N, self.dh, self.kmul, self.vmul)
+
+    @classmethod
+    def empty(cls, B, Hkv, N, dh, kmul=1.0, vmul=1.0, device="cuda"):
+        """A cache over new buffers."""
+        mk = [torch.zeros(B, Hkv, N, dh // q, dtype=torch.uint8, device=device)
+              for q in (2, 16, 2, 16)]
+        return cls(*mk, kmul=kmul, vmul=vmul)
+
+
+def _plain(t, dtype, shape, null=False):
+    """Pointer of a contiguous device tensor of this dtype and shape."""
+    if t is None and null:
+        return 0
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"expected a contiguous {dtype} device tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows_ld(t, B, H, dh):
+    """(rows, elements between rows) of t [B][R][H][dh], whose rows may be
+    parts of wider ones."""
+    if t.dim() != 4 or t.shape[0] != B or t.shape[2] != H or t.shape[3] != dh or not t.is_cuda:
+        raise ValueError(f"expected a device tensor [{B}][rows][{H}][{dh}], got {tuple(t.shape)}")
+    R = t.shape[1]
+    sb, sr, sh, sd = t.stride()
+    ok = sd == 1 and (sh == dh or H == 1)
+    if R > 1:
+        ok, ld = ok and (sb == R * sr or B == 1), sr
+    else:
+        ld = sb if B > 1 else H * dh
+    if not ok and t.numel() > 0:
+        raise ValueError(f"rows [{H}][{dh}] must be contiguous and equally spaced: strides "
+                         f"{t.stride()}")
+    return R, ld
+
+
+def _kv4_rows(name, c, K, V, off, rows, cnt, stream):
+    R, ld = _rows_ld(K, c.B, c.Hkv, c.dh)
+    if V.dtype != K.dtype or V.stride() != K.stride() or V.shape != K.shape or not V.is_cuda:
+        raise ValueError("K and V need one dtype, shape and stride")
+    lib = _lib()
+    st = getattr(lib.cdll, name)(
+        lib.handle(c.device.index), c._c, K.data_ptr(), V.data_ptr(), _dtype(K), R, ld,
+        _plain(off, torch.int32, (c.B,), True), _plain(rows, torch.int32, (c.B, R), True),
+        _plain(cnt, torch.int32, (c.B,), True), _stream(stream))
+    _check(st, name)
+
+
+def ps_kv4_store(c, K, V, off=None, rows=None, cnt=None, stream=None):
+    """Rows of K and V [B][R][Hkv][dh] (all, or the listed ones) into slots
+    off[b] + r of the cache."""
+    _kv4_rows("ps_kv4_store", c, K, V, off, rows, cnt, stream)
+
+
+def ps_kv4_load(c, K, V, off=None, rows=None, cnt=None, stream=None):
+    """The reverse of ps_kv4_store: slots off[b] + r as rows of K and V."""
+    _kv4_rows("ps_kv4_load", c, K, V, off, rows, cnt, stream)
+
+
+_Q_PACK = struct.Struct("6Pq3i2f")
+
+
+def _kv4_query(c, Q, len, span, kpos, qpos, slope, scale, cap):
+    if Q.dim() != 4:
+        raise ValueError(f"expected Q [B][T][Hq][dh], got {tuple(Q.shape)}")
+    Hq = Q.shape[2]
+    T, ld = _rows_ld(Q, c.B, Hq, c.dh)
+    i32 = torch.int32
+    return T, Hq, _Q_PACK.pack(
+        Q.data_ptr(), _plain(len, i32, (c.B,), True), _plain(span, i32, (c.B, T, 2), True),
+        _plain(kpos, i32, (c.B, c.Hkv, c.N), True), _plain(qpos, i32, (c.B, T), True),
+        _plain(slope, torch.float32, (Hq,), True), ld, _dtype(Q), T, Hq, scale, cap)
+
+
+def ps_kv4_attn(c, Q, O, lse=None, *, scale, len=None, span=None, kpos=None, qpos=None,
+                slope=None, cap=0.0, ws=None, stream=None):
+    """Attention of Q [B][T][Hq][dh] over the cache into O (Q's dtype) and lse
+    [B][T][Hq]; what a row sees, the cap and the distance bias as in
+    include/polestar.h."""
+    lib = _lib()
+    T, Hq, q = _kv4_query(c, Q, len, span, kpos, qpos, slope, scale, cap)
+    w, wn = _ws(ws)
+    st = lib.cdll.ps_kv4_attn(lib.handle(c.device.index), c._c, q,
+                              _plain(O, Q.dtype, (c.B, T, Hq, c.dh)),
+                              _plain(lse, torch.float32, (c.B, T, Hq), True), w, wn,
+                              _stream(stream))
+    _check(st, "ps_kv4_attn")
+
+
+def ps_kv4_weight(c, Q, lse, w_in, w_out, *, scale, len=None, span=None, kpos=None, qpos=None,
+                  slope=None, cap=0.0, ws=None, stream=None):
+    """w_out = w_in (None: 0) + the attention weight that Q's rows put on each
+    slot [B][Hkv][Ncache]; lse as ps_kv4_attn wrote it."""
+    lib = _lib()
+    T, Hq, q = _kv4_query(c, Q, len, span, kpos, qpos, slope, scale, cap)
+    shape = (c.B, c.Hkv, c.N)
+    w, wn = _ws(ws)
+    st = lib.cdll.ps_kv4_weight(lib.handle(c.device.index), c._c, q,
+                                _plain(lse, torch.float32, (c.B, T, Hq)),
+                                _plain(w_in, torch.float32, shape, True),
+                                _plain(w_out, torch.float32, shape), w, wn, _stream(stream))
+    _check(st, "ps_kv4_weight")
+
+
+def ps_kv4_evict(src, dst, w, w_dst, len_dst, keep, sink=0, recent=0, len=None, kpos=None,
+                 kpos_dst=None, ws=None, stream=None):
+    """Keeps `keep` slots of every (sequence, KV head) of src -- the first
+    `sink`, the last `recent` and the heaviest of the others by w -- in the
+    first slots of dst."""
+    lib = _lib()
+    f32, i32 = torch.float32, torch.int32
+    a, b = (src.B, src.Hkv, src.N), (src.B, src.Hkv, dst.N)
+    wsp, wn = _ws(ws)
+    st = lib.cdll.ps_kv4_evict(
+        lib.handle(src.device.index), src._c, dst._c, _plain(w, f32, a),
+        _plain(len, i32, (src.B,), True), _plain(kpos, i32, a, True), int(keep), int(sink),
+        int(recent), _plain(w_dst, f32, b), _plain(kpos_dst, i32, b, True),
+        _plain(len_dst, i32, (src.B,)), wsp, wn, _stream(stream))
+    _check(st, "ps_kv4_evict")
 
 
 # ---- refresh schedule of the decode loop (include/polestar.h; host only)

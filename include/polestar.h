@@ -54,7 +54,8 @@ typedef enum { PS_F32 = 0, PS_BF16 = 1 } ps_dtype;
 
 typedef enum {
   PS_OP_KMEANS = 0, PS_OP_NVFP4 = 1, PS_OP_PROXY_KL = 2,
-  PS_OP_TOPK = 3, PS_OP_REFRESH = 4, PS_OP_COMMIT = 5
+  PS_OP_TOPK = 3, PS_OP_REFRESH = 4, PS_OP_COMMIT = 5,
+  PS_OP_KV4_ATTN = 6, PS_OP_KV4_WEIGHT = 7, PS_OP_KV4_EVICT = 8
 } ps_op;
 
 typedef struct ps_handle_s* ps_handle;
@@ -460,6 +461,115 @@ typedef struct {
 
 int ps_schedule_step(const ps_schedule_params* p, ps_schedule_state* s,
                      int committed, int block_done);
+
+/* ---------------------------------------------------------------------------
+ * The 4-bit KV cache: rows in and out, the attention that reads it, the
+ * weight that attention puts on its slots, and eviction by that weight.
+ * [Polestar §2.A, sparse updates] keeps a KV cache that the refresh writes;
+ * holding it in NVFP4 and dropping rows of it are this library's own.
+ *
+ * A layer's cache holds a K and a V row for every (sequence, KV head, slot):
+ *   codes  [B][Hkv][Ncache][dh/2]  u8  E2M1, element 2j in byte j's low nibble
+ *   scales [B][Hkv][Ncache][dh/16] u8  E4M3, one per 16 elements along dh
+ * and two tensor scales (host values, positive and normal): an element is
+ * code * scale * kmul (vmul).  dh is 64, 128 or 256.  144 bytes a slot and
+ * head for dh = 128, against 512 in bf16.  A slot that was never stored may
+ * hold any bytes; calls never let it reach a result.
+ *
+ * ps_kv4_attn and ps_kv4_weight also need B * Hkv <= 65535; every call needs
+ * B >= 0 (0: no-op), Hkv >= 1, Ncache >= 1 and 16-byte aligned codes, scales,
+ * K, V, Q and O.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* kcode;
+  uint8_t* kscale;
+  uint8_t* vcode;
+  uint8_t* vscale;
+  int B, Hkv, Ncache, dh;
+  float kmul, vmul;
+} ps_kv4_cache;
+
+/* Stores rows of K and V.  For every list entry j < min(cnt[b], R) (R where
+ * cnt is NULL), r = rows[b*R + j] (j where rows is NULL) names row r of
+ * sequence b, which goes to slot off[b] + r (off NULL: 0); entries with r
+ * outside [0, R) or a slot outside the cache are skipped, other slots are
+ * untouched.  ps_topk_drift's pos / npos are such a list.
+ * Per 16 elements x: s = E4M3(fl(amax / fl(6 S))), code = E2M1(fl(x / fl(s S))),
+ * RNE, saturating, 0 where s == 0 (S = kmul or vmul): ps_nvfp4_residual's
+ * rounding with a given tensor scale.  Bit-exact.  Infinities saturate, a NaN
+ * becomes 6 s S.
+ * K, V: element (b, r, h, i) at [(b*R + r)*ld + h*dh + i], f32 or bf16 (dtype);
+ *   ld >= Hkv*dh, a multiple of 16 bytes (K and V may be parts of one
+ *   projection's output);  off [B], rows [B][R], cnt [B] i32 or NULL.
+ * A slot named twice in one call holds either row. */
+ps_status ps_kv4_store(ps_handle h, const ps_kv4_cache* c, const void* K,
+                       const void* V, int dtype, int R, int64_t ld,
+                       const int32_t* off, const int32_t* rows,
+                       const int32_t* cnt, void* stream);
+
+/* The reverse, with the same list: element = fl(code * s * S) rounded to
+ * dtype (bf16: RNE) into K and V; rows not listed are untouched. */
+ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V,
+                      int dtype, int R, int64_t ld, const int32_t* off,
+                      const int32_t* rows, const int32_t* cnt, void* stream);
+
+/* Queries of T tokens a sequence and what they see of the cache.
+ *   s   = scale * <q, k>                       k as the cache holds it
+ *   s   = cap * tanh(s / cap)                  if cap > 0
+ *   s  -= slope[h] * |qpos[b][t] - pos|        if slope (and qpos) given
+ * Slot n of head g holds position kpos[b][g][n] (kpos NULL: n).  Row (b, t)
+ * sees slot n iff n < len[b] (len NULL: Ncache) and span[b][t][0] <= pos <
+ * span[b][t][1] (span NULL: all): causal is [0, qpos + 1), a prefix mask
+ * [0, max(prefix, qpos + 1)), a document mask the document's bounds.
+ * Q: element (b, t, h, i) at [(b*T + t)*q_ld + h*dh + i]; query head h reads
+ * KV head h / (Hq / Hkv). */
+typedef struct {
+  const void* Q;
+  const int32_t* len;   /* [B] or NULL                                      */
+  const int32_t* span;  /* [B][T][2] or NULL                                */
+  const int32_t* kpos;  /* [B][Hkv][Ncache] or NULL                         */
+  const int32_t* qpos;  /* [B][T], needed with slope                        */
+  const float* slope;   /* [Hq] or NULL                                     */
+  int64_t q_ld;         /* >= Hq*dh, a multiple of 16 bytes                 */
+  int dtype, T, Hq;     /* PS_F32 or PS_BF16; T >= 0 (0: no-op)             */
+  float scale, cap;     /* finite; cap >= 0, 0 for none                     */
+} ps_kv4_query;
+
+/* O [B][T][Hq][dh] (dtype) = softmax over the seen slots of s, times V;
+ * lse [B][T][Hq] f32 (nullable) = ln sum exp s.  A row that sees nothing gives
+ * O = 0 and lse = -inf.  Sums and statistics in fp32; the products' operands
+ * are f16: the cache's values and bf16 queries exact, fp32 queries and their
+ * weights in two f16 terms, the weights of bf16 queries rounded to 11 bits.
+ * Deterministic.  Workspace: ps_workspace_bytes(PS_OP_KV4_ATTN, B, N = Ncache,
+ * Hq, Hkv, dh, P = T). */
+ps_status ps_kv4_attn(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,
+                      void* O, float* lse, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* w_out[b][g][n] = w_in[b][g][n] + the sum over the T tokens and the query
+ * heads of group g of exp(s - lse), lse [B][T][Hq] as ps_kv4_attn wrote it for
+ * the same query; slots that no row sees get w_in (w_in NULL: 0).  w_in may be
+ * w_out.  [B][Hkv][Ncache] f32.  Deterministic.  Workspace: PS_OP_KV4_WEIGHT,
+ * same sizes. */
+ps_status ps_kv4_weight(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,
+                        const float* lse, const float* w_in, float* w_out,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* Evicts: copies the kept slots of every (sequence, KV head) of src, in
+ * ascending order, to the first slots of dst (another cache of the same B,
+ * Hkv, dh and tensor scales, dst->Ncache >= keep, no memory in common).
+ * len[b] <= keep: all len[b] slots.  Else `keep` of them: the first `sink`, the
+ * last `recent`, and of the others the ones of largest w, ties to the lower
+ * slot, NaN below every number.  w_dst and kpos_dst [B][Hkv][dst->Ncache] take
+ * the kept slots' weights and positions (kpos NULL: the slot itself; kpos_dst
+ * nullable), len_dst[b] = min(len[b], keep).  What lies past that is untouched.
+ * 0 <= sink, recent; sink + recent <= keep; keep >= 1.  Bit-exact.
+ * Workspace: PS_OP_KV4_EVICT with B, N = Ncache, Hkv, k = keep. */
+ps_status ps_kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps_kv4_cache* dst,
+                       const float* w, const int32_t* len, const int32_t* kpos,
+                       int keep, int sink, int recent, float* w_dst,
+                       int32_t* kpos_dst, int32_t* len_dst, void* ws,
+                       size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -58,3 +58,4 @@ __all__ = [
 ]
 from .schedule import ScheduleState, schedule_step, block_progress
 from .scorers import SCORER_KL, SCORER_COSINE, SCORER_ENTROPY, drift_score
+from .kv4 import (kv4_encode, kv4_decode, kv4_scores, kv4_attention, kv4_weight, kv4_keep)
