@@ -66,4 +66,71 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr float kPShift = 12.f;  // log2 of the factor that P carries
+
+// Per-row constants of a tile, in shared memory.
+struct RowPar {
+  float f;       // score of a raw product: natural units
+  float slope;   // distance bias
+  int lo, hi;    // visible positions
+  int qpos;
+  float lse;     // k_kv4_weight
+};
+
+__device__ __forceinline__ int kv4_len(const Kv4AttnArgs& a, int b) {
+  return min(max(a.len != nullptr ? a.len[b] : a.Ncache, 0), a.Ncache);
+}
+
+// The power of two that a query row is scaled by before it is rounded to f16
+// (2^14 <= max |q| * up < 2^15; 1 for a row without a finite non-zero
+// maximum), and the factor that takes a product with K back to a score.  A
+// negative scale turns the query's sign instead, so the factor is positive
+// and row maxima may be taken of raw products.
+__device__ __forceinline__ void row_scale(float mx, float scale, float* up, float* f) {
+  int ex = 0;
+  if (mx > 0.f && mx < INFINITY) ex = 14 - ilogbf(mx);
+  ex = min(max(ex, -110), 110);
+  *up = __uint_as_float((uint32_t)(127 + ex) << 23) * (scale < 0.f ? -1.f : 1.f);
+  *f = fmaxf(fabsf(scale) * __uint_as_float((uint32_t)(127 - ex) << 23), FLT_MIN);
+}
+
+// The score of a raw product in natural units, before the mask.
+template <bool ACC>
+__device__ __forceinline__ float kv4_score(const Kv4AttnArgs& a, float raw, float f, float slope,
+                                           int qpos, int pos) {
+  float x = raw * f;
+  if (a.cap > 0.f) {
+    if constexpr (ACC) {
+      x = a.cap * tanhf(x * a.inv_cap);
+    } else {
+      // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7, which the cap
+      // scales to under 1e-5 of a score, far below P's own rounding
+      const float e = exp2_approx(x * a.inv_cap * (2.f * kLog2e));
+      x = a.cap * (1.f - 2.f * rcp_approx(e + 1.f));
+    }
+  }
+  if (a.slope != nullptr) x -= slope * fabsf((float)(qpos - pos));
+  return x;
+}
+
+// Four elements of a finished row: O = acc / l, lse = (mx + log2 l') ln 2.
+template <bool F32>
+__device__ __forceinline__ void kv4_finish(const Kv4AttnArgs& a, int b, int hkv, int m, int dh,
+                                           int d, float4 acc, float mx, float l) {
+  const int t = m / a.G, h = hkv * a.G + m % a.G;
+  const long row = ((long)b * a.T + t) * a.Hq + h;
+  const float inv = l == 0.f ? 0.f : a.vmul / l;  // l == 0: nothing seen
+  const float x = acc.x * inv, y = acc.y * inv, z = acc.z * inv, w = acc.w * inv;
+  if constexpr (F32) {
+    reinterpret_cast<float4*>(static_cast<float*>(a.O) + row * dh + d)[0] = make_float4(x, y, z, w);
+  } else {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x, y), q = __floats2bfloat162_rn(z, w);
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + row * dh + d)[0] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+  }
+  if (d == 0 && a.lse != nullptr)
+    a.lse[row] = l == 0.f ? -INFINITY
+                          : ((mx == -INFINITY ? 0.f : mx - kPShift) + log2f(l)) * kLn2;
+}
+
 }  // namespace ps

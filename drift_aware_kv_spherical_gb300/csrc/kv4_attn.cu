@@ -30,21 +30,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kPShift = 12.f;  // log2 of the factor that P carries
-
-// Per-row constants of a tile, in shared memory.
-struct RowPar {
-  float f;       // score of a raw product: natural units
-  float slope;   // distance bias
-  int lo, hi;    // visible positions
-  int qpos;
-  float lse;     // k_kv4_weight
-};
-
-__device__ __forceinline__ int kv4_len(const Kv4AttnArgs& a, int b) {
-  return min(max(a.len != nullptr ? a.len[b] : a.Ncache, 0), a.Ncache);
-}
-
 // Rows [m0, m0 + rows) of (b, hkv) into shared memory as A fragments
 // [mt][part][ks][lane] (uint4), with their constants; rows past M are zero
 // and see nothing.  One warp a row.
@@ -82,12 +67,8 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
 #pragma unroll
     for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
     mx = warp_max(mx);
-    // 2^(14 - floor(log2 mx)); 1 for a row without a finite non-zero maximum
-    int ex = 0;
-    if (mx > 0.f && mx < INFINITY) ex = 14 - ilogbf(mx);
-    ex = min(max(ex, -120), 120);
-    const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-    p.f = a.scale * __uint_as_float((uint32_t)(127 - ex) << 23);
+    float up;
+    row_scale(mx, a.scale, &up, &p.f);
     if (lane == 0) par[r] = p;
     __half* hq = reinterpret_cast<__half*>(qs);
 #pragma unroll
@@ -181,45 +162,6 @@ __device__ __forceinline__ void dequant_k(const RawK<DH>& r, uint32_t (*kf)[DH /
       kf[j][2 * w + 1][0] = h2_bits(__hmul2(h2_of(h[2]), s));
       kf[j][2 * w + 1][1] = h2_bits(__hmul2(h2_of(h[3]), s));
     }
-}
-
-// The score of a raw product in natural units, before the mask.
-template <bool ACC>
-__device__ __forceinline__ float kv4_score(const Kv4AttnArgs& a, float raw, float f, float slope,
-                                           int qpos, int pos) {
-  float x = raw * f;
-  if (a.cap > 0.f) {
-    if constexpr (ACC) {
-      x = a.cap * tanhf(x * a.inv_cap);
-    } else {
-      // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7, which the cap
-      // scales to under 1e-5 of a score, far below P's own rounding
-      const float e = exp2_approx(x * a.inv_cap * (2.f * kLog2e));
-      x = a.cap * (1.f - 2.f * rcp_approx(e + 1.f));
-    }
-  }
-  if (a.slope != nullptr) x -= slope * fabsf((float)(qpos - pos));
-  return x;
-}
-
-// Four elements of a finished row: O = acc / l, lse = (mx + log2 l') ln 2.
-template <bool F32>
-__device__ __forceinline__ void kv4_finish(const Kv4AttnArgs& a, int b, int hkv, int m, int dh,
-                                           int d, float4 acc, float mx, float l) {
-  const int t = m / a.G, h = hkv * a.G + m % a.G;
-  const long row = ((long)b * a.T + t) * a.Hq + h;
-  const float inv = l == 0.f ? 0.f : a.vmul / l;  // l == 0: nothing seen
-  const float x = acc.x * inv, y = acc.y * inv, z = acc.z * inv, w = acc.w * inv;
-  if constexpr (F32) {
-    reinterpret_cast<float4*>(static_cast<float*>(a.O) + row * dh + d)[0] = make_float4(x, y, z, w);
-  } else {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(x, y), q = __floats2bfloat162_rn(z, w);
-    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + row * dh + d)[0] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
-  }
-  if (d == 0 && a.lse != nullptr)
-    a.lse[row] = l == 0.f ? -INFINITY
-                          : ((mx == -INFINITY ? 0.f : mx - kPShift) + log2f(l)) * kLn2;
 }
 
 template <int DH, int MT, bool F32>
@@ -588,6 +530,13 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   }
 }
 
+template <int DH, bool F32>
+cudaError_t launch_combine(const Kv4AttnArgs& a, cudaStream_t s) {
+  const long rows = (long)a.B * a.Hkv * a.M;
+  return launch_pdl(k_kv4_combine<DH, F32>, dim3((unsigned)ceil_div(rows * (DH / 4), 128)),
+                    dim3(128), 0, s, a);
+}
+
 template <int DH, int MT, bool F32>
 cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t q_bytes = (size_t)MT * (F32 ? 2 : 1) * (DH / 16) * 32 * 16;
@@ -604,9 +553,7 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   const long grid = (long)a.B * a.Hkv * a.nsplit * a.ntile;
   cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess || a.nsplit == 1) return e;
-  const long rows = (long)a.B * a.Hkv * a.M;
-  return launch_pdl(k_kv4_combine<DH, F32>, dim3((unsigned)ceil_div(rows * (DH / 4), 128)),
-                    dim3(128), 0, s, a);
+  return launch_combine<DH, F32>(a, s);
 }
 
 template <int DH, bool F32>
@@ -629,24 +576,51 @@ cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
                     smem, s, a, steps);
 }
 
-// Rows of a tile (16 or 32) and shares of the slots for these sizes.
-void attn_plan(int B, int N, int Hq, int Hkv, int dh, int T, int* mt, int* ntile, int* nsplit) {
+// The kernel, rows of a tile, tiles and shares of the slots for these sizes.
+struct AttnPlan {
+  bool tc;  // k_kv4_attn_tc: 256-row tiles; else k_kv4_attn with 16 mt rows
+  int mt, ntile, nsplit;
+};
+AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
+  AttnPlan p;
   const int M = T * (Hq / Hkv);
-  *mt = (M > 16 && dh <= 128) ? 2 : 1;
-  *ntile = ceil_div(M, 16 * *mt);
-  const long base = (long)B * Hkv * *ntile;
+  p.tc = dtype == PS_BF16 && dh <= 128 && M >= 64;
+  if (p.tc) {
+    p.mt = 0;
+    p.ntile = ceil_div(M, 256);
+    // rounds of CTAs (one an SM) times the steps of each, set-up and join
+    // counted as four steps
+    const long base = (long)B * Hkv * p.ntile;
+    const int steps = ceil_div(N, 128);
+    p.nsplit = 1;
+    long best = ceil_div(base, kSmTarget) * (long)(steps + 4);
+    for (int ns = 2; ns <= 64 && ns <= steps; ++ns) {
+      const long cost = ceil_div(base * ns, kSmTarget) * (long)(ceil_div(steps, ns) + 4) + 4;
+      if (cost < best) {
+        best = cost;
+        p.nsplit = ns;
+      }
+    }
+    return p;
+  }
+  p.mt = (M > 16 && dh <= 128) ? 2 : 1;
+  p.ntile = ceil_div(M, 16 * p.mt);
+  const long base = (long)B * Hkv * p.ntile;
   const int most = ceil_div(N, 128);  // at least 128 slots a share
   long want = ceil_div(4 * kSmTarget, base);
   if (want > most) want = most;
   if (want > 256) want = 256;
-  *nsplit = (int)(want < 1 ? 1 : want);
+  p.nsplit = (int)(want < 1 ? 1 : want);
+  return p;
 }
 
 }  // namespace
 
 size_t kv4_attn_ws(int B, int N, int Hq, int Hkv, int dh, int T) {
-  int mt, ntile, nsplit;
-  attn_plan(B, N, Hq, Hkv, dh, T, &mt, &ntile, &nsplit);
+  // either type's: the size does not name it
+  const int a = attn_plan(PS_BF16, B, N, Hq, Hkv, dh, T).nsplit;
+  const int b = attn_plan(PS_F32, B, N, Hq, Hkv, dh, T).nsplit;
+  const int nsplit = a > b ? a : b;
   if (nsplit == 1) return 0;
   Carver c(nullptr);
   const size_t rows = (size_t)B * T * Hq * nsplit;
@@ -658,8 +632,9 @@ size_t kv4_attn_ws(int B, int N, int Hq, int Hkv, int dh, int T) {
 size_t kv4_weight_ws(int, int, int, int, int, int) { return 0; }
 
 cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
-  int mt;
-  attn_plan(a.B, a.Ncache, a.Hq, a.Hkv, a.dh, a.T, &mt, &a.ntile, &a.nsplit);
+  const AttnPlan p = attn_plan(a.dtype, a.B, a.Ncache, a.Hq, a.Hkv, a.dh, a.T);
+  a.ntile = p.ntile;
+  a.nsplit = p.nsplit;
   if (a.nsplit > 1) {
     Carver c(a.ws);
     const size_t rows = (size_t)a.B * a.T * a.Hq * a.nsplit;
@@ -667,8 +642,13 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
     a.pml = c.take<float>(rows * 2);
   }
   const bool f32 = a.dtype == PS_F32;
+  if (p.tc) {
+    cudaError_t e = kv4_attn_tc_launch(a, s);
+    if (e != cudaSuccess || a.nsplit == 1) return e;
+    return a.dh == 64 ? launch_combine<64, false>(a, s) : launch_combine<128, false>(a, s);
+  }
 #define PS_KV4_CASE(DH, MT)                                                          \
-  if (a.dh == DH && mt == MT)                                                        \
+  if (a.dh == DH && p.mt == MT)                                                      \
     return f32 ? launch_attn<DH, MT, true>(a, s) : launch_attn<DH, MT, false>(a, s);
   PS_KV4_CASE(64, 1)
   PS_KV4_CASE(64, 2)
