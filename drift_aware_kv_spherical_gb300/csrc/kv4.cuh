@@ -113,7 +113,13 @@ __device__ __forceinline__ float kv4_score(const Kv4AttnArgs& a, float raw, floa
   return x;
 }
 
-// Four elements of a finished row: O = acc / l, lse = (mx + log2 l') ln 2.
+// lse of a row whose sum l is of 2^(x - mx + kPShift), x its log2-unit scores
+// (mx = -inf: nothing but NaN was seen, or nothing at all and l == 0).
+__device__ __forceinline__ float row_lse(float mx, float l) {
+  return l == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx - kPShift) + log2f(l)) * kLn2;
+}
+
+// Four elements of a finished row: O = acc / l.
 template <bool F32>
 __device__ __forceinline__ void kv4_finish(const Kv4AttnArgs& a, int b, int hkv, int m, int dh,
                                            int d, float4 acc, float mx, float l) {
@@ -128,9 +134,7 @@ __device__ __forceinline__ void kv4_finish(const Kv4AttnArgs& a, int b, int hkv,
     reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + row * dh + d)[0] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
   }
-  if (d == 0 && a.lse != nullptr)
-    a.lse[row] = l == 0.f ? -INFINITY
-                          : ((mx == -INFINITY ? 0.f : mx - kPShift) + log2f(l)) * kLn2;
+  if (d == 0 && a.lse != nullptr) a.lse[row] = row_lse(mx, l);
 }
 
 }  // namespace ps

@@ -2,7 +2,7 @@
 // tcgen05 tensor cores.
 //
 // A CTA takes 256 rows (two tiles of 128) of one KV head against a share of
-// its slots, 128 slots at a time.  16 warps:
+// its slots, 128 slots at a time.  13 warps:
 //   0-3, 4-7  softmax of row tile 0 / 1: a thread a row.  Reads its 128 scores
 //             from TMEM, keeps the running maximum and sum in registers, writes
 //             P (f16) over the scores, rescales O in TMEM when it must
@@ -13,7 +13,6 @@
 //             same placement)
 //   12        issues the MMAs: S into 128 TMEM columns a row tile, O into 128
 //             more; P is the TMEM-resident A operand of P V
-//   13-15     complete the warpgroup for the register split
 // Order of the MMAs, per 128 slots j:  P0 V(j), S0(j+1), P1 V(j), S1(j+1): the
 // softmax of one row tile runs under the two products of the other.  The
 // commit that announces S(j+1) also says that P V(j) is done, so O may be
@@ -28,10 +27,7 @@
 namespace ps {
 namespace {
 
-constexpr int kTcThreads = 512;
-// Registers a thread after the split: 256 x 184 + 256 x 72 = 512 x 128, what
-// the CTA is launched with.
-constexpr int kLaunchRegs = 128;
+constexpr int kTcThreads = 416;
 constexpr int kTile = 128;          // slots a step; rows of a row tile
 constexpr float kGrow = 8.f;        // log2 growth of a maximum before O is rescaled
 constexpr float kTcShift = 4.f;     // log2 of the factor that P carries: P <= 2^12 in f16
@@ -41,14 +37,26 @@ struct TcSmem {
   static constexpr uint32_t kOp = (DH / 64) * 16384u;  // 128 rows of DH f16
   static constexpr uint32_t kK = 2 * kOp,  // Q at 0
                              kV = 4 * kOp, kPos = 6 * kOp;
-  static constexpr uint32_t kPar = kPos + 4 * kTile * 4;
-  static constexpr uint32_t kBar = kPar + 256 * sizeof(RowPar);
+  static constexpr uint32_t kFac = kPos + 4 * kTile * 4;
+  static constexpr uint32_t kBar = kFac + 256 * 4;
   static constexpr size_t kBytes = 1024 + kBar + 256;
 };
 
 // Byte offset of 16-byte chunk c (of DH / 8) of row r in an operand.
 __device__ __forceinline__ uint32_t sw128(int r, int c) {
   return (uint32_t)(c >> 3) * 16384u + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+// One lane of a converged warp.  The MMAs below are issued under this and not
+// under `lane == 0`: the operands of tcgen05.mma live in uniform registers, and
+// under a thread-indexed branch each instruction took 120 clocks to issue
+// (measured; 64 elected, the rate of the tensor cores at this size).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // D(tmem) (+)= A . B, f16 operands: A from shared memory, or from TMEM.
@@ -109,45 +117,120 @@ __device__ __forceinline__ void put_row(uint8_t* op, int r, const RawRow<DH>& v)
   }
 }
 
-// 256 query rows as f16 operands, with their constants: DH / 8 lanes a row.
+// 256 query rows as f16 operands and their score factors, DH / 8 lanes a row;
+// all of a thread's rows are loaded before the first is used.
 template <int DH>
 __device__ __forceinline__ void stage_queries(const Kv4AttnArgs& a, int b, int hkv, int m0,
-                                              uint8_t* qs, RowPar* par) {
-  constexpr int LN = DH / 8;                    // lanes a row
-  constexpr int RP = kTcThreads / LN;           // rows a pass
-  const int sub = threadIdx.x % LN, tid_lane = threadIdx.x & 31;
-#pragma unroll 2
-  for (int r = threadIdx.x / LN; r < 2 * kTile; r += RP) {
-    const int m = m0 + r;
-    float x[8];
-    RowPar p{0.f, 0.f, 0, 0, 0, 0.f};
-    if (m < a.M) {
-      const int t = m / a.G, h = hkv * a.G + m % a.G;
-      const long tok = (long)b * a.T + t;
-      load16(static_cast<const __nv_bfloat16*>(a.Q) + tok * a.q_ld + (long)h * DH + sub * 8, x);
-      p.slope = a.slope != nullptr ? a.slope[h] : 0.f;
-      p.lo = a.span != nullptr ? a.span[2 * tok] : 0;
-      p.hi = a.span != nullptr ? a.span[2 * tok + 1] : INT32_MAX;
-      p.qpos = a.qpos != nullptr ? a.qpos[tok] : 0;
-    } else {
+                                              uint8_t* qs, float* fac) {
+  constexpr int LN = DH / 8;                          // lanes a row
+  constexpr int RP = kTcThreads / LN;                 // rows a pass
+  constexpr int NP = (2 * kTile + RP - 1) / RP;       // passes
+  const int sub = threadIdx.x % LN;
+  uint4 raw[NP];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  for (int i = 0; i < NP; ++i) {
+    const int r = threadIdx.x / LN + i * RP, m = m0 + r;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < 2 * kTile && m < a.M) {
+      const int t = m / a.G, h = hkv * a.G + m % a.G;
+      raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Q) +
+                                                    ((long)b * a.T + t) * a.q_ld + (long)h * DH +
+                                                    sub * 8));
     }
+  }
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = threadIdx.x / LN + i * RP;
+    float x[8];
+    unpack16(raw[i], x, __nv_bfloat16{});
     float mx = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
-    const uint32_t mask = (uint32_t)((1ull << LN) - 1) << (tid_lane & ~(LN - 1));
 #pragma unroll
-    for (int o = LN / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, o));
-    float up;
-    row_scale(mx, a.scale, &up, &p.f);
-    if (sub == 0) par[r] = p;
+    for (int o = LN / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float up, f;
+    row_scale(mx, a.scale, &up, &f);
+    if (r >= 2 * kTile) continue;
+    if (sub == 0) fac[r] = f;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = h2_bits(__floats2half2_rn(x[2 * e] * up, x[2 * e + 1] * up));
     *reinterpret_cast<uint4*>(qs + (r / kTile) * TcSmem<DH>::kOp + sw128(r % kTile, sub)) =
         make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The constants of a softmax thread's row.
+struct TcRow {
+  float f;                // score factor of a raw product
+  float slope2;           // distance bias in log2 units
+  int lo, hi, qpos;
+};
+
+// s[0..63]: raw products of 64 slots from n0 on -> log2-unit scores (GEN), and
+// -inf where the row does not see the slot.  pos: explicit positions, or null.
+template <bool GEN>
+__device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, const TcRow& row,
+                                          int n0, int len, bool masked, const int* pos) {
+  if constexpr (GEN) {
+    if (a.cap > 0.f) {
+      const float fy = row.f * a.inv_cap, cap2 = a.cap * kLog2e;
+      float top = 0.f;
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        s[c] *= fy;
+        top = fmaxf(top, fabsf(s[c]));
+      }
+      if (__all_sync(0xffffffffu, top <= 0.4f)) {
+        // tanh's series to y^11: the next term is under 2^-23 of y here
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          const float y = s[c], z = y * y;
+          float q = fmaf(z, -1382.f / 155925.f, 62.f / 2835.f);
+          q = fmaf(z, q, -17.f / 315.f);
+          q = fmaf(z, q, 2.f / 15.f);
+          q = fmaf(z, q, -1.f / 3.f);
+          q = z * q;
+          s[c] = cap2 * fmaf(y, q, y);
+        }
+      } else {
+        // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          const float e = exp2_approx(s[c] * (2.f * kLog2e));
+          s[c] = cap2 * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
+        }
+      }
+    } else {
+      const float f2 = row.f * kLog2e;
+#pragma unroll
+      for (int c = 0; c < 64; ++c) s[c] *= f2;
+    }
+    if (a.slope != nullptr) {
+      if (pos == nullptr) {
+        const float dq = (float)(row.qpos - n0);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = fmaf(-row.slope2, fabsf(dq - (float)c), s[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          s[c] = fmaf(-row.slope2, fabsf((float)(row.qpos - pos[c])), s[c]);
+      }
+    }
+    if (masked && pos != nullptr) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        if (n0 + c >= len || pos[c] < row.lo || pos[c] >= row.hi) s[c] = -INFINITY;
+      return;
+    }
+  }
+  if (masked) {  // columns [lo, hi) are seen
+    const int lo = (int)min(max((long)row.lo - n0, 0L), 64L);
+    const int hi = (int)min(max((long)min(row.hi, len) - n0, 0L), 64L);
+#pragma unroll
+    for (int c = 0; c < 64; ++c)
+      if (c < lo || c >= hi) s[c] = -INFINITY;
   }
 }
 
@@ -161,15 +244,17 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   int* pos_ring = reinterpret_cast<int*>(smem + SM::kPos);  // [4][128]
-  RowPar* par = reinterpret_cast<RowPar*>(smem + SM::kPar);
+  float* fac = reinterpret_cast<float*>(smem + SM::kFac);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + SM::kBar);
   uint64_t *k_empty = k_full + 2, *v_full = k_full + 4, *v_empty = k_full + 6;
-  uint64_t *s_full = k_full + 8, *p_full = k_full + 10, *o_full = k_full + 12, *drain = k_full + 14;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 15);
+  uint64_t *s_full = k_full + 8, *o_full = k_full + 10, *drain = k_full + 12;
+  uint64_t* p_full = k_full + 13;  // [row tile][half of the slots]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 17);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_range = reinterpret_cast<int*>(tmem_slot + 2);  // lo, hi; per row tile lo_all, hi_all
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler too
   const int split = blockIdx.x % a.nsplit;
   const int tile = blockIdx.x / a.nsplit % a.ntile;
   const int bh = blockIdx.x / a.nsplit / a.ntile;
@@ -185,6 +270,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
       tc::mbar_init(v_empty + i, 1);
       tc::mbar_init(s_full + i, 1);
       tc::mbar_init(p_full + i, 4);
+      tc::mbar_init(p_full + 2 + i, 4);
       tc::mbar_init(o_full + i, 1);
     }
     tc::mbar_init(drain, 1);
@@ -196,17 +282,36 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
     tc::fence_mbar_init();
   }
   if (warp == 12) tc::tmem_alloc(tmem_slot, 512);
-  stage_queries<DH>(a, b, hkv, m0, smem, par);
+  TcRow row{0.f, 0.f, 0, 0, 0};
+  const int m = m0 + tid;  // a softmax thread's row
+  if (tid < 2 * kTile && m < a.M) {
+    const long tok = (long)b * a.T + m / a.G;
+    if (a.slope != nullptr) row.slope2 = a.slope[hkv * a.G + m % a.G] * kLog2e;
+    row.hi = INT32_MAX;
+    if (a.span != nullptr) {
+      row.lo = a.span[2 * tok];
+      row.hi = a.span[2 * tok + 1];
+    }
+    if (a.qpos != nullptr) row.qpos = a.qpos[tok];
+  }
+  stage_queries<DH>(a, b, hkv, m0, smem, fac);
   tc::fence_proxy_async_smem();
   __syncthreads();
-  if (tid < 2 * kTile && m0 + tid < a.M) {
+  if (tid < 2 * kTile && m < a.M) {
     // slots some row sees, and slots every row of a row tile sees
-    if (par[tid].lo < par[tid].hi) {
-      atomicMin(&s_range[0], par[tid].lo);
-      atomicMax(&s_range[1], par[tid].hi);
+    const int g = tid / kTile;
+    const bool any = row.lo < row.hi;
+    const uint32_t act = __activemask();
+    const int lo = __reduce_min_sync(act, any ? row.lo : INT32_MAX);
+    const int hi = __reduce_max_sync(act, any ? row.hi : INT32_MIN);
+    const int lo_all = __reduce_max_sync(act, row.lo), hi_all = __reduce_min_sync(act, row.hi);
+    if (lane == 0) {  // a warp's first row is there if any is
+      atomicMin(&s_range[0], lo);
+      atomicMax(&s_range[1], hi);
+      atomicMax(&s_range[2 + 2 * g], lo_all);
+      atomicMin(&s_range[3 + 2 * g], hi_all);
     }
-    atomicMax(&s_range[2 + 2 * (tid / kTile)], par[tid].lo);
-    atomicMin(&s_range[3 + 2 * (tid / kTile)], par[tid].hi);
+    row.f = fac[tid];
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -228,47 +333,41 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
   const int nt = ceil_div(n_hi - n_lo, kTile);
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    const int g = warp >> 2, r = tid;
+    const int g = warp >> 2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + g * 128;
     const uint32_t o_col = tmem + lane_base + 256 + g * 128;
-    const RowPar rp = par[r];
     const int all_lo = by_pos ? INT32_MAX : s_range[2 + 2 * g];
     const int all_hi = min(len, s_range[3 + 2 * g]);
-    const float f2 = GEN ? 1.f : rp.f * kLog2e;
+    const float f2 = GEN ? 1.f : row.f * kLog2e;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     if (g == 0 || two) {
       for (int j = 0; j < nt; ++j) {
         const int n0 = n_lo + j * kTile;
+        const bool masked = n0 < all_lo || n0 + kTile > all_hi;
+        const int* ps = by_pos ? pos_ring + (j & 3) * kTile : nullptr;
         if (!tc::mbar_wait(s_full + g, j & 1, a.status, abort_flag)) { ok = false; break; }
         tc::fence_after_sync();
-        float s[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          tc::tmem_ld32_nowait(s_col + 32 * q, reinterpret_cast<uint32_t*>(s) + 32 * q);
-        tc::tmem_wait_ld();
-        if constexpr (GEN) {
-          const int* ps = pos_ring + (j & 3) * kTile;
-#pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const int pos = by_pos ? ps[c] : n0 + c;
-            s[c] = kv4_score<false>(a, s[c], rp.f, rp.slope, rp.qpos, pos) * kLog2e;
-            if (n0 + c >= len || pos < rp.lo || pos >= rp.hi) s[c] = -INFINITY;
+        // The tile's maximum, 64 slots at a time; scores that are more than
+        // raw products go back to TMEM for the second pass.
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float s[64];
+          tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
+          tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+          tc::tmem_wait_ld();
+          if (GEN || masked) {
+            tc_scores<GEN>(a, s, row, n0 + 64 * h, len, masked, by_pos ? ps + 64 * h : nullptr);
+            tc::tmem_st32(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
+            tc::tmem_st32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
           }
-        } else if (n0 < all_lo || n0 + kTile > all_hi) {
-          // columns [lo, hi) of this tile are seen
-          const int lo = min(max((long)rp.lo - n0, 0L), 128L);
-          const int hi = (int)min(max((long)min(rp.hi, len) - n0, 0L), 128L);
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c < lo || c >= hi) s[c] = -INFINITY;
+          for (int c = 0; c < 64; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
         }
-        float mx = s[0];
-#pragma unroll
-        for (int c = 1; c < 128; ++c) mx = fmaxf(mx, s[c]);
-        const float m_tile = mx * f2;
+        if (GEN || masked) tc::tmem_wait_st();
+        const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f2;
         const bool grow = m_tile > m_used + kGrow;
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? m_tile : m_used;
@@ -287,67 +386,106 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
           l *= corr;
           m_used = m_new;
         }
+        // P over the scores: the first half lies on scores already read
         const float base = m_used == -INFINITY ? 0.f : m_used - kTcShift;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float s[64];
+          tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
+          tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+          tc::tmem_wait_ld();
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const float p0 = exp2_approx(fmaf(s[64 * q + 2 * c], f2, -base));
-            const float p1 = exp2_approx(fmaf(s[64 * q + 2 * c + 1], f2, -base));
-            sum[2 * (c & 1)] += p0;
-            sum[2 * (c & 1) + 1] += p1;
+            const float p0 = exp2_approx(fmaf(s[2 * c], f2, -base));
+            const float p1 = exp2_approx(fmaf(s[2 * c + 1], f2, -base));
+            s4[2 * (c & 1)] += p0;
+            s4[2 * (c & 1) + 1] += p1;
             pk[c] = h2_bits(__floats2half2_rn(p0, p1));
           }
-          tc::tmem_st32(s_col + 32 * q, pk);
+          tc::tmem_st32(s_col + 32 * h, pk);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(p_full + 2 * g + h);  // half of P V may start
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + g);
+        l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       }
-      // the finished row
-      const int m = m0 + r;
       if (ok && nt > 0) {
         ok = tc::mbar_wait(o_full + g, 0, a.status, abort_flag);
         tc::fence_after_sync();
       }
+      // The finished rows: through shared memory (Q's, no longer read), 256
+      // bytes a row at a time, so that a warp stores whole rows.
       if (ok) {
+        const bool part = a.nsplit > 1;
         const float mx = m_used == -INFINITY ? -INFINITY : m_used - kTcShift + kPShift;
-#pragma unroll 1
-        for (int q = 0; q < DH / 32; ++q) {
-          uint32_t o[32];
-          if (nt > 0) {
-            tc::tmem_ld32_nowait(o_col + 32 * q, o);  // warp-collective
-            tc::tmem_wait_ld();
+        const long orow = ((long)b * a.T + m / a.G) * a.Hq + hkv * a.G + m % a.G;
+        const long prow = ((long)bh * a.M + m) * a.nsplit + split;
+        if (m < a.M) {
+          if (part) {
+            a.pml[2 * prow] = mx;
+            a.pml[2 * prow + 1] = l;
+          } else if (a.lse != nullptr) {
+            a.lse[orow] = row_lse(mx, l);
           }
-          if (m < a.M) {
+        }
+        const float inv = part ? 1.f : l == 0.f ? 0.f : a.vmul / l;
+        uint8_t* buf = smem + warp * 8192;  // 32 rows
+        const int per = part ? 64 : DH;     // elements a row at a time
+        const int lanes = part ? 16 : DH / 8;
+#pragma unroll 1
+        for (int d0 = 0; d0 < DH; d0 += per) {
+#pragma unroll 1
+          for (int q = 0; q < per / 32; ++q) {
+            uint32_t o[32];
+            if (nt > 0) {
+              tc::tmem_ld32_nowait(o_col + d0 + 32 * q, o);
+              tc::tmem_wait_ld();
+            }
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              float4 v = make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]),
-                                     __uint_as_float(o[c + 2]), __uint_as_float(o[c + 3]));
-              if (l == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-              const int d = 32 * q + c;
-              if (a.nsplit > 1) {
-                const size_t at = ((size_t)bh * a.M + m) * a.nsplit + split;
-                *reinterpret_cast<float4*>(a.po + at * DH + d) = v;
-                if (d == 0) {
-                  a.pml[2 * at] = mx;
-                  a.pml[2 * at + 1] = l;
+            for (int c = 0; c < 32; ++c)  // nothing seen: 0, whatever TMEM holds
+              o[c] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
+            if (part) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(buf + lane * 256 + (((8 * q + c) ^ (lane & 15)) << 4)) =
+                    make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __nv_bfloat162 v =
+                      __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * e]),
+                                            __uint_as_float(o[8 * c + 2 * e + 1]));
+                  w[e] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-              } else {
-                kv4_finish<false>(a, b, hkv, m, DH, d, v, mx, l);
+                *reinterpret_cast<uint4*>(buf + lane * 256 + (((4 * q + c) ^ (lane & 15)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
           }
+          __syncwarp();
+          for (int i = 0; i < lanes; ++i) {
+            const int rr = i * (32 / lanes) + lane / lanes, c = lane % lanes;
+            const long at = __shfl_sync(0xffffffffu, part ? prow : orow, rr);
+            const bool in = __shfl_sync(0xffffffffu, m < a.M, rr);
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(buf + rr * 256 + ((c ^ (rr & 15)) << 4));
+            if (in) {
+              if (part) reinterpret_cast<uint4*>(a.po + at * DH + d0)[c] = v;
+              else reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + at * DH)[c] = v;
+            }
+          }
+          __syncwarp();
         }
       }
     }
     tc::fence_before_sync();
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int p = tid - 256, last = a.Ncache - 1;
     const uint8_t* kc = a.kcode + (long)bh * a.Ncache * (DH / 2);
     const uint8_t* ks = a.kscale + (long)bh * a.Ncache * (DH / 16);
@@ -379,11 +517,9 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
       if (j + 1 < nt) load_row<DH>(vc, vs, next, rv);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 12 && lane == 0 && nt > 0) {
+    if (warp == 12 && nt > 0) {
       constexpr uint32_t kIdQK = idesc_f16(128, false), kIdPV = idesc_f16(DH, true);
       const uint32_t qs = tc::smem_u32(smem), kb = qs + SM::kK, vb = qs + SM::kV;
-      bool ok = true;
       auto qk = [&](int g, int j) {
         const uint32_t q = qs + g * SM::kOp, k = kb + (j & 1) * SM::kOp;
 #pragma unroll
@@ -394,43 +530,50 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
         }
         tc::mma_commit(s_full + g);
       };
-      auto pv = [&](int g, int j) {
+      auto pv = [&](int g, int j, int half) {
         const uint32_t v = vb + (j & 1) * SM::kOp;
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
+        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
           mma_ts(tmem + 256 + g * 128, tmem + g * 128 + kk * 8,
                  tc::desc_sw128(v + kk * 2048u, 16384, 1024), kIdPV, j > 0 || kk > 0);
       };
       const int ng = two ? 2 : 1;
-      ok = tc::mbar_wait(k_full, 0, a.status, abort_flag);
+      bool ok = tc::mbar_wait(k_full, 0, a.status, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
-      if (ok) {
+      if (ok && elect_one()) {
         for (int g = 0; g < ng; ++g) qk(g, 0);
         tc::mma_commit(k_empty);
       }
       for (int j = 0; ok && j < nt; ++j) {
-        const uint32_t ph = (j >> 1) & 1;
-        if (!tc::mbar_wait(v_full + (j & 1), ph, a.status, abort_flag)) { ok = false; break; }
-        for (int g = 0; g < ng; ++g) {
-          if (!tc::mbar_wait(p_full + g, j & 1, a.status, abort_flag)) { ok = false; break; }
+        const int jn = j + 1, stn = jn & 1;
+        ok = tc::mbar_wait(v_full + (j & 1), (j >> 1) & 1, a.status, abort_flag);
+        for (int g = 0; ok && g < ng; ++g) {
+          ok = tc::mbar_wait(p_full + 2 * g, j & 1, a.status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
           tc::fence_after_sync();
-          pv(g, j);
-          if (g == ng - 1) tc::mma_commit(v_empty + (j & 1));
-          if (j + 1 < nt) {
-            if (g == 0) {
-              if (!tc::mbar_wait(k_full + ((j + 1) & 1), ((j + 1) >> 1) & 1, a.status,
-                                 abort_flag)) { ok = false; break; }
-              tc::fence_after_sync();
+          if (ok && elect_one()) pv(g, j, 0);
+          __syncwarp();
+          if (ok) ok = tc::mbar_wait(p_full + 2 * g + 1, j & 1, a.status, abort_flag);
+          if (ok && g == 0 && jn < nt)
+            ok = tc::mbar_wait(k_full + stn, (jn >> 1) & 1, a.status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          tc::fence_after_sync();
+          if (ok && elect_one()) {
+            pv(g, j, 1);
+            if (g == ng - 1) tc::mma_commit(v_empty + (j & 1));
+            if (jn < nt) {
+              qk(g, jn);
+              if (g == ng - 1) tc::mma_commit(k_empty + stn);
+            } else {
+              tc::mma_commit(o_full + g);
             }
-            qk(g, j + 1);
-            if (g == ng - 1) tc::mma_commit(k_empty + ((j + 1) & 1));
-          } else {
-            tc::mma_commit(o_full + g);
           }
+          __syncwarp();
         }
       }
-      if (!ok) {  // wait for the MMAs already issued before TMEM is freed
-        tc::mma_commit(drain);
+      if (!__all_sync(0xffffffffu, ok)) {  // wait for the MMAs issued before TMEM is freed
+        if (elect_one()) tc::mma_commit(drain);
         const uint64_t t0 = tc::globaltimer();
         while (!tc::mbar_try_wait(drain, 0) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {
         }
@@ -450,13 +593,8 @@ cudaError_t launch_tc(const Kv4AttnArgs& a, cudaStream_t s) {
   auto kern = k_kv4_attn_tc<DH, GEN>;
   static bool attr_set = false;
   if (!attr_set) {
-    // the register split waits for ever if the CTA is launched with fewer
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)TcSmem<DH>::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)TcSmem<DH>::kBytes);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
