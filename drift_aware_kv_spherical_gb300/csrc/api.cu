@@ -552,7 +552,7 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
   PS_REQUIRE((q->slope == nullptr) || (q->qpos != nullptr));
   *none = c->B == 0 || q->T == 0;
   if (*none) return PS_OK;
-  PS_REQUIRE((long)c->B * q->T * q->Hq <= INT32_MAX / 64);
+  PS_REQUIRE((long)c->B * q->T * q->Hq <= INT32_MAX / 64 && q->Hq / c->Hkv <= 4096);
   PS_REQUIRE(ld_ok(q->q_ld, (long)q->Hq * c->dh, q->dtype));
   PS_PTR(q->Q);
   *a = Kv4AttnArgs{};
@@ -560,6 +560,7 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
   a->Q = q->Q; a->dtype = q->dtype;
   a->B = c->B; a->T = q->T; a->Hq = q->Hq; a->Hkv = c->Hkv;
   a->G = q->Hq / c->Hkv; a->M = q->T * a->G;
+  a->g_recip = ((1ull << 40) + a->G - 1) / a->G;
   a->Ncache = c->Ncache; a->dh = c->dh; a->q_ld = (long)q->q_ld;
   a->len = q->len; a->span = q->span; a->kpos = q->kpos; a->qpos = q->qpos; a->slope = q->slope;
   a->scale = q->scale * c->kmul; a->vmul = c->vmul;

@@ -30,15 +30,16 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* r) {
       : "r"(w));
 }
 
-// (s, s) in f16 of one E4M3 scale byte.  A NaN byte, which the store never
-// writes but a slot that was never stored may hold, becomes 448: such slots
-// are masked, and a finite value keeps 0 * v at 0.
-__device__ __forceinline__ __half2 e4m3_pair(uint32_t byte) {
-  const uint16_t two = static_cast<uint16_t>(byte * 0x0101u);
+// Two E4M3 scale bytes (low byte first) in f16.  A NaN byte, which the store
+// never writes but a slot that was never stored may hold, becomes 448: such
+// slots are masked, and a finite value keeps 0 * v at 0.
+__device__ __forceinline__ __half2 e4m3x2_f16(uint32_t bytes) {
   uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(bytes)));
   return __hmin2(*reinterpret_cast<__half2*>(&h), __float2half2_rn(448.f));
 }
+// (s, s) of one scale byte.
+__device__ __forceinline__ __half2 e4m3_pair(uint32_t byte) { return e4m3x2_f16(byte * 0x0101u); }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ __half2 h2_of(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
@@ -52,6 +53,37 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations an instruction: the same rate on the FMA pipe, half the
+// issue slots.
+__device__ __forceinline__ uint64_t f2_pack(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -87,9 +119,8 @@ __device__ __forceinline__ int kv4_len(const Kv4AttnArgs& a, int b) {
 // negative scale turns the query's sign instead, so the factor is positive
 // and row maxima may be taken of raw products.
 __device__ __forceinline__ void row_scale(float mx, float scale, float* up, float* f) {
-  int ex = 0;
-  if (mx > 0.f && mx < INFINITY) ex = 14 - ilogbf(mx);
-  ex = min(max(ex, -110), 110);
+  int ex = 0;  // subnormal maxima count as 2^-127: the scale ends at 2^110 all the same
+  if (mx > 0.f && mx < INFINITY) ex = min(141 - (int)(__float_as_uint(mx) >> 23), 110);
   *up = __uint_as_float((uint32_t)(127 + ex) << 23) * (scale < 0.f ? -1.f : 1.f);
   *f = fmaxf(fabsf(scale) * __uint_as_float((uint32_t)(127 - ex) << 23), FLT_MIN);
 }
@@ -119,11 +150,17 @@ __device__ __forceinline__ float row_lse(float mx, float l) {
   return l == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx - kPShift) + log2f(l)) * kLn2;
 }
 
+// Row m of a KV head as (token, query head of the group): m = t G + j.  The
+// quotient by a 2^40 reciprocal, exact while m G < 2^40.
+__device__ __forceinline__ int row_token(const Kv4AttnArgs& a, int m) {
+  return (int)(((uint64_t)(uint32_t)m * a.g_recip) >> 40);
+}
+
 // Four elements of a finished row: O = acc / l.
 template <bool F32>
 __device__ __forceinline__ void kv4_finish(const Kv4AttnArgs& a, int b, int hkv, int m, int dh,
                                            int d, float4 acc, float mx, float l) {
-  const int t = m / a.G, h = hkv * a.G + m % a.G;
+  const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
   const long row = ((long)b * a.T + t) * a.Hq + h;
   const float inv = l == 0.f ? 0.f : a.vmul / l;  // l == 0: nothing seen
   const float x = acc.x * inv, y = acc.y * inv, z = acc.z * inv, w = acc.w * inv;

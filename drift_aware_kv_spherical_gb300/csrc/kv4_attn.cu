@@ -43,7 +43,7 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
     float x[E];
     RowPar p{0.f, 0.f, 0, 0, 0, -INFINITY};
     if (m < a.M) {
-      const int t = m / a.G, h = hkv * a.G + m % a.G;
+      const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
       const long tok = (long)b * a.T + t;
       const long at = tok * a.q_ld + (long)h * DH + lane * E;
       if constexpr (F32) {

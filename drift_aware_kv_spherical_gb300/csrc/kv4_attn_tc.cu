@@ -1,24 +1,28 @@
 // Attention over a 4-bit KV cache for many query rows a KV head, on the
 // tcgen05 tensor cores.
 //
-// A CTA takes 256 rows (two tiles of 128) of one KV head against a share of
-// its slots, 128 slots at a time.  13 warps:
+// A CTA an SM takes items in turn: 256 rows (two tiles of 128) of one KV head
+// against a share of its slots, 128 slots a step.  13 warps:
 //   0-3, 4-7  softmax of row tile 0 / 1: a thread a row.  Reads its 128 scores
 //             from TMEM, keeps the running maximum and sum in registers, writes
-//             P (f16) over the scores, rescales O in TMEM when it must
-//   8-11      the slots: 4-bit codes from global memory (the next tile's are in
-//             registers while this one is converted), exact f16 into shared
-//             memory in the 128-byte-swizzled layout of both operands (K is
-//             K-major for S = Q K^T, V is MN-major for O += P V, which is the
-//             same placement)
+//             P (f16) over the scores, 64 slots at a time, and rescales O in
+//             TMEM when it must.  Also stages the item's queries and stores its
+//             rows, each row tile for itself, so that one finishes and begins
+//             an item while the other still has the tensor cores
+//   8-11      the slots: 4-bit codes from global memory (the next step's are in
+//             registers while this one is converted, across items too), exact
+//             f16 into shared memory in the 128-byte-swizzled layout of both
+//             operands (K is K-major for S = Q K^T, V is MN-major for O += P V,
+//             which is the same placement)
 //   12        issues the MMAs: S into 128 TMEM columns a row tile, O into 128
 //             more; P is the TMEM-resident A operand of P V
-// Order of the MMAs, per 128 slots j:  P0 V(j), S0(j+1), P1 V(j), S1(j+1): the
-// softmax of one row tile runs under the two products of the other.  The
-// commit that announces S(j+1) also says that P V(j) is done, so O may be
-// rescaled then without another barrier.  O is rescaled only when a row's
-// maximum has grown by 2^kGrow or more since the last time: until then P just
-// carries a factor up to that.
+// Order of the MMAs, per step j:  P0 V(j), S0(j+1), P1 V(j), S1(j+1): the
+// softmax of one row tile runs under the two products of the other, and P V of
+// its first 64 slots under its second 64 exponentials.  The commit that
+// announces S(j+1) also says that P V(j) is done, so O may be rescaled then
+// without another barrier.  O is rescaled only when a row's maximum has grown
+// by 2^kGrow or more since the last time: until then P just carries a factor up
+// to that.
 // Every mbarrier wait is bounded (tc::mbar_wait); after a timeout the CTA waits
 // for the MMAs it issued, frees TMEM and returns with the status word set.
 #include "kv4.cuh"
@@ -36,9 +40,8 @@ template <int DH>
 struct TcSmem {
   static constexpr uint32_t kOp = (DH / 64) * 16384u;  // 128 rows of DH f16
   static constexpr uint32_t kK = 2 * kOp,  // Q at 0
-                             kV = 4 * kOp, kPos = 6 * kOp;
-  static constexpr uint32_t kFac = kPos + 4 * kTile * 4;
-  static constexpr uint32_t kBar = kFac + 256 * 4;
+                            kV = 4 * kOp, kPos = 6 * kOp;
+  static constexpr uint32_t kBar = kPos + 4 * kTile * 4;
   static constexpr size_t kBytes = 1024 + kBar + 256;
 };
 
@@ -78,6 +81,88 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) {
   return tc::idesc_bf16(128, N, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
+// ---------------------------------------------------------------- work items
+// An item: 256 rows of one KV head against one share of its slots.  A CTA takes
+// every gridDim.x-th; the mixed-radix step between two of its items saves the
+// divisions.
+struct TcWork {
+  int item, split, tile, hkv, b;
+  int n_lo, nt;  // first slot, steps
+  bool two;      // the second row tile holds rows
+};
+struct TcStride {
+  int split, tile, hkv, b;
+};
+__device__ __forceinline__ TcStride tc_digits(const Kv4AttnArgs& a, int n) {
+  TcStride d;
+  d.split = n % a.nsplit;
+  n /= a.nsplit;
+  d.tile = n % a.ntile;
+  n /= a.ntile;
+  d.hkv = n % a.Hkv;
+  d.b = n / a.Hkv;
+  return d;
+}
+
+// The slots of w, for a whole warp: those within the rows' spans.
+__device__ __forceinline__ void tc_slots(const Kv4AttnArgs& a, TcWork& w, int items) {
+  w.n_lo = w.nt = 0;
+  w.two = false;
+  if (w.item >= items) return;
+  const int m0 = w.tile * 2 * kTile;
+  w.two = a.M - m0 > kTile;
+  int n_lo = 0;
+  int n_hi = min(max(a.len != nullptr ? __ldg(a.len + w.b) : a.Ncache, 0), a.Ncache);
+  if (a.span != nullptr && a.kpos == nullptr) {
+    const int t0 = row_token(a, m0), t1 = row_token(a, min(m0 + 2 * kTile, a.M) - 1);
+    int lo = INT32_MAX, hi = INT32_MIN;
+    for (int t = t0 + (threadIdx.x & 31); t <= t1; t += 32) {
+      const int2 x = __ldg(reinterpret_cast<const int2*>(a.span) + (long)w.b * a.T + t);
+      if (x.x < x.y) {
+        lo = min(lo, x.x);
+        hi = max(hi, x.y);
+      }
+    }
+    n_lo = max(0, __reduce_min_sync(0xffffffffu, lo));
+    n_hi = min(n_hi, __reduce_max_sync(0xffffffffu, hi));
+  }
+  if (n_lo >= n_hi) return;
+  int n = n_hi - n_lo;
+  w.n_lo = n_lo;
+  if (a.nsplit > 1) {
+    const int share = ceil_div(ceil_div(n, kTile), a.nsplit) * kTile;
+    const int from = (int)min((long)n, (long)w.split * share);
+    w.n_lo += from;
+    n = min(n - from, share);
+  }
+  w.nt = (n + kTile - 1) / kTile;
+}
+__device__ __forceinline__ TcWork tc_first(const Kv4AttnArgs& a, int items) {
+  const TcStride d = tc_digits(a, blockIdx.x);
+  TcWork w{(int)blockIdx.x, d.split, d.tile, d.hkv, d.b, 0, 0, false};
+  tc_slots(a, w, items);
+  return w;
+}
+__device__ __forceinline__ TcWork tc_next(const Kv4AttnArgs& a, TcWork w, const TcStride& d,
+                                          int items) {
+  w.item += gridDim.x;
+  w.split += d.split;
+  w.tile += d.tile;
+  w.hkv += d.hkv;
+  w.b += d.b;
+  if (w.split >= a.nsplit) { w.split -= a.nsplit; ++w.tile; }
+  if (w.tile >= a.ntile) { w.tile -= a.ntile; ++w.hkv; }
+  if (w.hkv >= a.Hkv) { w.hkv -= a.Hkv; ++w.b; }
+  tc_slots(a, w, items);
+  return w;
+}
+
+// ---------------------------------------------------------------- slots
+__device__ __forceinline__ void l2_prefetch(const void* p, int bytes) {
+  for (int o = 0; o < bytes; o += 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + o));
+}
+
 // Codes and scales of one slot's row (K or V).
 template <int DH>
 struct RawRow {
@@ -98,114 +183,151 @@ __device__ __forceinline__ void load_row(const uint8_t* codes, const uint8_t* sc
   }
 }
 // The row as f16 into row r of an operand: 16-byte chunks, eight elements each,
-// two to a scale.
+// two to a scale, two scales to a conversion.
 template <int DH>
 __device__ __forceinline__ void put_row(uint8_t* op, int r, const RawRow<DH>& v) {
 #pragma unroll
-  for (int c = 0; c < DH / 8; ++c) {
-    const uint4& q = v.c[c / 4];
-    const uint32_t w = c % 4 == 0 ? q.x : c % 4 == 1 ? q.y : c % 4 == 2 ? q.z : q.w;
-    const __half2 s = e4m3_pair(((c < 8 ? v.s.x : v.s.y) >> (8 * ((c / 2) & 3))) & 0xffu);
-    uint32_t h[4];
-    e2m1x8_f16(w, h);
-    uint4 o;
-    o.x = h2_bits(__hmul2(h2_of(h[0]), s));
-    o.y = h2_bits(__hmul2(h2_of(h[1]), s));
-    o.z = h2_bits(__hmul2(h2_of(h[2]), s));
-    o.w = h2_bits(__hmul2(h2_of(h[3]), s));
-    *reinterpret_cast<uint4*>(op + sw128(r, c)) = o;
+  for (int p = 0; p < DH / 32; ++p) {
+    const uint32_t two = ((p < 2 ? v.s.x : v.s.y) >> (16 * (p & 1))) & 0xffffu;
+    const uint32_t sc = h2_bits(e4m3x2_f16(two));
+    const uint32_t w[4] = {v.c[p].x, v.c[p].y, v.c[p].z, v.c[p].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 s = h2_of(__byte_perm(sc, sc, i < 2 ? 0x1010u : 0x3232u));
+      uint32_t h[4];
+      e2m1x8_f16(w[i], h);
+      uint4 o;
+      o.x = h2_bits(__hmul2(h2_of(h[0]), s));
+      o.y = h2_bits(__hmul2(h2_of(h[1]), s));
+      o.z = h2_bits(__hmul2(h2_of(h[2]), s));
+      o.w = h2_bits(__hmul2(h2_of(h[3]), s));
+      *reinterpret_cast<uint4*>(op + sw128(r, 4 * p + i)) = o;
+    }
   }
 }
 
-// 256 query rows as f16 operands and their score factors, DH / 8 lanes a row;
-// all of a thread's rows are loaded before the first is used.
+// ---------------------------------------------------------------- queries
+// A softmax thread stages its own row as row r of the f16 operand at qs (zero
+// where src is null) and returns its score factor.  The lanes of a load lie in
+// different rows, but no lane needs another's maximum: staged by DH / 8 lanes a
+// row the same work took three times the instructions.
 template <int DH>
-__device__ __forceinline__ void stage_queries(const Kv4AttnArgs& a, int b, int hkv, int m0,
-                                              uint8_t* qs, float* fac) {
-  constexpr int LN = DH / 8;                          // lanes a row
-  constexpr int RP = kTcThreads / LN;                 // rows a pass
-  constexpr int NP = (2 * kTile + RP - 1) / RP;       // passes
-  const int sub = threadIdx.x % LN;
-  uint4 raw[NP];
+__device__ __forceinline__ float stage_q(const __nv_bfloat16* src, float scale, uint8_t* qs,
+                                         int r) {
+  uint4 v[DH / 8];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = threadIdx.x / LN + i * RP, m = m0 + r;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < 2 * kTile && m < a.M) {
-      const int t = m / a.G, h = hkv * a.G + m % a.G;
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Q) +
-                                                    ((long)b * a.T + t) * a.q_ld + (long)h * DH +
-                                                    sub * 8));
-    }
+  for (int c = 0; c < DH / 8; ++c)
+    v[c] = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + c)
+                          : make_uint4(0u, 0u, 0u, 0u);
+  __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);  // NaN elements do not count
+#pragma unroll
+  for (int c = 0; c < DH / 8; ++c) {
+    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
   }
+  float up, f;
+  row_scale(fmaxf(__low2float(m2), __high2float(m2)), scale, &up, &f);
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = threadIdx.x / LN + i * RP;
+  for (int c = 0; c < DH / 8; ++c) {
     float x[8];
-    unpack16(raw[i], x, __nv_bfloat16{});
-    float mx = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
-#pragma unroll
-    for (int o = LN / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float up, f;
-    row_scale(mx, a.scale, &up, &f);
-    if (r >= 2 * kTile) continue;
-    if (sub == 0) fac[r] = f;
+    unpack16(v[c], x, __nv_bfloat16{});
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = h2_bits(__floats2half2_rn(x[2 * e] * up, x[2 * e + 1] * up));
-    *reinterpret_cast<uint4*>(qs + (r / kTile) * TcSmem<DH>::kOp + sw128(r % kTile, sub)) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(qs + sw128(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  return f;
 }
 
+// ---------------------------------------------------------------- scores
 // The constants of a softmax thread's row.
 struct TcRow {
   float f;                // score factor of a raw product
   float slope2;           // distance bias in log2 units
-  int lo, hi, qpos;
+  int lo, hi, qpos;       // positions seen; the row's own
 };
+// Row m, token t of its sequence, query head h; nothing past the last row.
+__device__ __forceinline__ TcRow tc_row(const Kv4AttnArgs& a, bool in, int b, int t, int h) {
+  TcRow row{0.f, 0.f, 0, 0, 0};
+  if (in) {
+    const long tok = (long)b * a.T + t;
+    if (a.slope != nullptr) row.slope2 = a.slope[h] * kLog2e;
+    row.hi = INT32_MAX;
+    if (a.span != nullptr) {
+      row.lo = a.span[2 * tok];
+      row.hi = a.span[2 * tok + 1];
+    }
+    if (a.qpos != nullptr) row.qpos = a.qpos[tok];
+  }
+  return row;
+}
+
+// What the rows of a softmax warp see of 64 slots.  A row that sees nothing at
+// all has no say (its sum is dropped at the end).  Taken once an item, so that
+// a step compares two numbers and does not vote.
+enum TcSeen { kNone, kSome, kAll };
+struct TcRange {
+  int any_lo, any_hi, all_lo, all_hi;  // slots that some, that every row sees
+};
+__device__ __forceinline__ TcRange tc_range(const TcRow& row, int len) {
+  const bool live = row.lo < row.hi;
+  const int hi = min(row.hi, len);
+  TcRange r;
+  r.any_lo = __reduce_min_sync(0xffffffffu, live ? row.lo : INT32_MAX);
+  r.any_hi = __reduce_max_sync(0xffffffffu, live ? hi : INT32_MIN);
+  r.all_lo = __reduce_max_sync(0xffffffffu, live ? row.lo : INT32_MIN);
+  r.all_hi = __reduce_min_sync(0xffffffffu, live ? hi : INT32_MAX) - 64;  // of the first of 64
+  return r;
+}
+__device__ __forceinline__ TcSeen tc_seen(const TcRange& r, int n0) {
+  if (n0 >= r.any_hi || n0 <= r.any_lo - 64) return kNone;
+  return n0 >= r.all_lo && n0 <= r.all_hi ? kAll : kSome;
+}
 
 // s[0..63]: raw products of 64 slots from n0 on -> log2-unit scores (GEN), and
 // -inf where the row does not see the slot.  pos: explicit positions, or null.
 template <bool GEN>
 __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, const TcRow& row,
-                                          int n0, int len, bool masked, const int* pos) {
+                                          int n0, int len, TcSeen seen, const int* pos) {
   if constexpr (GEN) {
+    const float f2 = row.f * kLog2e;
+    const uint64_t ff = f2_pack(f2, f2);
     if (a.cap > 0.f) {
-      const float fy = row.f * a.inv_cap, cap2 = a.cap * kLog2e;
-      float top = 0.f;
+      float t4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 64; ++c) {
-        s[c] *= fy;
-        top = fmaxf(top, fabsf(s[c]));
-      }
-      if (__all_sync(0xffffffffu, top <= 0.4f)) {
-        // tanh's series to y^11: the next term is under 2^-23 of y here
+      for (int c = 0; c < 64; c += 2)
+        t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
+      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      // y = score / cap = u kc, u the score in log2 units
+      const float kc = a.inv_cap * kLn2, k2 = kc * kc;
+      if (__all_sync(0xffffffffu, top * f2 * kc <= 0.2f)) {
+        // tanh y = y (1 - y^2/3 + 2 y^4/15 - 17 y^6/315 + ...): the next term
+        // is under 2^-24 of y here
+        const float c1 = k2 * (-1.f / 3.f), c2 = k2 * k2 * (2.f / 15.f),
+                    c3 = k2 * k2 * k2 * (-17.f / 315.f);
+        const uint64_t cc1 = f2_pack(c1, c1), cc2 = f2_pack(c2, c2), cc3 = f2_pack(c3, c3);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const float y = s[c], z = y * y;
-          float q = fmaf(z, -1382.f / 155925.f, 62.f / 2835.f);
-          q = fmaf(z, q, -17.f / 315.f);
-          q = fmaf(z, q, 2.f / 15.f);
-          q = fmaf(z, q, -1.f / 3.f);
-          q = z * q;
-          s[c] = cap2 * fmaf(y, q, y);
+        for (int c = 0; c < 64; c += 2) {
+          const uint64_t u = f2_mul(f2_pack(s[c], s[c + 1]), ff), z = f2_mul(u, u);
+          const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, cc3, cc2), cc1));
+          f2_unpack(f2_fma(u, q, u), s[c], s[c + 1]);
         }
       } else {
         // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
+        const float fe = 2.f * row.f * a.inv_cap * kLog2e, cap2 = a.cap * kLog2e;
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
-          const float e = exp2_approx(s[c] * (2.f * kLog2e));
+          const float e = exp2_approx(s[c] * fe);
           s[c] = cap2 * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
         }
       }
     } else {
-      const float f2 = row.f * kLog2e;
 #pragma unroll
-      for (int c = 0; c < 64; ++c) s[c] *= f2;
+      for (int c = 0; c < 64; c += 2)
+        f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), ff), s[c], s[c + 1]);
     }
     if (a.slope != nullptr) {
       if (pos == nullptr) {
@@ -218,49 +340,129 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, const 
           s[c] = fmaf(-row.slope2, fabsf((float)(row.qpos - pos[c])), s[c]);
       }
     }
-    if (masked && pos != nullptr) {
+    if (pos != nullptr) {
 #pragma unroll
       for (int c = 0; c < 64; ++c)
         if (n0 + c >= len || pos[c] < row.lo || pos[c] >= row.hi) s[c] = -INFINITY;
       return;
     }
   }
-  if (masked) {  // columns [lo, hi) are seen
+  if (seen != kAll) {  // columns [lo, lo + num) are seen
     const int lo = (int)min(max((long)row.lo - n0, 0L), 64L);
     const int hi = (int)min(max((long)min(row.hi, len) - n0, 0L), 64L);
+    const uint32_t num = (uint32_t)max(hi - lo, 0);
 #pragma unroll
     for (int c = 0; c < 64; ++c)
-      if (c < lo || c >= hi) s[c] = -INFINITY;
+      if ((uint32_t)(c - lo) >= num) s[c] = -INFINITY;
   }
+}
+
+// One step of a softmax warp: its 32 rows' scores of 128 slots at s_col, P over
+// them (64 slots at a time: p_full[0], p_full[1]), the rows' maximum and sum,
+// and O at o_col rescaled where the maximum has outgrown it.  FAST: every row
+// sees every slot (its own copy of the code: tests inside the passes cost a
+// fifth of the step).
+template <int DH, bool GEN, bool FAST>
+__device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, const TcRow& row, float f2,
+                                             int n0, int len, TcSeen seen0, TcSeen seen1,
+                                             const int* ps, uint32_t s_col, uint32_t o_col,
+                                             bool has_o, uint64_t* p_full, float& m_used,
+                                             float& l) {
+  // The maximum, 64 slots at a time; scores that are more than raw products go
+  // back to TMEM for the second pass.
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains: one would wait on itself
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const TcSeen seen = FAST ? kAll : h == 0 ? seen0 : seen1;
+    if (seen == kNone) continue;
+    float s[64];
+    tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
+    tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+    tc::tmem_wait_ld();
+    if (GEN || !FAST) {
+      tc_scores<GEN>(a, s, row, n0 + 64 * h, len, seen, ps != nullptr ? ps + 64 * h : nullptr);
+      tc::tmem_st32(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
+      tc::tmem_st32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+    }
+#pragma unroll
+    for (int c = 0; c < 64; c += 2) m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
+  }
+  if (GEN || !FAST) tc::tmem_wait_st();
+  const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f2;
+  const bool grow = m_tile > m_used + kGrow;
+  if (__any_sync(0xffffffffu, grow)) {
+    const float m_new = grow ? m_tile : m_used;
+    const float corr = grow ? exp2_approx(m_used - m_new) : 1.f;
+    if (has_o) {
+#pragma unroll 1
+      for (int q = 0; q < DH / 32; ++q) {
+        uint32_t o[32];
+        tc::tmem_ld32_nowait(o_col + 32 * q, o);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * corr);
+        tc::tmem_st32(o_col + 32 * q, o);
+      }
+    }
+    l *= corr;
+    m_used = m_new;
+  }
+  // P over the scores: the first half lies on scores already read
+  const float base = m_used == -INFINITY ? 0.f : m_used - kTcShift;
+  const uint64_t ff = f2_pack(f2, f2), nb = f2_pack(-base, -base);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+    if (!FAST && (h == 0 ? seen0 : seen1) == kNone) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) pk[c] = 0u;
+    } else {
+      float s[64];
+      tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
+      tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(s[2 * c], s[2 * c + 1]), ff, nb), x0, x1);
+        const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+        sum[c & 1] = f2_add(sum[c & 1], f2_pack(p0, p1));
+        pk[c] = h2_bits(__floats2half2_rn(p0, p1));
+      }
+    }
+    tc::tmem_st32(s_col + 32 * h, pk);
+    tc::tmem_wait_st();
+    tc::fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(p_full + h);  // half of P V may start
+  }
+  float s0, s1;
+  f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+  l += s0 + s1;
 }
 
 // GEN: capped scores, a distance bias or explicit positions.
 template <int DH, bool GEN>
 __global__ void __launch_bounds__(kTcThreads, 1)
-k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
+k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
   using SM = TcSmem<DH>;
   pdl_prologue();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   int* pos_ring = reinterpret_cast<int*>(smem + SM::kPos);  // [4][128]
-  float* fac = reinterpret_cast<float*>(smem + SM::kFac);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + SM::kBar);
   uint64_t *k_empty = k_full + 2, *v_full = k_full + 4, *v_empty = k_full + 6;
-  uint64_t *s_full = k_full + 8, *o_full = k_full + 10, *drain = k_full + 12;
-  uint64_t* p_full = k_full + 13;  // [row tile][half of the slots]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 17);
+  uint64_t *s_full = k_full + 8, *o_full = k_full + 10, *q_full = k_full + 12;
+  uint64_t* p_full = k_full + 14;  // [row tile][half of the slots]
+  uint64_t* drain = k_full + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 19);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_range = reinterpret_cast<int*>(tmem_slot + 2);  // lo, hi; per row tile lo_all, hi_all
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler too
-  const int split = blockIdx.x % a.nsplit;
-  const int tile = blockIdx.x / a.nsplit % a.ntile;
-  const int bh = blockIdx.x / a.nsplit / a.ntile;
-  const int b = bh / a.Hkv, hkv = bh % a.Hkv, m0 = tile * 2 * kTile;
-  const bool two = a.M - m0 > kTile;  // the second row tile holds rows
-  const int len = min(max(a.len != nullptr ? a.len[b] : a.Ncache, 0), a.Ncache);
+  const bool by_pos = GEN && a.kpos != nullptr;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -269,213 +471,149 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
       tc::mbar_init(v_full + i, 4);
       tc::mbar_init(v_empty + i, 1);
       tc::mbar_init(s_full + i, 1);
+      tc::mbar_init(o_full + i, 1);
+      tc::mbar_init(q_full + i, 4);
       tc::mbar_init(p_full + i, 4);
       tc::mbar_init(p_full + 2 + i, 4);
-      tc::mbar_init(o_full + i, 1);
     }
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
-    s_range[0] = INT32_MAX;
-    s_range[1] = INT32_MIN;
-    s_range[2] = s_range[4] = INT32_MIN;
-    s_range[3] = s_range[5] = INT32_MAX;
     tc::fence_mbar_init();
   }
   if (warp == 12) tc::tmem_alloc(tmem_slot, 512);
-  TcRow row{0.f, 0.f, 0, 0, 0};
-  const int m = m0 + tid;  // a softmax thread's row
-  if (tid < 2 * kTile && m < a.M) {
-    const long tok = (long)b * a.T + m / a.G;
-    if (a.slope != nullptr) row.slope2 = a.slope[hkv * a.G + m % a.G] * kLog2e;
-    row.hi = INT32_MAX;
-    if (a.span != nullptr) {
-      row.lo = a.span[2 * tok];
-      row.hi = a.span[2 * tok + 1];
-    }
-    if (a.qpos != nullptr) row.qpos = a.qpos[tok];
-  }
-  stage_queries<DH>(a, b, hkv, m0, smem, fac);
-  tc::fence_proxy_async_smem();
-  __syncthreads();
-  if (tid < 2 * kTile && m < a.M) {
-    // slots some row sees, and slots every row of a row tile sees
-    const int g = tid / kTile;
-    const bool any = row.lo < row.hi;
-    const uint32_t act = __activemask();
-    const int lo = __reduce_min_sync(act, any ? row.lo : INT32_MAX);
-    const int hi = __reduce_max_sync(act, any ? row.hi : INT32_MIN);
-    const int lo_all = __reduce_max_sync(act, row.lo), hi_all = __reduce_min_sync(act, row.hi);
-    if (lane == 0) {  // a warp's first row is there if any is
-      atomicMin(&s_range[0], lo);
-      atomicMax(&s_range[1], hi);
-      atomicMax(&s_range[2 + 2 * g], lo_all);
-      atomicMin(&s_range[3 + 2 * g], hi_all);
-    }
-    row.f = fac[tid];
-  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const bool by_pos = GEN && a.kpos != nullptr;
-  int n_lo = 0, n_hi = len;
-  if (!by_pos) {
-    n_lo = max(0, s_range[0]);
-    n_hi = min(len, s_range[1]);
-  }
-  if (n_lo >= n_hi) {
-    n_lo = n_hi = 0;
-  } else {
-    const int share = ceil_div(ceil_div(n_hi - n_lo, kTile), a.nsplit) * kTile;
-    n_lo = min((long)n_hi, n_lo + (long)split * share);
-    n_hi = min((long)n_hi, (long)n_lo + share);
-  }
-  const int nt = ceil_div(n_hi - n_lo, kTile);
 
   if (warp < 8) {
-    const int g = warp >> 2;
+    // ------------------------------------------------------------ softmax
+    const int g = warp >> 2, r0 = warp * 32;  // row tile; first row of the warp
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + g * 128;
     const uint32_t o_col = tmem + lane_base + 256 + g * 128;
-    const int all_lo = by_pos ? INT32_MAX : s_range[2 + 2 * g];
-    const int all_hi = min(len, s_range[3 + 2 * g]);
-    const float f2 = GEN ? 1.f : row.f * kLog2e;
-    float m_used = -INFINITY, l = 0.f;
+    uint8_t* qs = smem + g * SM::kOp;         // the row tile's operand
+    const int qr = (warp & 3) * 32;           // the warp's first row in it
     bool ok = true;
-    if (g == 0 || two) {
-      for (int j = 0; j < nt; ++j) {
-        const int n0 = n_lo + j * kTile;
-        const bool masked = n0 < all_lo || n0 + kTile > all_hi;
-        const int* ps = by_pos ? pos_ring + (j & 3) * kTile : nullptr;
-        if (!tc::mbar_wait(s_full + g, j & 1, a.status, abort_flag)) { ok = false; break; }
-        tc::fence_after_sync();
-        // The tile's maximum, 64 slots at a time; scores that are more than
-        // raw products go back to TMEM for the second pass.
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          float s[64];
-          tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
-          tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
-          tc::tmem_wait_ld();
-          if (GEN || masked) {
-            tc_scores<GEN>(a, s, row, n0 + 64 * h, len, masked, by_pos ? ps + 64 * h : nullptr);
-            tc::tmem_st32(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
-            tc::tmem_st32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
-          }
-#pragma unroll
-          for (int c = 0; c < 64; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
-        }
-        if (GEN || masked) tc::tmem_wait_st();
-        const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f2;
-        const bool grow = m_tile > m_used + kGrow;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = grow ? m_tile : m_used;
-          const float corr = grow ? exp2_approx(m_used - m_new) : 1.f;
-          if (j > 0) {
-#pragma unroll 1
-            for (int q = 0; q < DH / 32; ++q) {
-              uint32_t o[32];
-              tc::tmem_ld32_nowait(o_col + 32 * q, o);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * corr);
-              tc::tmem_st32(o_col + 32 * q, o);
-            }
-          }
-          l *= corr;
-          m_used = m_new;
-        }
-        // P over the scores: the first half lies on scores already read
-        const float base = m_used == -INFINITY ? 0.f : m_used - kTcShift;
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          float s[64];
-          tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
-          tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
-          tc::tmem_wait_ld();
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float p0 = exp2_approx(fmaf(s[2 * c], f2, -base));
-            const float p1 = exp2_approx(fmaf(s[2 * c + 1], f2, -base));
-            s4[2 * (c & 1)] += p0;
-            s4[2 * (c & 1) + 1] += p1;
-            pk[c] = h2_bits(__floats2half2_rn(p0, p1));
-          }
-          tc::tmem_st32(s_col + 32 * h, pk);
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(p_full + 2 * g + h);  // half of P V may start
-        }
-        l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    int it = 0, rounds = 0;                   // steps and items that this row tile has done
+    int all = 0;                              // steps of both
+    const TcStride stride = tc_digits(a, gridDim.x);
+    TcWork w = tc_first(a, items);
+    while (ok && w.item < items) {
+      const int m = w.tile * 2 * kTile + r0 + lane;
+      const bool in = m < a.M;
+      const int t = row_token(a, m), h = w.hkv * a.G + (m - t * a.G);
+      const bool act = w.nt > 0 && (g == 0 || w.two);
+      TcRow row = tc_row(a, in, w.b, t, h);
+      const bool live = row.lo < row.hi;
+      const int len = min(max(a.len != nullptr ? __ldg(a.len + w.b) : a.Ncache, 0), a.Ncache);
+      const TcRange range = tc_range(row, len);
+      if (act) {
+        row.f = stage_q<DH>(in ? static_cast<const __nv_bfloat16*>(a.Q) +
+                                     ((long)w.b * a.T + t) * a.q_ld + (long)h * DH
+                               : nullptr,
+                            a.scale, qs, qr + lane);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(q_full + g);
       }
-      if (ok && nt > 0) {
-        ok = tc::mbar_wait(o_full + g, 0, a.status, abort_flag);
+      const float f2 = GEN ? 1.f : row.f * kLog2e;
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = 0; act && j < w.nt; ++j, ++it) {
+        const int n0 = w.n_lo + j * kTile;
+        if (!tc::mbar_wait(s_full + g, it & 1, a.status, abort_flag)) { ok = false; break; }
         tc::fence_after_sync();
+        const int* ps = by_pos ? pos_ring + ((all + j) & 3) * kTile : nullptr;
+        const TcSeen seen0 = by_pos ? kSome : tc_seen(range, n0);
+        const TcSeen seen1 = by_pos ? kSome : tc_seen(range, n0 + 64);
+        if (seen0 == kAll && seen1 == kAll)
+          softmax_step<DH, GEN, true>(a, row, f2, n0, len, kAll, kAll, nullptr, s_col, o_col, j > 0,
+                                      p_full + 2 * g, m_used, l);
+        else
+          softmax_step<DH, GEN, false>(a, row, f2, n0, len, seen0, seen1, ps, s_col, o_col, j > 0,
+                                       p_full + 2 * g, m_used, l);
       }
-      // The finished rows: through shared memory (Q's, no longer read), 256
-      // bytes a row at a time, so that a warp stores whole rows.
-      if (ok) {
+      all += w.nt;
+      if (!live) {  // sees nothing anywhere
+        l = 0.f;
+        m_used = -INFINITY;
+      }
+      const TcWork wn = tc_next(a, w, stride, items);
+      if (wn.item < items) {  // the next item's queries into L2 while this one is finished
+        const int mn = wn.tile * 2 * kTile + r0 + lane, tn = row_token(a, mn);
+        if (mn < a.M)
+          l2_prefetch(static_cast<const __nv_bfloat16*>(a.Q) +
+                          ((long)wn.b * a.T + tn) * a.q_ld +
+                          (long)(wn.hkv * a.G + (mn - tn * a.G)) * DH,
+                      DH * 2);
+      }
+      if (act && ok) {
+        ok = tc::mbar_wait(o_full + g, rounds & 1, a.status, abort_flag);
+        tc::fence_after_sync();
+        ++rounds;
+      }
+      // The finished rows: through the row's own place in the query operand
+      // (no longer read), 256 bytes at a time, so that a warp stores whole rows.
+      if (ok && (g == 0 || w.two)) {
         const bool part = a.nsplit > 1;
         const float mx = m_used == -INFINITY ? -INFINITY : m_used - kTcShift + kPShift;
-        const long orow = ((long)b * a.T + m / a.G) * a.Hq + hkv * a.G + m % a.G;
-        const long prow = ((long)bh * a.M + m) * a.nsplit + split;
-        if (m < a.M) {
+        const int orow = (w.b * a.T + t) * a.Hq + h;  // < 2^25
+        const uint32_t prow = ((uint32_t)(w.b * a.Hkv + w.hkv) * a.M + m) * a.nsplit + w.split;
+        if (in) {
           if (part) {
-            a.pml[2 * prow] = mx;
-            a.pml[2 * prow + 1] = l;
+            a.pml[2 * (size_t)prow] = mx;
+            a.pml[2 * (size_t)prow + 1] = l;
           } else if (a.lse != nullptr) {
             a.lse[orow] = row_lse(mx, l);
           }
         }
+        const bool zero = __any_sync(0xffffffffu, l == 0.f);  // rows that saw nothing
         const float inv = part ? 1.f : l == 0.f ? 0.f : a.vmul / l;
-        uint8_t* buf = smem + warp * 8192;  // 32 rows
-        const int per = part ? 64 : DH;     // elements a row at a time
-        const int lanes = part ? 16 : DH / 8;
+        const int per = part ? DH / 2 : DH;  // elements a row at a time
+        constexpr int kLanes = DH / 8;       // 16-byte pieces of them
 #pragma unroll 1
         for (int d0 = 0; d0 < DH; d0 += per) {
 #pragma unroll 1
           for (int q = 0; q < per / 32; ++q) {
             uint32_t o[32];
-            if (nt > 0) {
+            if (act) {
               tc::tmem_ld32_nowait(o_col + d0 + 32 * q, o);
               tc::tmem_wait_ld();
             }
 #pragma unroll
-            for (int c = 0; c < 32; ++c)  // nothing seen: 0, whatever TMEM holds
-              o[c] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+            if (zero) {  // 0, whatever TMEM holds
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = l == 0.f ? 0u : o[c];
+            }
             if (part) {
 #pragma unroll
               for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(buf + lane * 256 + (((8 * q + c) ^ (lane & 15)) << 4)) =
+                *reinterpret_cast<uint4*>(qs + sw128(qr + lane, 8 * q + c)) =
                     make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             } else {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                uint32_t w[4];
+                uint32_t v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 v =
+                  const __nv_bfloat162 p2 =
                       __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * e]),
                                             __uint_as_float(o[8 * c + 2 * e + 1]));
-                  w[e] = *reinterpret_cast<const uint32_t*>(&v);
+                  v[e] = *reinterpret_cast<const uint32_t*>(&p2);
                 }
-                *reinterpret_cast<uint4*>(buf + lane * 256 + (((4 * q + c) ^ (lane & 15)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(qs + sw128(qr + lane, 4 * q + c)) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
               }
             }
           }
           __syncwarp();
-          for (int i = 0; i < lanes; ++i) {
-            const int rr = i * (32 / lanes) + lane / lanes, c = lane % lanes;
-            const long at = __shfl_sync(0xffffffffu, part ? prow : orow, rr);
-            const bool in = __shfl_sync(0xffffffffu, m < a.M, rr);
-            const uint4 v =
-                *reinterpret_cast<const uint4*>(buf + rr * 256 + ((c ^ (rr & 15)) << 4));
-            if (in) {
+#pragma unroll 4
+          for (int i = 0; i < kLanes; ++i) {
+            const int rr = i * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
+            const size_t at = __shfl_sync(0xffffffffu, part ? prow : (uint32_t)orow, rr);
+            const uint4 v = *reinterpret_cast<const uint4*>(qs + sw128(qr + rr, c));
+            if (m - lane + rr < a.M) {
               if (part) reinterpret_cast<uint4*>(a.po + at * DH + d0)[c] = v;
               else reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + at * DH)[c] = v;
             }
@@ -483,100 +621,137 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
           __syncwarp();
         }
       }
+      tc::fence_before_sync();
+      w = wn;
     }
-    tc::fence_before_sync();
   } else if (warp < 12) {
+    // ------------------------------------------------------------ slots
     const int p = tid - 256, last = a.Ncache - 1;
-    const uint8_t* kc = a.kcode + (long)bh * a.Ncache * (DH / 2);
-    const uint8_t* ks = a.kscale + (long)bh * a.Ncache * (DH / 16);
-    const uint8_t* vc = a.vcode + (long)bh * a.Ncache * (DH / 2);
-    const uint8_t* vs = a.vscale + (long)bh * a.Ncache * (DH / 16);
-    const int32_t* kpos = a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
     RawRow<DH> rk, rv;
-    if (nt > 0) {
-      const int slot = min(n_lo + p, last);
-      load_row<DH>(kc, ks, slot, rk);
-      load_row<DH>(vc, vs, slot, rv);
+    // the first item from x on with slots to read
+    const TcStride stride = tc_digits(a, gridDim.x);
+    auto busy = [&](TcWork x) {
+      while (x.item < items && x.nt == 0) x = tc_next(a, x, stride, items);
+      return x;
+    };
+    auto load = [&](const TcWork& x, int j, const uint8_t* c, const uint8_t* s, RawRow<DH>& o) {
+      const long base = (long)(x.b * a.Hkv + x.hkv) * a.Ncache;
+      load_row<DH>(c, s, base + min((long)x.n_lo + (long)j * kTile + p, (long)last), o);
+    };
+    TcWork w = busy(tc_first(a, items));
+    int j = 0;
+    if (w.item < items) {
+      load(w, 0, a.kcode, a.kscale, rk);
+      load(w, 0, a.vcode, a.vscale, rv);
     }
-    for (int j = 0; j < nt; ++j) {
-      const int st = j & 1;
-      const uint32_t ph = ((j >> 1) & 1) ^ 1;
-      const int next = (int)min((long)n_lo + (long)(j + 1) * kTile + p, (long)last);
+    for (int it = 0; w.item < items; ++it) {
+      const int st = it & 1;
+      const uint32_t ph = ((it >> 1) & 1) ^ 1;
+      TcWork wn = w;
+      int jn = j + 1;
+      if (jn == w.nt) {
+        wn = busy(tc_next(a, w, stride, items));
+        jn = 0;
+      }
+      const bool more = wn.item < items;
       if (!tc::mbar_wait(k_empty + st, ph, a.status, abort_flag)) break;
-      if (by_pos) pos_ring[(j & 3) * kTile + p] = kpos[min(n_lo + j * kTile + p, last)];
+      if (by_pos)
+        pos_ring[(it & 3) * kTile + p] =
+            a.kpos[(long)(w.b * a.Hkv + w.hkv) * a.Ncache + min(w.n_lo + j * kTile + p, last)];
       put_row<DH>(smem + SM::kK + st * SM::kOp, p, rk);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(k_full + st);
-      if (j + 1 < nt) load_row<DH>(kc, ks, next, rk);
+      if (more) load(wn, jn, a.kcode, a.kscale, rk);
       if (!tc::mbar_wait(v_empty + st, ph, a.status, abort_flag)) break;
       put_row<DH>(smem + SM::kV + st * SM::kOp, p, rv);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(v_full + st);
-      if (j + 1 < nt) load_row<DH>(vc, vs, next, rv);
+      if (more) load(wn, jn, a.vcode, a.vscale, rv);
+      w = wn;
+      j = jn;
     }
   } else {
-    if (warp == 12 && nt > 0) {
-      constexpr uint32_t kIdQK = idesc_f16(128, false), kIdPV = idesc_f16(DH, true);
-      const uint32_t qs = tc::smem_u32(smem), kb = qs + SM::kK, vb = qs + SM::kV;
-      auto qk = [&](int g, int j) {
-        const uint32_t q = qs + g * SM::kOp, k = kb + (j & 1) * SM::kOp;
+    // ------------------------------------------------------------ MMAs
+    constexpr uint32_t kIdQK = idesc_f16(128, false), kIdPV = idesc_f16(DH, true);
+    const uint32_t qb = tc::smem_u32(smem), kb = qb + SM::kK, vb = qb + SM::kV;
+    auto qk = [&](int g, int st) {
+      const uint32_t q = qb + g * SM::kOp, k = kb + st * SM::kOp;
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          const uint32_t off = (kk / 4) * 16384u + (kk % 4) * 32u;
-          mma_ss(tmem + g * 128, tc::desc_sw128(q + off, 16, 1024),
-                 tc::desc_sw128(k + off, 16, 1024), kIdQK, kk > 0);
-        }
-        tc::mma_commit(s_full + g);
-      };
-      auto pv = [&](int g, int j, int half) {
-        const uint32_t v = vb + (j & 1) * SM::kOp;
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        const uint32_t off = (kk / 4) * 16384u + (kk % 4) * 32u;
+        mma_ss(tmem + g * 128, tc::desc_sw128(q + off, 16, 1024),
+               tc::desc_sw128(k + off, 16, 1024), kIdQK, kk > 0);
+      }
+      tc::mma_commit(s_full + g);
+    };
+    auto pv = [&](int g, int st, int half, bool first) {
+      const uint32_t v = vb + st * SM::kOp;
 #pragma unroll
-        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-          mma_ts(tmem + 256 + g * 128, tmem + g * 128 + kk * 8,
-                 tc::desc_sw128(v + kk * 2048u, 16384, 1024), kIdPV, j > 0 || kk > 0);
-      };
-      const int ng = two ? 2 : 1;
-      bool ok = tc::mbar_wait(k_full, 0, a.status, abort_flag);
+      for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+        mma_ts(tmem + 256 + g * 128, tmem + g * 128 + kk * 8,
+               tc::desc_sw128(v + kk * 2048u, 16384, 1024), kIdPV, !first || kk > 0);
+    };
+    bool ok = true;
+    int it = 0, c0 = 0, c1 = 0, i0 = 0, i1 = 0;  // steps; each row tile's steps and items
+    auto wait = [&](uint64_t* bar, int n) {
+      if (ok) ok = tc::mbar_wait(bar, n & 1, a.status, abort_flag);
+    };
+    // P V of row tile g's step n, then S of its next step from stage stn
+    auto row_tile = [&](int g, int n, bool last_tile, bool first, bool more) {
+      const int st = it & 1, stn = st ^ 1;
+      wait(p_full + 2 * g, n);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+      if (ok && elect_one()) pv(g, st, 0, first);
+      __syncwarp();
+      wait(p_full + 2 * g + 1, n);
+      if (g == 0 && more) wait(k_full + stn, (it + 1) >> 1);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
       if (ok && elect_one()) {
-        for (int g = 0; g < ng; ++g) qk(g, 0);
-        tc::mma_commit(k_empty);
-      }
-      for (int j = 0; ok && j < nt; ++j) {
-        const int jn = j + 1, stn = jn & 1;
-        ok = tc::mbar_wait(v_full + (j & 1), (j >> 1) & 1, a.status, abort_flag);
-        for (int g = 0; ok && g < ng; ++g) {
-          ok = tc::mbar_wait(p_full + 2 * g, j & 1, a.status, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          tc::fence_after_sync();
-          if (ok && elect_one()) pv(g, j, 0);
-          __syncwarp();
-          if (ok) ok = tc::mbar_wait(p_full + 2 * g + 1, j & 1, a.status, abort_flag);
-          if (ok && g == 0 && jn < nt)
-            ok = tc::mbar_wait(k_full + stn, (jn >> 1) & 1, a.status, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          tc::fence_after_sync();
-          if (ok && elect_one()) {
-            pv(g, j, 1);
-            if (g == ng - 1) tc::mma_commit(v_empty + (j & 1));
-            if (jn < nt) {
-              qk(g, jn);
-              if (g == ng - 1) tc::mma_commit(k_empty + stn);
-            } else {
-              tc::mma_commit(o_full + g);
-            }
-          }
-          __syncwarp();
+        pv(g, st, 1, first);
+        if (last_tile) tc::mma_commit(v_empty + st);
+        if (more) {
+          qk(g, stn);
+          if (last_tile) tc::mma_commit(k_empty + stn);
+        } else {
+          tc::mma_commit(o_full + g);
         }
       }
-      if (!__all_sync(0xffffffffu, ok)) {  // wait for the MMAs issued before TMEM is freed
-        if (elect_one()) tc::mma_commit(drain);
-        const uint64_t t0 = tc::globaltimer();
-        while (!tc::mbar_try_wait(drain, 0) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {
-        }
+      __syncwarp();
+    };
+    auto first_s = [&](int g, int n, bool last_tile) {
+      wait(q_full + g, n);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+      if (ok && elect_one()) {
+        qk(g, it & 1);
+        if (last_tile) tc::mma_commit(k_empty + (it & 1));
+      }
+      __syncwarp();
+    };
+    const TcStride stride = tc_digits(a, gridDim.x);
+    TcWork w = tc_first(a, items);
+    while (ok && w.item < items) {
+      const TcWork wn = tc_next(a, w, stride, items);
+      if (w.nt > 0) {
+        wait(k_full + (it & 1), it >> 1);
+        first_s(0, i0++, !w.two);
+        if (w.two) first_s(1, i1++, true);
+      }
+      for (int j = 0; ok && j < w.nt; ++j, ++it) {
+        wait(v_full + (it & 1), it >> 1);
+        row_tile(0, c0++, !w.two, j == 0, j + 1 < w.nt);
+        if (w.two) row_tile(1, c1++, true, j == 0, j + 1 < w.nt);
+      }
+      w = wn;
+    }
+    if (!__all_sync(0xffffffffu, ok)) {  // wait for the MMAs issued before TMEM is freed
+      if (elect_one()) tc::mma_commit(drain);
+      const uint64_t t0 = tc::globaltimer();
+      while (!tc::mbar_try_wait(drain, 0) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {
       }
     }
     __syncwarp();
@@ -598,8 +773,9 @@ cudaError_t launch_tc(const Kv4AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  const long grid = (long)a.B * a.Hkv * a.ntile * a.nsplit;
-  return launch_pdl(kern, dim3((unsigned)grid), dim3(kTcThreads), TcSmem<DH>::kBytes, s, a);
+  const int items = a.B * a.Hkv * a.ntile * a.nsplit;
+  const int grid = items < a.num_sms ? items : a.num_sms;
+  return launch_pdl(kern, dim3((unsigned)grid), dim3(kTcThreads), TcSmem<DH>::kBytes, s, a, items);
 }
 
 }  // namespace

@@ -113,6 +113,7 @@ cudaError_t kv4_rows_run(const Kv4RowsArgs& a, bool load, cudaStream_t s);
 struct Kv4AttnArgs {
   const uint8_t* kcode; const uint8_t* kscale; const uint8_t* vcode; const uint8_t* vscale;
   const void* Q; int dtype; int B, T, Hq, Hkv, G, M, Ncache, dh; long q_ld;
+  uint64_t g_recip;     // ceil(2^40 / G)
   const int32_t* len; const int32_t* span; const int32_t* kpos; const int32_t* qpos;
   const float* slope;
   float scale;          // of a raw product: the caller's scale times kmul

@@ -522,7 +522,7 @@ ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V,
  * span[b][t][1] (span NULL: all): causal is [0, qpos + 1), a prefix mask
  * [0, max(prefix, qpos + 1)), a document mask the document's bounds.
  * Q: element (b, t, h, i) at [(b*T + t)*q_ld + h*dh + i]; query head h reads
- * KV head h / (Hq / Hkv). */
+ * KV head h / (Hq / Hkv).  B * T * Hq <= 2^25 - 1, Hq / Hkv <= 4096. */
 typedef struct {
   const void* Q;
   const int32_t* len;   /* [B] or NULL                                      */
