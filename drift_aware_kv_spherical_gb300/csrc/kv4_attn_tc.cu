@@ -41,7 +41,9 @@ struct TcSmem {
   static constexpr uint32_t kOp = (DH / 64) * 16384u;  // 128 rows of DH f16
   static constexpr uint32_t kK = 2 * kOp,  // Q at 0
                             kV = 4 * kOp, kPos = 6 * kOp;
-  static constexpr uint32_t kBar = kPos + 4 * kTile * 4;
+  static constexpr uint32_t kRow = kPos + 4 * kTile * 4;           // TcRow [256]
+  static constexpr uint32_t kWork = kRow + 2 * kTile * 24;         // TcWork, TcStride [8 warps]
+  static constexpr uint32_t kBar = kWork + 8 * 64;
   static constexpr size_t kBytes = 1024 + kBar + 256;
 };
 
@@ -88,7 +90,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) {
 struct TcWork {
   int item, split, tile, hkv, b;
   int n_lo, nt;  // first slot, steps
-  bool two;      // the second row tile holds rows
+  int two;       // the second row tile holds rows
 };
 struct TcStride {
   int split, tile, hkv, b;
@@ -107,7 +109,7 @@ __device__ __forceinline__ TcStride tc_digits(const Kv4AttnArgs& a, int n) {
 // The slots of w, for a whole warp: those within the rows' spans.
 __device__ __forceinline__ void tc_slots(const Kv4AttnArgs& a, TcWork& w, int items) {
   w.n_lo = w.nt = 0;
-  w.two = false;
+  w.two = 0;
   if (w.item >= items) return;
   const int m0 = w.tile * 2 * kTile;
   w.two = a.M - m0 > kTile;
@@ -139,7 +141,7 @@ __device__ __forceinline__ void tc_slots(const Kv4AttnArgs& a, TcWork& w, int it
 }
 __device__ __forceinline__ TcWork tc_first(const Kv4AttnArgs& a, int items) {
   const TcStride d = tc_digits(a, blockIdx.x);
-  TcWork w{(int)blockIdx.x, d.split, d.tile, d.hkv, d.b, 0, 0, false};
+  TcWork w{(int)blockIdx.x, d.split, d.tile, d.hkv, d.b, 0, 0, 0};
   tc_slots(a, w, items);
   return w;
 }
@@ -243,15 +245,32 @@ __device__ __forceinline__ float stage_q(const __nv_bfloat16* src, float scale, 
 }
 
 // ---------------------------------------------------------------- scores
-// The constants of a softmax thread's row.
+// The constants of a softmax thread's row.  They wait in shared memory, like the
+// item: what is not read in every step would push the scores out of registers.
 struct TcRow {
   float f;                // score factor of a raw product
   float slope2;           // distance bias in log2 units
-  int lo, hi, qpos;       // positions seen; the row's own
+  int lo, hi, qpos, len;  // positions seen; the row's own; the sequence's slots
 };
+template <class T>
+__device__ __forceinline__ void sm_put(volatile int* p, const T& x) {
+  static_assert(sizeof(T) % 4 == 0, "words");
+  const int* w = reinterpret_cast<const int*>(&x);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 4; ++i) p[i] = w[i];
+}
+template <class T>
+__device__ __forceinline__ T sm_get(volatile int* p) {
+  T x;
+  int* w = reinterpret_cast<int*>(&x);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 4; ++i) w[i] = p[i];
+  return x;
+}
 // Row m, token t of its sequence, query head h; nothing past the last row.
 __device__ __forceinline__ TcRow tc_row(const Kv4AttnArgs& a, bool in, int b, int t, int h) {
-  TcRow row{0.f, 0.f, 0, 0, 0};
+  TcRow row{0.f, 0.f, 0, 0, 0, 0};
+  row.len = min(max(a.len != nullptr ? __ldg(a.len + b) : a.Ncache, 0), a.Ncache);
   if (in) {
     const long tok = (long)b * a.T + t;
     if (a.slope != nullptr) row.slope2 = a.slope[h] * kLog2e;
@@ -272,9 +291,9 @@ enum TcSeen { kNone, kSome, kAll };
 struct TcRange {
   int any_lo, any_hi, all_lo, all_hi;  // slots that some, that every row sees
 };
-__device__ __forceinline__ TcRange tc_range(const TcRow& row, int len) {
+__device__ __forceinline__ TcRange tc_range(const TcRow& row) {
   const bool live = row.lo < row.hi;
-  const int hi = min(row.hi, len);
+  const int hi = min(row.hi, row.len);
   TcRange r;
   r.any_lo = __reduce_min_sync(0xffffffffu, live ? row.lo : INT32_MAX);
   r.any_hi = __reduce_max_sync(0xffffffffu, live ? hi : INT32_MIN);
@@ -287,18 +306,19 @@ __device__ __forceinline__ TcSeen tc_seen(const TcRange& r, int n0) {
   return n0 >= r.all_lo && n0 <= r.all_hi ? kAll : kSome;
 }
 
-// s[0..63]: raw products of 64 slots from n0 on -> log2-unit scores (GEN), and
+// s[0..C): raw products of C slots from n0 on -> log2-unit scores (GEN), and
 // -inf where the row does not see the slot.  pos: explicit positions, or null.
-template <bool GEN>
-__device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, const TcRow& row,
-                                          int n0, int len, TcSeen seen, const int* pos) {
+template <bool GEN, int C>
+__device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, volatile int* rowp,
+                                          int n0, TcSeen seen, const int* pos) {
+  const TcRow row = sm_get<TcRow>(rowp);
   if constexpr (GEN) {
     const float f2 = row.f * kLog2e;
     const uint64_t ff = f2_pack(f2, f2);
     if (a.cap > 0.f) {
       float t4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 64; c += 2)
+      for (int c = 0; c < C; c += 2)
         t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
       const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
       // y = score / cap = u kc, u the score in log2 units
@@ -310,7 +330,7 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, const 
                     c3 = k2 * k2 * k2 * (-17.f / 315.f);
         const uint64_t cc1 = f2_pack(c1, c1), cc2 = f2_pack(c2, c2), cc3 = f2_pack(c3, c3);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < C; c += 2) {
           const uint64_t u = f2_mul(f2_pack(s[c], s[c + 1]), ff), z = f2_mul(u, u);
           const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, cc3, cc2), cc1));
           f2_unpack(f2_fma(u, q, u), s[c], s[c + 1]);
@@ -319,40 +339,40 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, const 
         // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
         const float fe = 2.f * row.f * a.inv_cap * kLog2e, cap2 = a.cap * kLog2e;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
+        for (int c = 0; c < C; ++c) {
           const float e = exp2_approx(s[c] * fe);
           s[c] = cap2 * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
         }
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 64; c += 2)
+      for (int c = 0; c < C; c += 2)
         f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), ff), s[c], s[c + 1]);
     }
     if (a.slope != nullptr) {
       if (pos == nullptr) {
         const float dq = (float)(row.qpos - n0);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = fmaf(-row.slope2, fabsf(dq - (float)c), s[c]);
+        for (int c = 0; c < C; ++c) s[c] = fmaf(-row.slope2, fabsf(dq - (float)c), s[c]);
       } else {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < C; ++c)
           s[c] = fmaf(-row.slope2, fabsf((float)(row.qpos - pos[c])), s[c]);
       }
     }
     if (pos != nullptr) {
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
-        if (n0 + c >= len || pos[c] < row.lo || pos[c] >= row.hi) s[c] = -INFINITY;
+      for (int c = 0; c < C; ++c)
+        if (n0 + c >= row.len || pos[c] < row.lo || pos[c] >= row.hi) s[c] = -INFINITY;
       return;
     }
   }
   if (seen != kAll) {  // columns [lo, lo + num) are seen
-    const int lo = (int)min(max((long)row.lo - n0, 0L), 64L);
-    const int hi = (int)min(max((long)min(row.hi, len) - n0, 0L), 64L);
+    const int lo = (int)min(max((long)row.lo - n0, 0L), (long)C);
+    const int hi = (int)min(max((long)min(row.hi, row.len) - n0, 0L), (long)C);
     const uint32_t num = (uint32_t)max(hi - lo, 0);
 #pragma unroll
-    for (int c = 0; c < 64; ++c)
+    for (int c = 0; c < C; ++c)
       if ((uint32_t)(c - lo) >= num) s[c] = -INFINITY;
   }
 }
@@ -363,29 +383,30 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, const 
 // sees every slot (its own copy of the code: tests inside the passes cost a
 // fifth of the step).
 template <int DH, bool GEN, bool FAST>
-__device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, const TcRow& row, float f2,
-                                             int n0, int len, TcSeen seen0, TcSeen seen1,
-                                             const int* ps, uint32_t s_col, uint32_t o_col,
-                                             bool has_o, uint64_t* p_full, float& m_used,
-                                             float& l) {
-  // The maximum, 64 slots at a time; scores that are more than raw products go
-  // back to TMEM for the second pass.
+__device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int* row, float f2,
+                                             int n0, TcSeen seen0, TcSeen seen1, const int* ps,
+                                             uint32_t s_col, uint32_t o_col, bool has_o,
+                                             uint64_t* p_full, float& m_used, float& l) {
+  // The maximum; scores that are more than raw products go back to TMEM for the
+  // second pass (32 at a time then: their arithmetic needs registers too).
+  constexpr int C = GEN ? 32 : 64;
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains: one would wait on itself
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const TcSeen seen = FAST ? kAll : h == 0 ? seen0 : seen1;
+  for (int k = 0; k < 128; k += C) {
+    const TcSeen seen = FAST ? kAll : k < 64 ? seen0 : seen1;
     if (seen == kNone) continue;
-    float s[64];
-    tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
-    tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+    float s[C];
+#pragma unroll
+    for (int q = 0; q < C; q += 32)
+      tc::tmem_ld32_nowait(s_col + k + q, reinterpret_cast<uint32_t*>(s) + q);
     tc::tmem_wait_ld();
     if (GEN || !FAST) {
-      tc_scores<GEN>(a, s, row, n0 + 64 * h, len, seen, ps != nullptr ? ps + 64 * h : nullptr);
-      tc::tmem_st32(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
-      tc::tmem_st32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+      tc_scores<GEN, C>(a, s, row, n0 + k, seen, ps != nullptr ? ps + k : nullptr);
+#pragma unroll
+      for (int q = 0; q < C; q += 32) tc::tmem_st32(s_col + k + q, reinterpret_cast<uint32_t*>(s) + q);
     }
 #pragma unroll
-    for (int c = 0; c < 64; c += 2) m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
+    for (int c = 0; c < C; c += 2) m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
   }
   if (GEN || !FAST) tc::tmem_wait_st();
   const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f2;
@@ -494,58 +515,83 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
     const uint32_t o_col = tmem + lane_base + 256 + g * 128;
     uint8_t* qs = smem + g * SM::kOp;         // the row tile's operand
     const int qr = (warp & 3) * 32;           // the warp's first row in it
+    volatile int* rowp = reinterpret_cast<volatile int*>(smem + SM::kRow) + 6 * tid;
+    volatile int* keep = reinterpret_cast<volatile int*>(smem + SM::kWork) + warp * 16;
     bool ok = true;
-    int it = 0, rounds = 0;                   // steps and items that this row tile has done
-    int all = 0;                              // steps of both
-    const TcStride stride = tc_digits(a, gridDim.x);
-    TcWork w = tc_first(a, items);
-    while (ok && w.item < items) {
-      const int m = w.tile * 2 * kTile + r0 + lane;
-      const bool in = m < a.M;
-      const int t = row_token(a, m), h = w.hkv * a.G + (m - t * a.G);
-      const bool act = w.nt > 0 && (g == 0 || w.two);
-      TcRow row = tc_row(a, in, w.b, t, h);
-      const bool live = row.lo < row.hi;
-      const int len = min(max(a.len != nullptr ? __ldg(a.len + w.b) : a.Ncache, 0), a.Ncache);
-      const TcRange range = tc_range(row, len);
-      if (act) {
-        row.f = stage_q<DH>(in ? static_cast<const __nv_bfloat16*>(a.Q) +
-                                     ((long)w.b * a.T + t) * a.q_ld + (long)h * DH
-                               : nullptr,
-                            a.scale, qs, qr + lane);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(q_full + g);
+    int it = 0, rounds = 0, all = 0;  // the row tile's steps and items, both row tiles' steps
+    int nt;
+    {
+      if (lane == 0) sm_put(keep + 8, tc_digits(a, gridDim.x));
+      const TcWork w = tc_first(a, items);
+      if (lane == 0) sm_put(keep, w);
+      __syncwarp();
+    }
+    while (ok && keep[0] < items) {
+      TcRange range;
+      float f2;
+      bool act;
+      int n_lo;
+      {  // an item begins: the row's constants, its query
+        const TcWork w = sm_get<TcWork>(keep);
+        const int m = w.tile * 2 * kTile + r0 + lane;
+        const bool in = m < a.M;
+        const int t = row_token(a, m), h = w.hkv * a.G + (m - t * a.G);
+        nt = w.nt;
+        n_lo = w.n_lo;
+        act = nt > 0 && (g == 0 || w.two);
+        TcRow row = tc_row(a, in, w.b, t, h);
+        range = tc_range(row);
+        if (act) {
+          row.f = stage_q<DH>(in ? static_cast<const __nv_bfloat16*>(a.Q) +
+                                       ((long)w.b * a.T + t) * a.q_ld + (long)h * DH
+                                 : nullptr,
+                              a.scale, qs, qr + lane);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(q_full + g);
+        }
+        sm_put(rowp, row);
+        f2 = GEN ? 1.f : row.f * kLog2e;
       }
-      const float f2 = GEN ? 1.f : row.f * kLog2e;
       float m_used = -INFINITY, l = 0.f;
-      for (int j = 0; act && j < w.nt; ++j, ++it) {
-        const int n0 = w.n_lo + j * kTile;
+      for (int j = 0; act && j < nt; ++j, ++it) {
+        const int n0 = n_lo + j * kTile;
         if (!tc::mbar_wait(s_full + g, it & 1, a.status, abort_flag)) { ok = false; break; }
         tc::fence_after_sync();
-        const int* ps = by_pos ? pos_ring + ((all + j) & 3) * kTile : nullptr;
         const TcSeen seen0 = by_pos ? kSome : tc_seen(range, n0);
         const TcSeen seen1 = by_pos ? kSome : tc_seen(range, n0 + 64);
         if (seen0 == kAll && seen1 == kAll)
-          softmax_step<DH, GEN, true>(a, row, f2, n0, len, kAll, kAll, nullptr, s_col, o_col, j > 0,
+          softmax_step<DH, GEN, true>(a, rowp, f2, n0, kAll, kAll, nullptr, s_col, o_col, j > 0,
                                       p_full + 2 * g, m_used, l);
         else
-          softmax_step<DH, GEN, false>(a, row, f2, n0, len, seen0, seen1, ps, s_col, o_col, j > 0,
-                                       p_full + 2 * g, m_used, l);
+          // a step's positions: written before its K, and not again until the
+          // V of the third step after it has been asked for
+          softmax_step<DH, GEN, false>(a, rowp, f2, n0, seen0, seen1,
+                                       by_pos ? pos_ring + ((all + j) & 3) * kTile : nullptr,
+                                       s_col, o_col, j > 0, p_full + 2 * g, m_used, l);
       }
-      all += w.nt;
-      if (!live) {  // sees nothing anywhere
+      all += nt;
+      const TcWork w = sm_get<TcWork>(keep);
+      const int m = w.tile * 2 * kTile + r0 + lane;
+      const bool in = m < a.M;
+      const int t = row_token(a, m), h = w.hkv * a.G + (m - t * a.G);
+      if (rowp[2] >= rowp[3]) {  // sees nothing anywhere
         l = 0.f;
         m_used = -INFINITY;
       }
-      const TcWork wn = tc_next(a, w, stride, items);
-      if (wn.item < items) {  // the next item's queries into L2 while this one is finished
-        const int mn = wn.tile * 2 * kTile + r0 + lane, tn = row_token(a, mn);
-        if (mn < a.M)
-          l2_prefetch(static_cast<const __nv_bfloat16*>(a.Q) +
-                          ((long)wn.b * a.T + tn) * a.q_ld +
-                          (long)(wn.hkv * a.G + (mn - tn * a.G)) * DH,
-                      DH * 2);
+      {
+        const TcWork wn = tc_next(a, w, sm_get<TcStride>(keep + 8), items);
+        __syncwarp();
+        if (lane == 0) sm_put(keep, wn);
+        __syncwarp();
+        if (wn.item < items) {  // the next item's queries into L2 while this one is finished
+          const int mn = wn.tile * 2 * kTile + r0 + lane, tn = row_token(a, mn);
+          if (mn < a.M)
+            l2_prefetch(static_cast<const __nv_bfloat16*>(a.Q) +
+                            ((long)wn.b * a.T + tn) * a.q_ld +
+                            (long)(wn.hkv * a.G + (mn - tn * a.G)) * DH,
+                        DH * 2);
+        }
       }
       if (act && ok) {
         ok = tc::mbar_wait(o_full + g, rounds & 1, a.status, abort_flag);
@@ -622,7 +668,6 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
         }
       }
       tc::fence_before_sync();
-      w = wn;
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ slots
