@@ -98,7 +98,7 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr float kPShift = 12.f;  // log2 of the factor that P carries
+constexpr float kPShift = 10.f;  // log2 of the factor that P carries (times growth: < 2^16)
 
 // Per-row constants of a tile, in shared memory.
 struct RowPar {

@@ -1,7 +1,7 @@
 // Attention over a 4-bit KV cache, and the weight it puts on each slot.
 //
-//   k_kv4_attn     online-softmax attention of a 16- or 32-row tile of one KV
-//                  head's queries over a share of its slots
+//   k_kv4_attn     online-softmax attention of 8, 16 or 32 rows of one KV head's
+//                  queries over a share of its slots
 //   k_kv4_combine  the shares of a row joined
 //   k_kv4_weight   column sums of exp(s - lse), K only
 //
@@ -9,20 +9,22 @@
 // serves (row t G + j), so a head's K and V are read once for all of them.
 //
 // A warp works alone on 16 slots at a time, straight from global memory into
-// m16n8k16 operand fragments (f16, fp32 accumulators):
-//   S = Q K^T   the 16 contraction indices of a step may be any 16 elements as
+// m16n8k16 operand fragments (f16, fp32 accumulators), the slots as the 16 and
+// the query rows as the 8, since one token has few rows:
+//   S^T = K Q^T  the 16 contraction indices of a step may be any 16 elements as
 //     long as Q and K agree: lane (g, t) = (lane / 4, lane % 4) takes elements
-//     [t dh/4, (t+1) dh/4) of the slot of its column g, one contiguous load,
-//     and step ks uses elements 4 ks .. 4 ks + 3 of it.  Q is laid out in that
-//     order in shared memory, one 16-byte load a step.
-//   O = P V     column c of S stands for slot 4 (c/2) + c%2 (first n8 tile) or
-//     that + 2 (second), so lane t's four scores belong to slots 4t .. 4t+3,
-//     whose V rows it loads itself: elements [g dh/8, (g+1) dh/8), one n8 tile
-//     of O a code.  The slot pairs are joined by byte permutes.
+//     [t dh/4, (t+1) dh/4) of slots g and g + 8, one contiguous load each, and
+//     step ks uses elements 4 ks .. 4 ks + 3 of them.  Q is laid out in that
+//     order in shared memory.
+//   O^T = V^T P^T  P^T needs the slots where S^T has the rows: one 8 x 8
+//     transpose instruction each 8 slots.  Lane (g, t) then multiplies V of
+//     slots 2t, 2t+1, 2t+8, 2t+9, elements [g dh/8, (g+1) dh/8), which it loads
+//     itself; the codes of two slots are interleaved before they are converted,
+//     so that a conversion gives a pair of slots.
 // Q is scaled by a power of two of its row's own (2^14 <= max |q| < 2^15), so
 // bf16 queries are exact in f16 down to 2^-25 of the row's largest; fp32
-// queries and P take two f16 terms (hi + lo).  P carries a factor 2^12, which
-// keeps weights down to 2^-26 of the row's largest out of f16's subnormals.
+// queries and P take two f16 terms (hi + lo).  P carries a factor 2^kPShift,
+// which keeps small weights out of f16's subnormals.
 #include "kv4.cuh"
 
 namespace ps {
@@ -30,63 +32,68 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-// Rows [m0, m0 + rows) of (b, hkv) into shared memory as A fragments
-// [mt][part][ks][lane] (uint4), with their constants; rows past M are zero
-// and see nothing.  One warp a row.
+constexpr float kGrow = 4.f;  // log2 growth of a maximum before O is rescaled
+// Rows [m0, m0 + rows) of (b, hkv) into shared memory as B fragments
+// [row / 8][part][ks / 2][lane] (uint4: two steps' pairs), with their constants;
+// rows past M are zero and see nothing.  DH / 8 lanes a row, every load of a
+// thread issued before the first is used.
 template <int DH, bool F32>
 __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv, int m0, int rows,
-                                           uint4* qs, RowPar* par, int nwarps) {
-  constexpr int KS = DH / 16, E = DH / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = warp; r < rows; r += nwarps) {
+                                           uint4* qs, RowPar* par) {
+  constexpr int KS = DH / 16, LN = DH / 8, P = F32 ? 2 : 1;
+  const int sub = threadIdx.x % LN, step = blockDim.x / LN;
+  for (int r = threadIdx.x / LN; r < rows; r += step) {
     const int m = m0 + r;
-    float x[E];
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     RowPar p{0.f, 0.f, 0, 0, 0, -INFINITY};
     if (m < a.M) {
       const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
       const long tok = (long)b * a.T + t;
-      const long at = tok * a.q_ld + (long)h * DH + lane * E;
+      const long at = tok * a.q_ld + (long)h * DH + sub * 8;
       if constexpr (F32) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = static_cast<const float*>(a.Q)[at + e];
+        load16(static_cast<const float*>(a.Q) + at, x);
+        load16(static_cast<const float*>(a.Q) + at + 4, x + 4);
       } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          x[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.Q)[at + e]);
+        load16(static_cast<const __nv_bfloat16*>(a.Q) + at, x);
       }
       p.slope = a.slope != nullptr ? a.slope[h] : 0.f;
       p.lo = a.span != nullptr ? a.span[2 * tok] : 0;
       p.hi = a.span != nullptr ? a.span[2 * tok + 1] : INT32_MAX;
       p.qpos = a.qpos != nullptr ? a.qpos[tok] : 0;
       p.lse = a.lse_in != nullptr ? a.lse_in[tok * a.Hq + h] : -INFINITY;
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = 0.f;
     }
     float mx = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
-    mx = warp_max(mx);
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+    const uint32_t mask = (uint32_t)((1ull << LN) - 1) << ((threadIdx.x & 31) & ~(LN - 1));
+#pragma unroll
+    for (int o = LN / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, o));
     float up;
     row_scale(mx, a.scale, &up, &p.f);
-    if (lane == 0) par[r] = p;
-    __half* hq = reinterpret_cast<__half*>(qs);
+    if (sub == 0) par[r] = p;
+    // elements 8 sub .. 8 sub + 7: lane t = d / (DH / 4) of the fragment, steps
+    // ks = d % (DH / 4) / 4 and the next, two pairs each
+    const int t = 8 * sub / (DH / 4), ks = 8 * sub % (DH / 4) / 4;
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int d = lane * E + e, t = d / (DH / 4), rem = d % (DH / 4);
-      const int ks = rem / 4, j = rem % 4;
-      const int reg = (j / 2) * 2 + (r % 16) / 8, fl = (r % 8) * 4 + t;
-      const float v = x[e] * up;
-      const __half hi = __float2half_rn(v);
-      constexpr int P = F32 ? 2 : 1;
-      const size_t base = ((((size_t)(r / 16) * P) * KS + ks) * 32 + fl) * 8 + reg * 2 + (j & 1);
-      hq[base] = hi;
-      if constexpr (F32) hq[base + (size_t)KS * 32 * 8] = __float2half_rn(v - __half2float(hi));
+    for (int e = 0; e < 4; ++e) {
+      const float v0 = x[2 * e] * up, v1 = x[2 * e + 1] * up;
+      const __half2 h = __floats2half2_rn(v0, v1);
+      hi[e] = h2_bits(h);
+      if constexpr (F32) {
+        const float2 back = __half22float2(h);
+        lo[e] = h2_bits(__floats2half2_rn(v0 - back.x, v1 - back.y));
+      }
     }
+    uint4* at = qs + ((size_t)(r / 8) * P * (KS / 2) + ks / 2) * 32 + (r % 8) * 4 + t;
+    *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (F32) at[(KS / 2) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
-// K of the lane's two slots of a 16-slot step (raw codes and scale bytes).
+// What a lane loads of a 16-slot step: K of slots g and g + 8, elements
+// [t dh/4, (t+1) dh/4); V of slots 2t, 2t+1, 2t+8, 2t+9, elements [g dh/8,
+// (g+1) dh/8); the block scales that go with them.
 template <int DH>
 struct RawK {
   uint32_t c[2][DH / 32];
@@ -103,7 +110,7 @@ __device__ __forceinline__ void load_k(const uint8_t* kc, const uint8_t* ks, int
                                        int g, int t, RawK<DH>& o) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const long slot = min(n + 4 * (g >> 1) + (g & 1) + 2 * j, last);
+    const long slot = min(n + g + 8 * j, last);
     const uint8_t* p = kc + slot * (DH / 2) + t * (DH / 8);
     const uint8_t* q = ks + slot * (DH / 16) + t * (DH / 64);
     if constexpr (DH == 64) {
@@ -128,7 +135,7 @@ __device__ __forceinline__ void load_v(const uint8_t* vc, const uint8_t* vs, int
                                        int g, int t, RawV<DH>& o) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const long slot = min(n + 4 * t + j, last);
+    const long slot = min(n + 2 * t + (j & 1) + 4 * (j & 2), last);
     const uint8_t* p = vc + slot * (DH / 2) + g * (DH / 16);
     const uint8_t* q = vs + slot * (DH / 16);
     if constexpr (DH == 64) {
@@ -146,36 +153,49 @@ __device__ __forceinline__ void load_v(const uint8_t* vc, const uint8_t* vs, int
   }
 }
 
-// B fragments of K: kf[j][ks][0..1] for the lane's slot of n8 tile j.
+// Word w of the lane's K as A fragments of steps 2 w and 2 w + 1.
 template <int DH>
-__device__ __forceinline__ void dequant_k(const RawK<DH>& r, uint32_t (*kf)[DH / 16][2]) {
+__device__ __forceinline__ void dequant_k(const RawK<DH>& r, int w, uint32_t* a0, uint32_t* a1) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int w = 0; w < DH / 32; ++w) {
-      uint32_t h[4];
-      e2m1x8_f16(r.c[j][w], h);
-      // word w holds elements 8 w .. 8 w + 7 of the lane's dh / 4: two a scale
-      const __half2 s = e4m3_pair((r.s[j] >> (8 * (w / 2))) & 0xffu);
-      kf[j][2 * w][0] = h2_bits(__hmul2(h2_of(h[0]), s));
-      kf[j][2 * w][1] = h2_bits(__hmul2(h2_of(h[1]), s));
-      kf[j][2 * w + 1][0] = h2_bits(__hmul2(h2_of(h[2]), s));
-      kf[j][2 * w + 1][1] = h2_bits(__hmul2(h2_of(h[3]), s));
-    }
+  for (int j = 0; j < 2; ++j) {
+    // eight elements a word, two words a scale, two scales a conversion
+    const uint32_t two = h2_bits(e4m3x2_f16(DH == 64 ? r.s[j] : r.s[j] >> (16 * (w / 4))));
+    const __half2 s = h2_of(__byte_perm(two, two, (w / 2) & 1 ? 0x3232u : 0x1010u));
+    uint32_t h[4];
+    e2m1x8_f16(r.c[j][w], h);
+    a0[j] = h2_bits(__hmul2(h2_of(h[0]), s));
+    a0[2 + j] = h2_bits(__hmul2(h2_of(h[1]), s));
+    a1[j] = h2_bits(__hmul2(h2_of(h[2]), s));
+    a1[2 + j] = h2_bits(__hmul2(h2_of(h[3]), s));
+  }
 }
 
-template <int DH, int MT, bool F32>
+// Codes of word w of slots a and b (a = 2 j2) interleaved before they are
+// converted: byte q of *even holds element 2 q of both, of *odd element 2 q + 1.
+__device__ __forceinline__ void pair_codes(uint32_t a, uint32_t b, uint32_t* even, uint32_t* odd) {
+  *even = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+  *odd = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+}
+
+// The 8 x 8 matrix of 16-bit values that a warp holds (lane 4 i + j: row i,
+// columns 2 j and 2 j + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <int DH, int NB, bool F32>
 __global__ void __launch_bounds__(kThreads)
 k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
-  constexpr int KS = DH / 16, NT = DH / 8, P = F32 ? 2 : 1;
-  constexpr int kRows = 16 * MT;
+  constexpr int KS = DH / 16, MT = DH / 16, P = F32 ? 2 : 1;  // QK steps; O tiles of 16 elements
+  constexpr int kRows = 8 * NB;
   pdl_prologue();
   extern __shared__ uint4 smem4[];
-  uint4* qs = smem4;                                             // MT * P * KS * 32
-  float* obuf = reinterpret_cast<float*>(smem4);                 // kWarps * kRows * DH, after the loop
+  uint4* qs = smem4;                               // NB * P * KS / 2 * 32
+  float* obuf = reinterpret_cast<float*>(smem4);   // kWarps * kRows * DH, after the loop
   __shared__ RowPar par[kRows];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  __shared__ int s_range[4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int tile = blockIdx.x % a.ntile;
   const int split = blockIdx.x / a.ntile % a.nsplit;
@@ -184,47 +204,40 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   const int rows = min(kRows, a.M - m0);
   const int len = kv4_len(a, b);
 
-  stage_rows<DH, F32>(a, b, hkv, m0, kRows, qs, par, kWarps);
+  stage_rows<DH, F32>(a, b, hkv, m0, kRows, qs, par);
   __syncthreads();
   // positions that some row sees, and that every row sees
-  if (warp == 0) {
-    int lo = INT32_MAX, hi = INT32_MIN, lo_all = INT32_MIN, hi_all = INT32_MAX;
-    for (int r = lane; r < rows; r += 32) {
-      if (par[r].lo < par[r].hi) {
-        lo = min(lo, par[r].lo);
-        hi = max(hi, par[r].hi);
-      }
-      lo_all = max(lo_all, par[r].lo);
-      hi_all = min(hi_all, par[r].hi);
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      lo_all = max(lo_all, __shfl_xor_sync(0xffffffffu, lo_all, o));
-      hi_all = min(hi_all, __shfl_xor_sync(0xffffffffu, hi_all, o));
-    }
-    if (lane == 0) {
-      s_range[0] = lo; s_range[1] = hi; s_range[2] = lo_all; s_range[3] = hi_all;
-    }
-  }
-  __syncthreads();
-  const int32_t* kpos = a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
   int n_lo = 0, n_hi = len, all_lo = 0, all_hi = len;
-  if (kpos == nullptr) {  // slots are positions: skip what no row sees
-    n_lo = max(0, s_range[0]) & ~15;
-    n_hi = min(len, s_range[1]);
-    all_lo = s_range[2];
-    all_hi = min(len, s_range[3]);
-  } else if (a.span != nullptr) {
-    all_hi = -1;
+  const int32_t* kpos = a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
+  if (kpos != nullptr) {
+    if (a.span != nullptr) all_hi = -1;
+  } else if (a.span != nullptr) {  // slots are positions: skip what no row sees
+    const int lo = lane < rows ? par[lane].lo : 0, hi = lane < rows ? par[lane].hi : 0;
+    const bool in = lo < hi, row = lane < rows;
+    n_lo = max(0, __reduce_min_sync(0xffffffffu, in ? lo : INT32_MAX));
+    n_hi = min(len, __reduce_max_sync(0xffffffffu, in ? hi : INT32_MIN));
+    all_lo = __reduce_max_sync(0xffffffffu, row ? lo : INT32_MIN);
+    all_hi = min(len, __reduce_min_sync(0xffffffffu, row ? hi : INT32_MAX));
   }
-  // this CTA's share: whole 64-slot groups
+  // This CTA's share, whole 64-slot groups: of the slots seen where spans pick
+  // them, else of the cache, so that all shares take as long and sequences of
+  // unequal length just have fewer of them.
   if (n_lo >= n_hi) {
     n_lo = n_hi = 0;
-  } else {
-    const int share = ceil_div(ceil_div(n_hi - n_lo, 64), a.nsplit) * 64;
-    n_lo = min(n_hi, n_lo + split * share);
-    n_hi = min(n_hi, n_lo + share);
+  } else if (a.nsplit > 1) {
+    const int of = a.span != nullptr ? n_hi - n_lo : a.Ncache;
+    const int share = ceil_div(ceil_div(of, 64), a.nsplit) * 64;
+    n_lo = (int)min((long)n_hi, n_lo + (long)split * share);
+    n_hi = (int)min((long)n_hi, (long)n_lo + share);
+  }
+
+  if (a.nsplit > 1 && n_lo >= n_hi) {  // an empty share
+    if (tid < rows) {
+      const size_t at = ((size_t)bh * a.M + m0 + tid) * a.nsplit + split;
+      a.pml[2 * at] = -INFINITY;
+      a.pml[2 * at + 1] = 0.f;
+    }
+    return;
   }
 
   const uint8_t* kc = a.kcode + (long)bh * a.Ncache * (DH / 2);
@@ -233,162 +246,178 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   const uint8_t* vs = a.vscale + (long)bh * a.Ncache * (DH / 16);
   const int last = a.Ncache - 1;
 
-  float o[MT][NT][4], mrow[MT][2], lrow[MT][2];
+  // O of rows 8 nb + 2 t + (c & 1), elements [g dh/8, (g+1) dh/8): element
+  // 2 i + c / 2 in o[nb][i][c]
+  float o[NB][MT][4], mrow[NB][2], lrow[NB][2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[mt][i][c] = 0.f;
-    mrow[mt][0] = mrow[mt][1] = -INFINITY;
-    lrow[mt][0] = lrow[mt][1] = 0.f;
+      for (int c = 0; c < 4; ++c) o[nb][i][c] = 0.f;
+    mrow[nb][0] = mrow[nb][1] = -INFINITY;
+    lrow[nb][0] = lrow[nb][1] = 0.f;
   }
-  for (int n = n_lo + 16 * warp; n < n_hi; n += 16 * kWarps) {
-    RawK<DH> rk;
-    RawV<DH> rv;
+  RawK<DH> rk;
+  RawV<DH> rv;
+  int n = n_lo + 16 * warp;
+  if (n < n_hi) {
     load_k<DH>(kc, ks, n, last, g, t, rk);
     load_v<DH>(vc, vs, n, last, g, t, rv);
-    // scores
-    float s[MT][2][4];
-    {
-      uint32_t kf[2][KS][2];
-      dequant_k<DH>(rk, kf);
+  }
+  for (; n < n_hi; n += 16 * kWarps) {
+    const int next = min(n + 16 * kWarps, last);  // past the end: loaded, not used
+    // S^T: slots g and g + 8 (c / 2), rows 2 t and 2 t + 1 (c & 1) of block nb
+    float s[NB][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int c = 0; c < 4; ++c) s[nb][c] = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[mt][j][c] = 0.f;
+    for (int w = 0; w < KS / 2; ++w) {
+      uint32_t a0[4], a1[4];
+      dequant_k<DH>(rk, w, a0, a1);
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const uint4 q = qs[((mt * P + p) * KS + k) * 32 + lane];
-            mma_f16(s[mt][0], &q.x, kf[0][k][0], kf[0][k][1]);
-            mma_f16(s[mt][1], &q.x, kf[1][k][0], kf[1][k][1]);
-          }
+        for (int p = 0; p < P; ++p) {
+          const uint4 q = qs[((nb * P + p) * (KS / 2) + w) * 32 + lane];
+          mma_f16(s[nb], a0, q.x, q.y);
+          mma_f16(s[nb], a1, q.z, q.w);
+        }
     }
+    load_k<DH>(kc, ks, next, last, g, t, rk);
     const bool masked = n < all_lo || n + 16 > all_hi;
-    int pos[4];
+    int pos[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int slot = min(n + 4 * t + i, last);
-      pos[i] = kpos != nullptr ? __ldg(kpos + slot) : slot;
+    for (int j = 0; j < 2; ++j) {
+      const int slot = min(n + g + 8 * j, last);
+      pos[j] = kpos != nullptr ? __ldg(kpos + slot) : slot;
     }
-    uint32_t ph[MT][4], pl[MT][F32 ? 4 : 1];
+    uint32_t ph[NB][2], pl[NB][F32 ? 2 : 1];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nb = 0; nb < NB; ++nb) {
+      float x[4];
+      bool grow = false;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {  // rows g and g + 8
-        const RowPar& rp = par[mt * 16 + g + 8 * u];
-        const float f = rp.f, slope = rp.slope;
-        const int qpos = rp.qpos, lo = rp.lo, hi = rp.hi;
-        float x[4], mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = kv4_score<F32>(a, s[mt][i >> 1][2 * u + (i & 1)], f, slope, qpos, pos[i]) * kLog2e;
-          if (masked && (n + 4 * t + i >= len || pos[i] < lo || pos[i] >= hi)) x[i] = -INFINITY;
-          mx = fmaxf(mx, x[i]);
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(mrow[mt][u], mx);
-        if (__any_sync(0xffffffffu, m_new > mrow[mt][u])) {
-          const float corr = m_new > mrow[mt][u] ? exp2_approx(mrow[mt][u] - m_new) : 1.f;
-          lrow[mt][u] *= corr;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            o[mt][i][2 * u] *= corr;
-            o[mt][i][2 * u + 1] *= corr;
-          }
-          mrow[mt][u] = m_new;
-        }
-        const float base = m_new == -INFINITY ? 0.f : m_new - kPShift;
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = exp2_approx(x[i] - base);
-          lrow[mt][u] += p[i];
-        }
-        // A fragment: a0/a1 first n8 tile (rows g, g + 8), a2/a3 the second
+      for (int u = 0; u < 2; ++u) {  // rows 2 t, 2 t + 1
+        const RowPar& rp = par[nb * 8 + 2 * t + u];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
-          ph[mt][2 * j + u] = h2_bits(h);
-          if constexpr (F32) {
-            const float2 back = __half22float2(h);
-            pl[mt][2 * j + u] = h2_bits(__floats2half2_rn(p[2 * j] - back.x, p[2 * j + 1] - back.y));
+          float v = kv4_score<F32>(a, s[nb][2 * j + u], rp.f, rp.slope, rp.qpos, pos[j]) * kLog2e;
+          if (masked && (n + g + 8 * j >= len || pos[j] < rp.lo || pos[j] >= rp.hi)) v = -INFINITY;
+          x[2 * j + u] = v;
+        }
+        grow |= fmaxf(x[u], x[2 + u]) > mrow[nb][u] + kGrow;
+      }
+      // The running maximum follows only when some row has outgrown it by
+      // 2^kGrow; until then P carries a factor up to that.
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float mx = fmaxf(x[u], x[2 + u]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const bool up = mx > mrow[nb][u] + kGrow;
+          const float corr = up ? exp2_approx(mrow[nb][u] - mx) : 1.f;
+          if (up) mrow[nb][u] = mx;
+          lrow[nb][u] *= corr;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[nb][i][u] *= corr;
+            o[nb][i][2 + u] *= corr;
           }
         }
       }
+      float p[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float base = mrow[nb][c & 1] == -INFINITY ? 0.f : mrow[nb][c & 1] - kPShift;
+        p[c] = exp2_approx(x[c] - base);
+        lrow[nb][c & 1] += p[c];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {  // slots 8 j .. 8 j + 7: (slot, rows) -> (row, slots)
+        const __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
+        ph[nb][j] = transpose8(h2_bits(h));
+        if constexpr (F32) {
+          const float2 back = __half22float2(h);
+          pl[nb][j] =
+              transpose8(h2_bits(__floats2half2_rn(p[2 * j] - back.x, p[2 * j + 1] - back.y)));
+        }
+      }
     }
-    // O += P V
+    // O^T += V^T P^T
 #pragma unroll
     for (int w = 0; w < DH / 64; ++w) {
-      uint32_t v[4][4];
+      uint32_t v[2][2][4];  // [even, odd element][slots 2t.., 2t + 8..][byte]
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        e2m1x8_f16(rv.c[j][w], v[j]);
-        const __half2 sc = e4m3_pair((rv.s[j] >> (DH == 256 ? 8 * (w / 2) : 0)) & 0xffu);
+      for (int j = 0; j < 2; ++j) {
+        uint32_t even, odd;
+        pair_codes(rv.c[2 * j][w], rv.c[2 * j + 1][w], &even, &odd);
+        const int sh = DH == 256 ? 8 * (w / 2) : 0;
+        const __half2 sc =
+            e4m3x2_f16(((rv.s[2 * j] >> sh) & 0xffu) | ((rv.s[2 * j + 1] >> sh) & 0xffu) << 8);
+        e2m1x8_f16(even, v[0][j]);
+        e2m1x8_f16(odd, v[1][j]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[j][q] = h2_bits(__hmul2(h2_of(v[j][q]), sc));
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[e][j][q] = h2_bits(__hmul2(h2_of(v[e][j][q]), sc));
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t av[4] = {v[0][0][q], v[1][0][q], v[0][1][q], v[1][1][q]};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half == 0 ? 0x5410u : 0x7632u;
-          const uint32_t b0 = __byte_perm(v[0][q], v[1][q], sel);
-          const uint32_t b1 = __byte_perm(v[2][q], v[3][q], sel);
-          const int i = 8 * w + 2 * q + half;
+        for (int nb = 0; nb < NB; ++nb) {
+          float* d = o[nb][4 * w + q];
+          if constexpr (F32) {
+            // the tensor cores truncate what they add to an accumulator: over
+            // thousands of steps that shows in fp32, so each step's product is
+            // added by a rounding instruction
+            float e[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(e, av, ph[nb][0], ph[nb][1]);
+            mma_f16(e, av, pl[nb][0], pl[nb][1]);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if constexpr (F32) {
-              // the tensor cores truncate what they add to an accumulator:
-              // over thousands of steps that shows in fp32, so each step's
-              // product is added by a rounding instruction
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(d, ph[mt], b0, b1);
-              mma_f16(d, pl[mt], b0, b1);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) o[mt][i][c] += d[c];
-            } else {
-              mma_f16(o[mt][i], ph[mt], b0, b1);
-            }
+            for (int c = 0; c < 4; ++c) d[c] += e[c];
+          } else {
+            mma_f16(d, av, ph[nb][0], ph[nb][1]);
           }
         }
+      }
     }
+    load_v<DH>(vc, vs, next, last, g, t, rv);
   }
 
   // the four warps' shares of each row joined
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      float l = lrow[mt][u];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (t == 0) {
-        s_m[warp][mt * 16 + g + 8 * u] = mrow[mt][u];
-        s_l[warp][mt * 16 + g + 8 * u] = l;
+      float l = lrow[nb][u];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (g == 0) {
+        s_m[warp][nb * 8 + 2 * t + u] = mrow[nb][u];
+        s_l[warp][nb * 8 + 2 * t + u] = l;
       }
     }
   __syncthreads();  // Q is no longer read
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      const int r = nb * 8 + 2 * t + u;
+      if (r < rows) {
+        float* dst = obuf + ((size_t)warp * kRows + r) * DH + g * (DH / 8);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float* dst = obuf + ((size_t)warp * kRows + mt * 16 + g + 8 * u) * DH + (2 * t + c) * NT;
-#pragma unroll
-        for (int i = 0; i < NT; i += 4)
-          *reinterpret_cast<float4*>(dst + i) =
-              make_float4(o[mt][i][2 * u + c], o[mt][i + 1][2 * u + c], o[mt][i + 2][2 * u + c],
-                          o[mt][i + 3][2 * u + c]);
+        for (int i = 0; i < MT; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(
+              o[nb][i][u], o[nb][i][2 + u], o[nb][i + 1][u], o[nb][i + 1][2 + u]);
       }
+    }
   __syncthreads();
   for (int e = tid; e < rows * (DH / 4); e += kThreads) {
     const int r = e / (DH / 4), d = e % (DH / 4) * 4, m = m0 + r;
@@ -406,7 +435,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     }
     if (a.nsplit > 1) {
       const size_t at = ((size_t)bh * a.M + m) * a.nsplit + split;
-      *reinterpret_cast<float4*>(a.po + at * DH + d) = acc;
+      if (l != 0.f) *reinterpret_cast<float4*>(a.po + at * DH + d) = acc;
       if (d == 0) {
         a.pml[2 * at] = mx;
         a.pml[2 * at + 1] = l;
@@ -417,36 +446,52 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   }
 }
 
-// dh / 4 threads a row, four elements each.
+// One CTA a row: dh / 4 threads take four elements each of every 512 / dh-th
+// share, and the groups are joined in order.
 template <int DH, bool F32>
 __global__ void __launch_bounds__(128)
 k_kv4_combine(const __grid_constant__ Kv4AttnArgs a) {
+  constexpr int LN = DH / 4, NG = 128 / LN;  // threads a share, shares at a time
   pdl_prologue();
-  constexpr int LN = DH / 4;  // threads a row
-  const long idx = ((long)blockIdx.x * 128 + threadIdx.x) / LN;
-  const int d = (threadIdx.x % LN) * 4;
-  if (idx >= (long)a.B * a.Hkv * a.M) return;
-  const int bh = (int)(idx / a.M), m = (int)(idx % a.M);
+  __shared__ float s_part[NG][DH], s_l[NG], s_w[4];
+  const int idx = blockIdx.x, bh = idx / a.M, m = idx - bh * a.M;
+  const int tid = threadIdx.x, grp = tid / LN, d = (tid % LN) * 4;
   const float* ml = a.pml + (size_t)idx * a.nsplit * 2;
   const float* po = a.po + (size_t)idx * a.nsplit * DH + d;
   float mx = -INFINITY;
-  for (int s = 0; s < a.nsplit; ++s) mx = fmaxf(mx, ml[2 * s]);
+  for (int s = tid; s < a.nsplit; s += 128) mx = fmaxf(mx, ml[2 * s]);
+  mx = warp_max(mx);
+  if ((tid & 31) == 0) s_w[tid >> 5] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(s_w[0], s_w[1]), fmaxf(s_w[2], s_w[3]));
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float c = ml[2 * s] == -INFINITY ? 1.f : exp2_approx(ml[2 * s] - mx);
+  for (int s = grp; s < a.nsplit; s += NG) {
+    const float ms = ml[2 * s], ls = ml[2 * s + 1];
+    if (ls == 0.f) continue;  // saw nothing: its sums may not have been written
+    const float c = ms == -INFINITY ? 1.f : exp2_approx(ms - mx);
     const float4 v = *reinterpret_cast<const float4*>(po + (size_t)s * DH);
-    l += c * ml[2 * s + 1];
+    l += c * ls;
     acc.x += c * v.x; acc.y += c * v.y; acc.z += c * v.z; acc.w += c * v.w;
+  }
+  *reinterpret_cast<float4*>(&s_part[grp][d]) = acc;
+  if (d == 0) s_l[grp] = l;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int q = 1; q < NG; ++q) {
+    const float4 v = *reinterpret_cast<const float4*>(&s_part[q][d]);
+    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    l = q == 1 ? s_l[0] + s_l[1] : l + s_l[q];
   }
   kv4_finish<F32>(a, bh / a.Hkv, bh % a.Hkv, m, DH, d, acc, mx, l);
 }
 
-// K only: a CTA owns 64 slots at a time (16 a warp), their K fragments stay in
-// registers while all rows of the head pass by (64 at a time through shared
-// memory); every slot's sum is one CTA's, in row order, so the result does not
-// depend on timing.
+// K only: a warp owns 16 slots at a time, whose K fragments stay in registers
+// while all rows of the head pass by (kWRows at a time through shared memory);
+// every slot's sum is one warp's, in row order, so the result does not depend
+// on timing.
 constexpr int kWRows = 64;
 
 template <int DH, bool F32>
@@ -455,7 +500,7 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   constexpr int KS = DH / 16, P = F32 ? 2 : 1;
   pdl_prologue();
   extern __shared__ uint4 smem4[];
-  uint4* qs = smem4;  // (kWRows / 16) * P * KS * 32
+  uint4* qs = smem4;  // (kWRows / 8) * P * KS / 2 * 32
   __shared__ RowPar par[kWRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int bh = blockIdx.y, b = bh / a.Hkv, hkv = bh % a.Hkv;
@@ -466,83 +511,81 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   const float* w_in = a.w_in != nullptr ? a.w_in + (long)bh * a.Ncache : nullptr;
   float* w_out = a.w_out + (long)bh * a.Ncache;
   const int chunks = ceil_div(a.M, kWRows);
+  const int n0 = (blockIdx.x * steps) * 64 + 16 * warp;
+  RawK<DH> rk;
+  if (n0 < len) load_k<DH>(kc, ks, n0, last, g, t, rk);
   for (int st = 0; st < steps; ++st) {
-    const int n = (blockIdx.x * steps + st) * 64 + 16 * warp;
+    const int n = n0 + 64 * st;
     const bool live = n < len;  // warp-uniform
-    uint32_t kf[2][KS][2];
-    int pos[4];
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t kf[KS][4];
+    int pos[2];
+    float acc[2] = {0.f, 0.f};  // slots g and g + 8
     if (live) {
-      RawK<DH> rk;
-      load_k<DH>(kc, ks, n, last, g, t, rk);
-      dequant_k<DH>(rk, kf);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int slot = min(n + 4 * t + i, last);
-        pos[i] = kpos != nullptr ? __ldg(kpos + slot) : slot;
+      for (int w = 0; w < KS / 2; ++w) dequant_k<DH>(rk, w, kf[2 * w], kf[2 * w + 1]);
+      if (st + 1 < steps && n + 64 < len) load_k<DH>(kc, ks, n + 64, last, g, t, rk);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int slot = min(n + g + 8 * j, last);
+        pos[j] = kpos != nullptr ? __ldg(kpos + slot) : slot;
       }
     }
     for (int ch = 0; ch < chunks; ++ch) {
       const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
       if (st == 0 || chunks > 1) {
         __syncthreads();
-        stage_rows<DH, F32>(a, b, hkv, m0, (rows + 15) & ~15, qs, par, kWarps);
+        stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
         __syncthreads();
       }
       if (!live) continue;
-      for (int mt = 0; mt * 16 < rows; ++mt) {
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      for (int nb = 0; nb * 8 < rows; ++nb) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int w = 0; w < KS / 2; ++w)
 #pragma unroll
           for (int p = 0; p < P; ++p) {
-            const uint4 q = qs[((mt * P + p) * KS + k) * 32 + lane];
-            mma_f16(s[0], &q.x, kf[0][k][0], kf[0][k][1]);
-            mma_f16(s[1], &q.x, kf[1][k][0], kf[1][k][1]);
+            const uint4 q = qs[((nb * P + p) * (KS / 2) + w) * 32 + lane];
+            mma_f16(s, kf[2 * w], q.x, q.y);
+            mma_f16(s, kf[2 * w + 1], q.z, q.w);
           }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const RowPar rp = par[mt * 16 + g + 8 * u];
+          const RowPar rp = par[nb * 8 + 2 * t + u];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x =
-                kv4_score<true>(a, s[i >> 1][2 * u + (i & 1)], rp.f, rp.slope, rp.qpos, pos[i]);
-            const bool see = n + 4 * t + i < len && pos[i] >= rp.lo && pos[i] < rp.hi &&
+          for (int j = 0; j < 2; ++j) {
+            const float x = kv4_score<true>(a, s[2 * j + u], rp.f, rp.slope, rp.qpos, pos[j]);
+            const bool see = n + g + 8 * j < len && pos[j] >= rp.lo && pos[j] < rp.hi &&
                              rp.lse != -INFINITY;
-            acc[i] += see ? exp2_approx((x - rp.lse) * kLog2e) : 0.f;
+            acc[j] += see ? exp2_approx((x - rp.lse) * kLog2e) : 0.f;
           }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 4);
-      acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 8);
-      acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+    for (int j = 0; j < 2; ++j) {
+      acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 1);
+      acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 2);
     }
-    if (g == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int slot = n + 4 * t + i;
-        if (slot < a.Ncache) w_out[slot] = (w_in != nullptr ? w_in[slot] : 0.f) + acc[i];
-      }
+    if (t < 2) {
+      const int slot = n + g + 8 * t;
+      if (slot < a.Ncache)
+        w_out[slot] = (w_in != nullptr ? w_in[slot] : 0.f) + (t == 0 ? acc[0] : acc[1]);
     }
   }
 }
 
 template <int DH, bool F32>
 cudaError_t launch_combine(const Kv4AttnArgs& a, cudaStream_t s) {
-  const long rows = (long)a.B * a.Hkv * a.M;
-  return launch_pdl(k_kv4_combine<DH, F32>, dim3((unsigned)ceil_div(rows * (DH / 4), 128)),
-                    dim3(128), 0, s, a);
+  return launch_pdl(k_kv4_combine<DH, F32>, dim3((unsigned)(a.B * a.Hkv * a.M)), dim3(128), 0, s,
+                    a);
 }
 
-template <int DH, int MT, bool F32>
+template <int DH, int NB, bool F32>
 cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
-  constexpr size_t q_bytes = (size_t)MT * (F32 ? 2 : 1) * (DH / 16) * 32 * 16;
-  constexpr size_t o_bytes = (size_t)kWarps * 16 * MT * DH * 4;
+  constexpr size_t q_bytes = (size_t)NB * (F32 ? 2 : 1) * (DH / 32) * 32 * 16;
+  constexpr size_t o_bytes = (size_t)kWarps * 8 * NB * DH * 4;
   constexpr size_t smem = q_bytes > o_bytes ? q_bytes : o_bytes;
-  auto kern = k_kv4_attn<DH, MT, F32>;
+  auto kern = k_kv4_attn<DH, NB, F32>;
   static bool attr_set = false;
   if (!attr_set && smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -558,7 +601,7 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
 
 template <int DH, bool F32>
 cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
-  constexpr size_t smem = (size_t)(kWRows / 16) * (F32 ? 2 : 1) * (DH / 16) * 32 * 16;
+  constexpr size_t smem = (size_t)(kWRows / 8) * (F32 ? 2 : 1) * (DH / 32) * 32 * 16;
   auto kern = k_kv4_weight<DH, F32>;
   static bool attr_set = false;
   if (!attr_set && smem > 48 * 1024) {
@@ -578,15 +621,15 @@ cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
 
 // The kernel, rows of a tile, tiles and shares of the slots for these sizes.
 struct AttnPlan {
-  bool tc;  // k_kv4_attn_tc: 256-row tiles; else k_kv4_attn with 16 mt rows
-  int mt, ntile, nsplit;
+  bool tc;  // k_kv4_attn_tc: 256-row tiles; else k_kv4_attn: 8 nb
+  int nb, ntile, nsplit;
 };
 AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   AttnPlan p;
   const int M = T * (Hq / Hkv);
   p.tc = dtype == PS_BF16 && dh <= 128 && M >= 64;
   if (p.tc) {
-    p.mt = 0;
+    p.nb = 0;
     p.ntile = ceil_div(M, 256);
     // rounds of CTAs (one an SM) times the steps of each, set-up and join
     // counted as four steps
@@ -603,8 +646,8 @@ AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
     }
     return p;
   }
-  p.mt = (M > 16 && dh <= 128) ? 2 : 1;
-  p.ntile = ceil_div(M, 16 * p.mt);
+  p.nb = M <= 8 ? 1 : M <= 16 || dh > 128 ? 2 : 4;
+  p.ntile = ceil_div(M, 8 * p.nb);
   const long base = (long)B * Hkv * p.ntile;
   const int most = ceil_div(N, 128);  // at least 128 slots a share
   long want = ceil_div(4 * kSmTarget, base);
@@ -647,14 +690,17 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
     if (e != cudaSuccess || a.nsplit == 1) return e;
     return a.dh == 64 ? launch_combine<64, false>(a, s) : launch_combine<128, false>(a, s);
   }
-#define PS_KV4_CASE(DH, MT)                                                          \
-  if (a.dh == DH && p.mt == MT)                                                      \
-    return f32 ? launch_attn<DH, MT, true>(a, s) : launch_attn<DH, MT, false>(a, s);
+#define PS_KV4_CASE(DH, NB)                                                          \
+  if (a.dh == DH && p.nb == NB)                                                      \
+    return f32 ? launch_attn<DH, NB, true>(a, s) : launch_attn<DH, NB, false>(a, s);
   PS_KV4_CASE(64, 1)
   PS_KV4_CASE(64, 2)
+  PS_KV4_CASE(64, 4)
   PS_KV4_CASE(128, 1)
   PS_KV4_CASE(128, 2)
+  PS_KV4_CASE(128, 4)
   PS_KV4_CASE(256, 1)
+  PS_KV4_CASE(256, 2)
 #undef PS_KV4_CASE
   return cudaErrorInvalidValue;
 }
