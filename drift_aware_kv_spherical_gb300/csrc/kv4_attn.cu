@@ -26,6 +26,7 @@
 // queries and P take two f16 terms (hi + lo).  P carries a factor 2^kPShift,
 // which keeps small weights out of f16's subnormals.
 #include "kv4.cuh"
+#include "tc.cuh"
 
 namespace ps {
 namespace {
@@ -91,9 +92,68 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
   }
 }
 
-// What a lane loads of a 16-slot step: K of slots g and g + 8, elements
-// [t dh/4, (t+1) dh/4); V of slots 2t, 2t+1, 2t+8, 2t+9, elements [g dh/8,
-// (g+1) dh/8); the block scales that go with them.
+// A warp's own ring of 16-slot steps in shared memory, filled with cp.async
+// well ahead of use: codes and scales as they lie in the cache.  (Loaded
+// straight into registers one step ahead, too few bytes were in flight: 90 us
+// against 54 with V left out, on 64 K slots x 8 sequences x 4 heads.)
+constexpr int kStages = 4;
+template <int DH, bool WITH_V>
+struct Ring {
+  static constexpr int kCode = 16 * (DH / 2), kScale = 16 * (DH / 16);
+  static constexpr int kV = kCode + kScale;            // V's codes, then its scales
+  static constexpr int kStage = WITH_V ? 2 * kV : kV;
+  static constexpr int kBytes = kStages * kStage;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in) {
+  const int n = in ? BYTES : 0;  // nothing read, zeros written
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+                 "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Slots [n, n + 16) of a head into the stage at dst; zeros past the cache.
+template <int DH, bool WITH_V>
+__device__ __forceinline__ void ring_fill(const Kv4AttnArgs& a, long bh, int n, uint32_t dst) {
+  using R = Ring<DH, WITH_V>;
+  const int lane = threadIdx.x & 31;
+  const long row = bh * a.Ncache + n;
+  const int left = a.Ncache - n;
+#pragma unroll
+  for (int i = 0; i < DH / 64; ++i) {
+    const int c = lane + 32 * i;  // 16-byte piece of the step's codes
+    const bool in = c / (DH / 32) < left;
+    const long off = in ? row * (DH / 2) + c * 16 : 0;
+    cp_async<16>(dst + c * 16, a.kcode + off, in);
+    if constexpr (WITH_V) cp_async<16>(dst + R::kV + c * 16, a.vcode + off, in);
+  }
+  const int r = lane & 15;
+  const bool in = r < left;
+  const long off = in ? (row + r) * (DH / 16) : 0;
+  if (WITH_V || lane < 16)
+    cp_async<DH / 16>(dst + R::kCode + (lane >= 16 ? R::kV : 0) + r * (DH / 16),
+                      (lane >= 16 ? a.vscale : a.kscale) + off, in);
+}
+
+// The slot that stands at index r of a 16-slot step: 0 4 1 5 2 6 3 7, and 8 more
+// for the second half.  Indices 2t, 2t+1, 2t+8, 2t+9 are then slots t, t+4, t+8,
+// t+12, so that the lanes of a V load read neighbouring rows (no bank is hit
+// twice).
+__device__ __forceinline__ int slot_at(int r) { return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1); }
+
+// What a lane reads of a stage: K of slots slot_at(g) and slot_at(g) + 8,
+// elements [t dh/4, (t+1) dh/4); V of slots t + 4 j, elements [g dh/8, (g+1)
+// dh/8); the block scales that go with them.
 template <int DH>
 struct RawK {
   uint32_t c[2][DH / 32];
@@ -106,49 +166,47 @@ struct RawV {
 };
 
 template <int DH>
-__device__ __forceinline__ void load_k(const uint8_t* kc, const uint8_t* ks, int n, int last,
-                                       int g, int t, RawK<DH>& o) {
+__device__ __forceinline__ void read_k(const uint8_t* st, int g, int t, RawK<DH>& o) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const long slot = min(n + g + 8 * j, last);
-    const uint8_t* p = kc + slot * (DH / 2) + t * (DH / 8);
-    const uint8_t* q = ks + slot * (DH / 16) + t * (DH / 64);
+    const int slot = slot_at(g) + 8 * j;
+    const uint8_t* p = st + slot * (DH / 2) + t * (DH / 8);
+    const uint8_t* q = st + 16 * (DH / 2) + slot * (DH / 16) + t * (DH / 64);
     if constexpr (DH == 64) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
       o.c[j][0] = v.x; o.c[j][1] = v.y;
-      o.s[j] = __ldg(q);
+      o.s[j] = *q;
     } else {
 #pragma unroll
       for (int i = 0; i < DH / 128; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
         o.c[j][4 * i] = v.x; o.c[j][4 * i + 1] = v.y;
         o.c[j][4 * i + 2] = v.z; o.c[j][4 * i + 3] = v.w;
       }
-      if constexpr (DH == 128) o.s[j] = __ldg(reinterpret_cast<const uint16_t*>(q));
-      else o.s[j] = __ldg(reinterpret_cast<const uint32_t*>(q));
+      if constexpr (DH == 128) o.s[j] = *reinterpret_cast<const uint16_t*>(q);
+      else o.s[j] = *reinterpret_cast<const uint32_t*>(q);
     }
   }
 }
 
 template <int DH>
-__device__ __forceinline__ void load_v(const uint8_t* vc, const uint8_t* vs, int n, int last,
-                                       int g, int t, RawV<DH>& o) {
+__device__ __forceinline__ void read_v(const uint8_t* st, int g, int t, RawV<DH>& o) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const long slot = min(n + 2 * t + (j & 1) + 4 * (j & 2), last);
-    const uint8_t* p = vc + slot * (DH / 2) + g * (DH / 16);
-    const uint8_t* q = vs + slot * (DH / 16);
+    const int slot = t + 4 * j;
+    const uint8_t* p = st + slot * (DH / 2) + g * (DH / 16);
+    const uint8_t* q = st + 16 * (DH / 2) + slot * (DH / 16);
     if constexpr (DH == 64) {
-      o.c[j][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-      o.s[j] = __ldg(q + (g >> 1));
+      o.c[j][0] = *reinterpret_cast<const uint32_t*>(p);
+      o.s[j] = q[g >> 1];
     } else if constexpr (DH == 128) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
       o.c[j][0] = v.x; o.c[j][1] = v.y;
-      o.s[j] = __ldg(q + g);
+      o.s[j] = q[g];
     } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
       o.c[j][0] = v.x; o.c[j][1] = v.y; o.c[j][2] = v.z; o.c[j][3] = v.w;
-      o.s[j] = __ldg(reinterpret_cast<const uint16_t*>(q) + g);
+      o.s[j] = reinterpret_cast<const uint16_t*>(q)[g];
     }
   }
 }
@@ -192,6 +250,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   constexpr int kRows = 8 * NB;
   pdl_prologue();
   extern __shared__ uint4 smem4[];
+  using R = Ring<DH, true>;
   uint4* qs = smem4;                               // NB * P * KS / 2 * 32
   float* obuf = reinterpret_cast<float*>(smem4);   // kWarps * kRows * DH, after the loop
   __shared__ RowPar par[kRows];
@@ -240,11 +299,9 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     return;
   }
 
-  const uint8_t* kc = a.kcode + (long)bh * a.Ncache * (DH / 2);
-  const uint8_t* ks = a.kscale + (long)bh * a.Ncache * (DH / 16);
-  const uint8_t* vc = a.vcode + (long)bh * a.Ncache * (DH / 2);
-  const uint8_t* vs = a.vscale + (long)bh * a.Ncache * (DH / 16);
   const int last = a.Ncache - 1;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(qs + NB * P * (KS / 2) * 32) + warp * R::kBytes;
+  const uint32_t ring32 = tc::smem_u32(ring);
 
   // O of rows 8 nb + 2 t + (c & 1), elements [g dh/8, (g+1) dh/8): element
   // 2 i + c / 2 in o[nb][i][c]
@@ -258,16 +315,28 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     mrow[nb][0] = mrow[nb][1] = -INFINITY;
     lrow[nb][0] = lrow[nb][1] = 0.f;
   }
-  RawK<DH> rk;
-  RawV<DH> rv;
-  int n = n_lo + 16 * warp;
-  if (n < n_hi) {
-    load_k<DH>(kc, ks, n, last, g, t, rk);
-    load_v<DH>(vc, vs, n, last, g, t, rv);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    const int n = n_lo + 16 * (warp + kWarps * i);
+    if (n < n_hi) ring_fill<DH, true>(a, bh, n, ring32 + i * R::kStage);
+    cp_commit();
   }
-  for (; n < n_hi; n += 16 * kWarps) {
-    const int next = min(n + 16 * kWarps, last);  // past the end: loaded, not used
-    // S^T: slots g and g + 8 (c / 2), rows 2 t and 2 t + 1 (c & 1) of block nb
+  const int sg = slot_at(g);
+  int stage = 0;
+  for (int n = n_lo + 16 * warp; n < n_hi; n += 16 * kWarps) {
+    cp_wait<kStages - 2>();
+    __syncwarp();  // the step has arrived, and the one before it has been read by every lane
+    {
+      const int ahead = n + 16 * kWarps * (kStages - 1);
+      const int to = stage == 0 ? kStages - 1 : stage - 1;
+      if (ahead < n_hi) ring_fill<DH, true>(a, bh, ahead, ring32 + to * R::kStage);
+      cp_commit();
+    }
+    const uint8_t* st = ring + stage * R::kStage;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    RawK<DH> rk;
+    read_k<DH>(st, g, t, rk);
+    // S^T: slots sg and sg + 8 (c / 2), rows 2 t and 2 t + 1 (c & 1) of block nb
     float s[NB][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -286,12 +355,11 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
           mma_f16(s[nb], a1, q.z, q.w);
         }
     }
-    load_k<DH>(kc, ks, next, last, g, t, rk);
     const bool masked = n < all_lo || n + 16 > all_hi;
     int pos[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int slot = min(n + g + 8 * j, last);
+      const int slot = min(n + sg + 8 * j, last);
       pos[j] = kpos != nullptr ? __ldg(kpos + slot) : slot;
     }
     uint32_t ph[NB][2], pl[NB][F32 ? 2 : 1];
@@ -305,7 +373,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float v = kv4_score<F32>(a, s[nb][2 * j + u], rp.f, rp.slope, rp.qpos, pos[j]) * kLog2e;
-          if (masked && (n + g + 8 * j >= len || pos[j] < rp.lo || pos[j] >= rp.hi)) v = -INFINITY;
+          if (masked && (n + sg + 8 * j >= len || pos[j] < rp.lo || pos[j] >= rp.hi)) v = -INFINITY;
           x[2 * j + u] = v;
         }
         grow |= fmaxf(x[u], x[2 + u]) > mrow[nb][u] + kGrow;
@@ -349,9 +417,11 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       }
     }
     // O^T += V^T P^T
+    RawV<DH> rv;
+    read_v<DH>(st + R::kV, g, t, rv);
 #pragma unroll
     for (int w = 0; w < DH / 64; ++w) {
-      uint32_t v[2][2][4];  // [even, odd element][slots 2t.., 2t + 8..][byte]
+      uint32_t v[2][2][4];  // [even, odd element][slots t and t + 4, t + 8 and t + 12][byte]
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t even, odd;
@@ -387,7 +457,6 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
         }
       }
     }
-    load_v<DH>(vc, vs, next, last, g, t, rv);
   }
 
   // the four warps' shares of each row joined
@@ -404,7 +473,8 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
         s_l[warp][nb * 8 + 2 * t + u] = l;
       }
     }
-  __syncthreads();  // Q is no longer read
+  cp_wait<0>();
+  __syncthreads();  // Q and the rings are no longer read
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -500,33 +570,49 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   constexpr int KS = DH / 16, P = F32 ? 2 : 1;
   pdl_prologue();
   extern __shared__ uint4 smem4[];
+  using R = Ring<DH, false>;
   uint4* qs = smem4;  // (kWRows / 8) * P * KS / 2 * 32
   __shared__ RowPar par[kWRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int bh = blockIdx.y, b = bh / a.Hkv, hkv = bh % a.Hkv;
   const int len = kv4_len(a, b), last = a.Ncache - 1;
-  const uint8_t* kc = a.kcode + (long)bh * a.Ncache * (DH / 2);
-  const uint8_t* ks = a.kscale + (long)bh * a.Ncache * (DH / 16);
   const int32_t* kpos = a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
   const float* w_in = a.w_in != nullptr ? a.w_in + (long)bh * a.Ncache : nullptr;
   float* w_out = a.w_out + (long)bh * a.Ncache;
   const int chunks = ceil_div(a.M, kWRows);
   const int n0 = (blockIdx.x * steps) * 64 + 16 * warp;
-  RawK<DH> rk;
-  if (n0 < len) load_k<DH>(kc, ks, n0, last, g, t, rk);
+  uint8_t* ring =
+      reinterpret_cast<uint8_t*>(qs + (kWRows / 8) * P * (KS / 2) * 32) + warp * R::kBytes;
+  const uint32_t ring32 = tc::smem_u32(ring);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < steps && n0 + 64 * i < len)
+      ring_fill<DH, false>(a, bh, n0 + 64 * i, ring32 + i * R::kStage);
+    cp_commit();
+  }
+  const int sg = slot_at(g);
   for (int st = 0; st < steps; ++st) {
     const int n = n0 + 64 * st;
     const bool live = n < len;  // warp-uniform
     uint32_t kf[KS][4];
     int pos[2];
-    float acc[2] = {0.f, 0.f};  // slots g and g + 8
+    float acc[2] = {0.f, 0.f};  // slots sg and sg + 8
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    {
+      const int ahead = st + kStages - 1;
+      if (ahead < steps && n0 + 64 * ahead < len)
+        ring_fill<DH, false>(a, bh, n0 + 64 * ahead, ring32 + ahead % kStages * R::kStage);
+      cp_commit();
+    }
     if (live) {
+      RawK<DH> rk;
+      read_k<DH>(ring + st % kStages * R::kStage, g, t, rk);
 #pragma unroll
       for (int w = 0; w < KS / 2; ++w) dequant_k<DH>(rk, w, kf[2 * w], kf[2 * w + 1]);
-      if (st + 1 < steps && n + 64 < len) load_k<DH>(kc, ks, n + 64, last, g, t, rk);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int slot = min(n + g + 8 * j, last);
+        const int slot = min(n + sg + 8 * j, last);
         pos[j] = kpos != nullptr ? __ldg(kpos + slot) : slot;
       }
     }
@@ -554,7 +640,7 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float x = kv4_score<true>(a, s[2 * j + u], rp.f, rp.slope, rp.qpos, pos[j]);
-            const bool see = n + g + 8 * j < len && pos[j] >= rp.lo && pos[j] < rp.hi &&
+            const bool see = n + sg + 8 * j < len && pos[j] >= rp.lo && pos[j] < rp.hi &&
                              rp.lse != -INFINITY;
             acc[j] += see ? exp2_approx((x - rp.lse) * kLog2e) : 0.f;
           }
@@ -567,7 +653,7 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
       acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 2);
     }
     if (t < 2) {
-      const int slot = n + g + 8 * t;
+      const int slot = n + sg + 8 * t;
       if (slot < a.Ncache)
         w_out[slot] = (w_in != nullptr ? w_in[slot] : 0.f) + (t == 0 ? acc[0] : acc[1]);
     }
@@ -582,7 +668,8 @@ cudaError_t launch_combine(const Kv4AttnArgs& a, cudaStream_t s) {
 
 template <int DH, int NB, bool F32>
 cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
-  constexpr size_t q_bytes = (size_t)NB * (F32 ? 2 : 1) * (DH / 32) * 32 * 16;
+  constexpr size_t q_bytes =
+      (size_t)NB * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, true>::kBytes;
   constexpr size_t o_bytes = (size_t)kWarps * 8 * NB * DH * 4;
   constexpr size_t smem = q_bytes > o_bytes ? q_bytes : o_bytes;
   auto kern = k_kv4_attn<DH, NB, F32>;
@@ -601,7 +688,8 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
 
 template <int DH, bool F32>
 cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
-  constexpr size_t smem = (size_t)(kWRows / 8) * (F32 ? 2 : 1) * (DH / 32) * 32 * 16;
+  constexpr size_t smem =
+      (size_t)(kWRows / 8) * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, false>::kBytes;
   auto kern = k_kv4_weight<DH, F32>;
   static bool attr_set = false;
   if (!attr_set && smem > 48 * 1024) {
@@ -650,7 +738,7 @@ AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   p.ntile = ceil_div(M, 8 * p.nb);
   const long base = (long)B * Hkv * p.ntile;
   const int most = ceil_div(N, 128);  // at least 128 slots a share
-  long want = ceil_div(4 * kSmTarget, base);
+  long want = ceil_div(6 * kSmTarget, base);
   if (want > most) want = most;
   if (want > 256) want = 256;
   p.nsplit = (int)(want < 1 ? 1 : want);
