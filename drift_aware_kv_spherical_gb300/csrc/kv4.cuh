@@ -101,12 +101,12 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 constexpr float kPShift = 10.f;  // log2 of the factor that P carries (times growth: < 2^16)
 
 // Per-row constants of a tile, in shared memory.
-struct RowPar {
+struct alignas(16) RowPar {
   float f;       // score of a raw product: natural units
+  float lse;     // k_kv4_weight; +inf past the last row
   float slope;   // distance bias
-  int lo, hi;    // visible positions
   int qpos;
-  float lse;     // k_kv4_weight
+  int lo, hi;    // visible positions
 };
 
 __device__ __forceinline__ int kv4_len(const Kv4AttnArgs& a, int b) {

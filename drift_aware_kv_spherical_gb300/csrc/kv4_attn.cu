@@ -46,7 +46,7 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
   for (int r = threadIdx.x / LN; r < rows; r += step) {
     const int m = m0 + r;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    RowPar p{0.f, 0.f, 0, 0, 0, -INFINITY};
+    RowPar p{0.f, INFINITY, 0.f, 0, 0, 0};
     if (m < a.M) {
       const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
       const long tok = (long)b * a.T + t;
@@ -70,7 +70,9 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
 #pragma unroll
     for (int o = LN / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, o));
     float up;
-    row_scale(mx, a.scale, &up, &p.f);
+    float f;
+    row_scale(mx, a.scale, &up, &f);
+    if (m < a.M) p.f = f;
     if (sub == 0) par[r] = p;
     // elements 8 sub .. 8 sub + 7: lane t = d / (DH / 4) of the fragment, steps
     // ks = d % (DH / 4) / 4 and the next, two pairs each
@@ -122,28 +124,57 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Slots [n, n + 16) of a head into the stage at dst; zeros past the cache.
+// Fills a lane's part of the stages, one 16-slot step after another `stride`
+// slots on: the pieces of codes lane, lane + 32, ...; K's scales of slot lane
+// (lanes 0-15), V's of slot lane - 16.  Zeros past the cache.
 template <int DH, bool WITH_V>
-__device__ __forceinline__ void ring_fill(const Kv4AttnArgs& a, long bh, int n, uint32_t dst) {
+struct RingFill {
   using R = Ring<DH, WITH_V>;
-  const int lane = threadIdx.x & 31;
-  const long row = bh * a.Ncache + n;
-  const int left = a.Ncache - n;
-#pragma unroll
-  for (int i = 0; i < DH / 64; ++i) {
-    const int c = lane + 32 * i;  // 16-byte piece of the step's codes
-    const bool in = c / (DH / 32) < left;
-    const long off = in ? row * (DH / 2) + c * 16 : 0;
-    cp_async<16>(dst + c * 16, a.kcode + off, in);
-    if constexpr (WITH_V) cp_async<16>(dst + R::kV + c * 16, a.vcode + off, in);
+  const uint8_t *kc, *vc, *sc;
+  uint32_t scale_at;
+  int left, piece, slot;
+
+  __device__ __forceinline__ RingFill(const Kv4AttnArgs& a, long bh, int n) {
+    const int lane = threadIdx.x & 31;
+    const long row = bh * a.Ncache + n;
+    slot = lane & 15;
+    piece = lane / (DH / 32);  // the slot of the lane's first piece
+    left = a.Ncache - n;
+    kc = a.kcode + row * (DH / 2) + lane * 16;
+    vc = a.vcode + row * (DH / 2) + lane * 16;
+    sc = (lane >= 16 ? a.vscale : a.kscale) + (row + slot) * (DH / 16);
+    scale_at = R::kCode + (lane >= 16 ? R::kV : 0) + slot * (DH / 16);
+    if (!WITH_V && lane >= 16) slot = 1 << 30;  // nothing to do
   }
-  const int r = lane & 15;
-  const bool in = r < left;
-  const long off = in ? (row + r) * (DH / 16) : 0;
-  if (WITH_V || lane < 16)
-    cp_async<DH / 16>(dst + R::kCode + (lane >= 16 ? R::kV : 0) + r * (DH / 16),
-                      (lane >= 16 ? a.vscale : a.kscale) + off, in);
-}
+  __device__ __forceinline__ void next(uint32_t dst, int stride) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t d = dst + lane * 16;
+    if (left >= 16) {  // warp-uniform
+#pragma unroll
+      for (int i = 0; i < DH / 64; ++i) {
+        cp_async<16>(d + 512 * i, kc + 512 * i, true);
+        if constexpr (WITH_V) cp_async<16>(d + R::kV + 512 * i, vc + 512 * i, true);
+      }
+      if (slot < 16) cp_async<DH / 16>(dst + scale_at, sc, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < DH / 64; ++i) {
+        const bool in = piece + i * (1024 / DH) < left;
+        cp_async<16>(d + 512 * i, in ? kc + 512 * i : kc - lane * 16, in);
+        if constexpr (WITH_V)
+          cp_async<16>(d + R::kV + 512 * i, in ? vc + 512 * i : vc - lane * 16, in);
+      }
+      if (slot < 16) {
+        const bool in = slot < left;
+        cp_async<DH / 16>(dst + scale_at, in ? sc : sc - slot * (DH / 16), in);
+      }
+    }
+    kc += (long)stride * (DH / 2);
+    if constexpr (WITH_V) vc += (long)stride * (DH / 2);
+    sc += (long)stride * (DH / 16);
+    left -= stride;
+  }
+};
 
 // The slot that stands at index r of a 16-slot step: 0 4 1 5 2 6 3 7, and 8 more
 // for the second half.  Indices 2t, 2t+1, 2t+8, 2t+9 are then slots t, t+4, t+8,
@@ -315,25 +346,38 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     mrow[nb][0] = mrow[nb][1] = -INFINITY;
     lrow[nb][0] = lrow[nb][1] = 0.f;
   }
+  // Row constants of the scores in log2 units: the factor of a raw product (of
+  // 2 score / cap where scores are capped), the maximum so far as what is
+  // subtracted and as what must not be passed.
+  float fa[NB][2], base[NB][2];
+  const float cap2 = a.cap * kLog2e;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      fa[nb][u] = par[nb * 8 + 2 * t + u].f *
+                  (F32 ? 1.f : a.cap > 0.f ? 2.f * kLog2e * a.inv_cap : kLog2e);
+      base[nb][u] = 0.f;
+    }
+  RingFill<DH, true> fill(a, bh, n_lo + 16 * warp);
+  int ahead = n_lo + 16 * warp;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    const int n = n_lo + 16 * (warp + kWarps * i);
-    if (n < n_hi) ring_fill<DH, true>(a, bh, n, ring32 + i * R::kStage);
+    if (ahead < n_hi) fill.next(ring32 + i * R::kStage, 16 * kWarps);
+    ahead += 16 * kWarps;
     cp_commit();
   }
   const int sg = slot_at(g);
-  int stage = 0;
+  uint32_t at = 0, to = (kStages - 1) * R::kStage;  // stage to read, stage to fill
   for (int n = n_lo + 16 * warp; n < n_hi; n += 16 * kWarps) {
     cp_wait<kStages - 2>();
     __syncwarp();  // the step has arrived, and the one before it has been read by every lane
-    {
-      const int ahead = n + 16 * kWarps * (kStages - 1);
-      const int to = stage == 0 ? kStages - 1 : stage - 1;
-      if (ahead < n_hi) ring_fill<DH, true>(a, bh, ahead, ring32 + to * R::kStage);
-      cp_commit();
-    }
-    const uint8_t* st = ring + stage * R::kStage;
-    stage = stage + 1 == kStages ? 0 : stage + 1;
+    if (ahead < n_hi) fill.next(ring32 + to, 16 * kWarps);
+    ahead += 16 * kWarps;
+    cp_commit();
+    const uint8_t* st = ring + at;
+    to = at;
+    at = at + R::kStage == R::kBytes ? 0 : at + R::kStage;
     RawK<DH> rk;
     read_k<DH>(st, g, t, rk);
     // S^T: slots sg and sg + 8 (c / 2), rows 2 t and 2 t + 1 (c & 1) of block nb
@@ -356,53 +400,65 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
         }
     }
     const bool masked = n < all_lo || n + 16 > all_hi;
-    int pos[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int slot = min(n + sg + 8 * j, last);
-      pos[j] = kpos != nullptr ? __ldg(kpos + slot) : slot;
+    int pos[2] = {n + sg, n + sg + 8};
+    if (kpos != nullptr) {
+      pos[0] = __ldg(kpos + min(pos[0], last));
+      pos[1] = __ldg(kpos + min(pos[1], last));
     }
     uint32_t ph[NB][2], pl[NB][F32 ? 2 : 1];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       float x[4];
-      bool grow = false;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {  // rows 2 t, 2 t + 1
-        const RowPar& rp = par[nb * 8 + 2 * t + u];
+      for (int c = 0; c < 4; ++c) {
+        const float raw = s[nb][c] * fa[nb][c & 1];
+        if constexpr (F32)
+          x[c] = (a.cap > 0.f ? a.cap * tanhf(raw * a.inv_cap) : raw) * kLog2e;
+        else  // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
+          x[c] = a.cap > 0.f ? fmaf(-2.f * cap2, rcp_approx(exp2_approx(raw) + 1.f), cap2) : raw;
+      }
+      if (a.slope != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v = kv4_score<F32>(a, s[nb][2 * j + u], rp.f, rp.slope, rp.qpos, pos[j]) * kLog2e;
-          if (masked && (n + sg + 8 * j >= len || pos[j] < rp.lo || pos[j] >= rp.hi)) v = -INFINITY;
-          x[2 * j + u] = v;
+        for (int c = 0; c < 4; ++c) {
+          const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
+          x[c] = fmaf(-rp.slope * kLog2e, fabsf((float)(rp.qpos - pos[c >> 1])), x[c]);
         }
-        grow |= fmaxf(x[u], x[2 + u]) > mrow[nb][u] + kGrow;
+      }
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
+          if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
+            x[c] = -INFINITY;
+        }
       }
       // The running maximum follows only when some row has outgrown it by
       // 2^kGrow; until then P carries a factor up to that.
-      if (__any_sync(0xffffffffu, grow)) {
+      const float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      if (__any_sync(0xffffffffu, top[0] > mrow[nb][0] + kGrow || top[1] > mrow[nb][1] + kGrow)) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float mx = fmaxf(x[u], x[2 + u]);
+          float mx = top[u];
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const bool up = mx > mrow[nb][u] + kGrow;
-          const float corr = up ? exp2_approx(mrow[nb][u] - mx) : 1.f;
-          if (up) mrow[nb][u] = mx;
-          lrow[nb][u] *= corr;
+          if (mx > mrow[nb][u] + kGrow) {
+            const float corr = exp2_approx(mrow[nb][u] - mx);
+            mrow[nb][u] = mx;
+            base[nb][u] = mx - kPShift;
+            lrow[nb][u] *= corr;
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[nb][i][u] *= corr;
-            o[nb][i][2 + u] *= corr;
+            for (int i = 0; i < MT; ++i) {
+              o[nb][i][u] *= corr;
+              o[nb][i][2 + u] *= corr;
+            }
           }
         }
       }
       float p[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float base = mrow[nb][c & 1] == -INFINITY ? 0.f : mrow[nb][c & 1] - kPShift;
-        p[c] = exp2_approx(x[c] - base);
+        p[c] = exp2_approx(x[c] - base[nb][c & 1]);
         lrow[nb][c & 1] += p[c];
       }
 #pragma unroll
@@ -584,46 +640,63 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   uint8_t* ring =
       reinterpret_cast<uint8_t*>(qs + (kWRows / 8) * P * (KS / 2) * 32) + warp * R::kBytes;
   const uint32_t ring32 = tc::smem_u32(ring);
+  RingFill<DH, false> fill(a, bh, n0);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if (i < steps && n0 + 64 * i < len)
-      ring_fill<DH, false>(a, bh, n0 + 64 * i, ring32 + i * R::kStage);
+    if (i < steps && n0 + 64 * i < len) fill.next(ring32 + i * R::kStage, 64);
     cp_commit();
   }
   const int sg = slot_at(g);
+  uint32_t at = 0, to = (kStages - 1) * R::kStage;  // stage to read, stage to fill
+  // slots that some row, that every row of the chunk in shared memory sees
+  int any_lo = 0, any_hi = len, all_lo = 0, all_hi = kpos != nullptr && a.span != nullptr ? -1 : len;
   for (int st = 0; st < steps; ++st) {
     const int n = n0 + 64 * st;
     const bool live = n < len;  // warp-uniform
     uint32_t kf[KS][4];
-    int pos[2];
+    int pos[2] = {n + sg, n + sg + 8};
     float acc[2] = {0.f, 0.f};  // slots sg and sg + 8
     cp_wait<kStages - 2>();
     __syncwarp();
-    {
-      const int ahead = st + kStages - 1;
-      if (ahead < steps && n0 + 64 * ahead < len)
-        ring_fill<DH, false>(a, bh, n0 + 64 * ahead, ring32 + ahead % kStages * R::kStage);
-      cp_commit();
-    }
+    if (st + kStages - 1 < steps && n + 64 * (kStages - 1) < len) fill.next(ring32 + to, 64);
+    cp_commit();
     if (live) {
       RawK<DH> rk;
-      read_k<DH>(ring + st % kStages * R::kStage, g, t, rk);
+      read_k<DH>(ring + at, g, t, rk);
 #pragma unroll
       for (int w = 0; w < KS / 2; ++w) dequant_k<DH>(rk, w, kf[2 * w], kf[2 * w + 1]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int slot = min(n + sg + 8 * j, last);
-        pos[j] = kpos != nullptr ? __ldg(kpos + slot) : slot;
+      if (kpos != nullptr) {
+        pos[0] = __ldg(kpos + min(pos[0], last));
+        pos[1] = __ldg(kpos + min(pos[1], last));
       }
     }
+    to = at;
+    at = at + R::kStage == R::kBytes ? 0 : at + R::kStage;
     for (int ch = 0; ch < chunks; ++ch) {
       const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
       if (st == 0 || chunks > 1) {
         __syncthreads();
         stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
         __syncthreads();
+        if (a.span != nullptr && kpos == nullptr) {
+          int lo = INT32_MAX, hi = INT32_MIN, lo_all = INT32_MIN, hi_all = INT32_MAX;
+          for (int r = lane; r < rows; r += 32) {
+            const int x = par[r].lo, y = par[r].hi;
+            if (x < y) {
+              lo = min(lo, x);
+              hi = max(hi, y);
+            }
+            lo_all = max(lo_all, x);
+            hi_all = min(hi_all, y);
+          }
+          any_lo = __reduce_min_sync(0xffffffffu, lo);
+          any_hi = __reduce_max_sync(0xffffffffu, hi);
+          all_lo = __reduce_max_sync(0xffffffffu, lo_all);
+          all_hi = min(len, __reduce_min_sync(0xffffffffu, hi_all));
+        }
       }
-      if (!live) continue;
+      if (!live || n >= any_hi || n + 16 <= any_lo) continue;
+      const bool masked = n < all_lo || n + 16 > all_hi;
       for (int nb = 0; nb * 8 < rows; ++nb) {
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -636,13 +709,17 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
           }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const RowPar rp = par[nb * 8 + 2 * t + u];
+          const RowPar& rp = par[nb * 8 + 2 * t + u];
+          const float f = rp.f, lse = rp.lse;
+          float x[2];  // score - lse
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float x = kv4_score<true>(a, s[2 * j + u], rp.f, rp.slope, rp.qpos, pos[j]);
-            const bool see = n + sg + 8 * j < len && pos[j] >= rp.lo && pos[j] < rp.hi &&
-                             rp.lse != -INFINITY;
-            acc[j] += see ? exp2_approx((x - rp.lse) * kLog2e) : 0.f;
+            x[j] = fmaf(s[2 * j + u], f, -lse);
+            if (a.cap > 0.f) x[j] = fmaf(a.cap, tanhf(s[2 * j + u] * f * a.inv_cap), -lse);
+            if (a.slope != nullptr) x[j] = fmaf(-rp.slope, fabsf((float)(rp.qpos - pos[j])), x[j]);
+            if (masked && (n + sg + 8 * j >= len || pos[j] < rp.lo || pos[j] >= rp.hi))
+              x[j] = -INFINITY;
+            acc[j] += exp2_approx(x[j] * kLog2e);
           }
         }
       }
@@ -715,7 +792,7 @@ struct AttnPlan {
 AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   AttnPlan p;
   const int M = T * (Hq / Hkv);
-  p.tc = dtype == PS_BF16 && dh <= 128 && M >= 64;
+  p.tc = dtype == PS_BF16 && dh <= 128 && M >= 24;
   if (p.tc) {
     p.nb = 0;
     p.ntile = ceil_div(M, 256);
