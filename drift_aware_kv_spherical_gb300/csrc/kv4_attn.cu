@@ -33,7 +33,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kGrow = 4.f;  // log2 growth of a maximum before O is rescaled
+constexpr float kGrow = 4.f;      // log2 growth of a maximum before O is rescaled
+constexpr float kNoMax = -1e30f;  // a maximum that every score outgrows
 // Rows [m0, m0 + rows) of (b, hkv) into shared memory as B fragments
 // [row / 8][part][ks / 2][lane] (uint4: two steps' pairs), with their constants;
 // rows past M are zero and see nothing.  DH / 8 lanes a row, every load of a
@@ -274,8 +275,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-template <int DH, int NB, bool F32>
-__global__ void __launch_bounds__(kThreads)
+// GEN: a distance bias or explicit positions.
+template <int DH, int NB, bool F32, bool GEN>
+__global__ void __launch_bounds__(kThreads, DH <= 128 && NB == 1 && !F32 ? 5 : 1)
 k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   constexpr int KS = DH / 16, MT = DH / 16, P = F32 ? 2 : 1;  // QK steps; O tiles of 16 elements
   constexpr int kRows = 8 * NB;
@@ -298,7 +300,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   __syncthreads();
   // positions that some row sees, and that every row sees
   int n_lo = 0, n_hi = len, all_lo = 0, all_hi = len;
-  const int32_t* kpos = a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
+  const int32_t* kpos = GEN && a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
   if (kpos != nullptr) {
     if (a.span != nullptr) all_hi = -1;
   } else if (a.span != nullptr) {  // slots are positions: skip what no row sees
@@ -335,30 +337,26 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   const uint32_t ring32 = tc::smem_u32(ring);
 
   // O of rows 8 nb + 2 t + (c & 1), elements [g dh/8, (g+1) dh/8): element
-  // 2 i + c / 2 in o[nb][i][c]
-  float o[NB][MT][4], mrow[NB][2], lrow[NB][2];
+  // 2 i + c / 2 in o[nb][i][c].  Scores are in log2 units: a raw product times
+  // fa (of 2 score / cap where scores are capped); `base` is subtracted, the
+  // maximum so far less kPShift.
+  float o[NB][MT][4], fa[NB][2], base[NB][2], lrow[NB][2];
+  const float cap2 = a.cap * kLog2e;
+  const bool capped = a.cap > 0.f;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[nb][i][c] = 0.f;
-    mrow[nb][0] = mrow[nb][1] = -INFINITY;
-    lrow[nb][0] = lrow[nb][1] = 0.f;
-  }
-  // Row constants of the scores in log2 units: the factor of a raw product (of
-  // 2 score / cap where scores are capped), the maximum so far as what is
-  // subtracted and as what must not be passed.
-  float fa[NB][2], base[NB][2];
-  const float cap2 = a.cap * kLog2e;
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      fa[nb][u] = par[nb * 8 + 2 * t + u].f *
-                  (F32 ? 1.f : a.cap > 0.f ? 2.f * kLog2e * a.inv_cap : kLog2e);
-      base[nb][u] = 0.f;
+      fa[nb][u] =
+          par[nb * 8 + 2 * t + u].f * (F32 ? 1.f : capped ? 2.f * kLog2e * a.inv_cap : kLog2e);
+      base[nb][u] = kNoMax;
+      lrow[nb][u] = 0.f;
     }
+  }
   RingFill<DH, true> fill(a, bh, n_lo + 16 * warp);
   int ahead = n_lo + 16 * warp;
 #pragma unroll
@@ -401,51 +399,63 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     }
     const bool masked = n < all_lo || n + 16 > all_hi;
     int pos[2] = {n + sg, n + sg + 8};
-    if (kpos != nullptr) {
+    if (GEN && kpos != nullptr) {
       pos[0] = __ldg(kpos + min(pos[0], last));
       pos[1] = __ldg(kpos + min(pos[1], last));
     }
     uint32_t ph[NB][2], pl[NB][F32 ? 2 : 1];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
+      // the four scores less sub
+      auto scores = [&](const float* sub, float* x) {
+        if (F32) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float raw = s[nb][c] * fa[nb][c & 1];
+            x[c] = fmaf(capped ? a.cap * tanhf(raw * a.inv_cap) : raw, kLog2e, -sub[c & 1]);
+          }
+        } else if (capped) {  // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            x[c] = fmaf(-2.f * cap2, rcp_approx(exp2_approx(s[nb][c] * fa[nb][c & 1]) + 1.f),
+                        cap2 - sub[c & 1]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = fmaf(s[nb][c], fa[nb][c & 1], -sub[c & 1]);
+        }
+        if (GEN && a.slope != nullptr) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
+            x[c] = fmaf(-rp.slope * kLog2e, fabsf((float)(rp.qpos - pos[c >> 1])), x[c]);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
+            if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
+              x[c] = -INFINITY;
+          }
+        }
+      };
       float x[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float raw = s[nb][c] * fa[nb][c & 1];
-        if constexpr (F32)
-          x[c] = (a.cap > 0.f ? a.cap * tanhf(raw * a.inv_cap) : raw) * kLog2e;
-        else  // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
-          x[c] = a.cap > 0.f ? fmaf(-2.f * cap2, rcp_approx(exp2_approx(raw) + 1.f), cap2) : raw;
-      }
-      if (a.slope != nullptr) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
-          x[c] = fmaf(-rp.slope * kLog2e, fabsf((float)(rp.qpos - pos[c >> 1])), x[c]);
-        }
-      }
-      if (masked) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
-          if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
-            x[c] = -INFINITY;
-        }
-      }
+      scores(base[nb], x);
       // The running maximum follows only when some row has outgrown it by
       // 2^kGrow; until then P carries a factor up to that.
-      const float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-      if (__any_sync(0xffffffffu, top[0] > mrow[nb][0] + kGrow || top[1] > mrow[nb][1] + kGrow)) {
+      if (__any_sync(0xffffffffu,
+                     fmaxf(fmaxf(x[0], x[2]), fmaxf(x[1], x[3])) > kPShift + kGrow)) {
+        const float zero[2] = {0.f, 0.f};
+        scores(zero, x);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float mx = top[u];
+          float mx = fmaxf(x[u], x[2 + u]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (mx > mrow[nb][u] + kGrow) {
-            const float corr = exp2_approx(mrow[nb][u] - mx);
-            mrow[nb][u] = mx;
-            base[nb][u] = mx - kPShift;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) - kPShift;
+          if (mx > base[nb][u] + kGrow) {
+            const float corr = exp2_approx(base[nb][u] - mx);
+            base[nb][u] = mx;
             lrow[nb][u] *= corr;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -453,12 +463,14 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
               o[nb][i][2 + u] *= corr;
             }
           }
+          x[u] -= base[nb][u];
+          x[2 + u] -= base[nb][u];
         }
       }
       float p[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        p[c] = exp2_approx(x[c] - base[nb][c & 1]);
+        p[c] = exp2_approx(x[c]);
         lrow[nb][c & 1] += p[c];
       }
 #pragma unroll
@@ -525,7 +537,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       if (g == 0) {
-        s_m[warp][nb * 8 + 2 * t + u] = mrow[nb][u];
+        s_m[warp][nb * 8 + 2 * t + u] = base[nb][u] == kNoMax ? -INFINITY : base[nb][u] + kPShift;
         s_l[warp][nb * 8 + 2 * t + u] = l;
       }
     }
@@ -620,7 +632,8 @@ k_kv4_combine(const __grid_constant__ Kv4AttnArgs a) {
 // on timing.
 constexpr int kWRows = 64;
 
-template <int DH, bool F32>
+// GEN: capped scores, a distance bias or explicit positions.
+template <int DH, bool F32, bool GEN>
 __global__ void __launch_bounds__(kThreads)
 k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   constexpr int KS = DH / 16, P = F32 ? 2 : 1;
@@ -632,7 +645,7 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int bh = blockIdx.y, b = bh / a.Hkv, hkv = bh % a.Hkv;
   const int len = kv4_len(a, b), last = a.Ncache - 1;
-  const int32_t* kpos = a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
+  const int32_t* kpos = GEN && a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
   const float* w_in = a.w_in != nullptr ? a.w_in + (long)bh * a.Ncache : nullptr;
   float* w_out = a.w_out + (long)bh * a.Ncache;
   const int chunks = ceil_div(a.M, kWRows);
@@ -656,6 +669,9 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
     uint32_t kf[KS][4];
     int pos[2] = {n + sg, n + sg + 8};
     float acc[2] = {0.f, 0.f};  // slots sg and sg + 8
+    // the slot that this lane writes, and what is there: asked for early
+    const int mine = t < 2 ? n + sg + 8 * t : INT32_MAX;
+    const float w_old = w_in != nullptr && mine < a.Ncache ? w_in[mine] : 0.f;
     cp_wait<kStages - 2>();
     __syncwarp();
     if (st + kStages - 1 < steps && n + 64 * (kStages - 1) < len) fill.next(ring32 + to, 64);
@@ -665,7 +681,7 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
       read_k<DH>(ring + at, g, t, rk);
 #pragma unroll
       for (int w = 0; w < KS / 2; ++w) dequant_k<DH>(rk, w, kf[2 * w], kf[2 * w + 1]);
-      if (kpos != nullptr) {
+      if (GEN && kpos != nullptr) {
         pos[0] = __ldg(kpos + min(pos[0], last));
         pos[1] = __ldg(kpos + min(pos[1], last));
       }
@@ -707,21 +723,37 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
             mma_f16(s, kf[2 * w], q.x, q.y);
             mma_f16(s, kf[2 * w + 1], q.z, q.w);
           }
+        const RowPar& r0 = par[nb * 8 + 2 * t];
+        const RowPar& r1 = par[nb * 8 + 2 * t + 1];
+        // score - lse of slots sg, sg + 8 (c / 2), rows 2 t, 2 t + 1 (c & 1)
+        float x[4];
+        if (GEN && a.cap > 0.f) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const RowPar& rp = par[nb * 8 + 2 * t + u];
-          const float f = rp.f, lse = rp.lse;
-          float x[2];  // score - lse
+          for (int c = 0; c < 4; ++c) {
+            const RowPar& rp = c & 1 ? r1 : r0;
+            x[c] = fmaf(a.cap, tanhf(s[c] * rp.f * a.inv_cap), -rp.lse);
+          }
+        } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            x[j] = fmaf(s[2 * j + u], f, -lse);
-            if (a.cap > 0.f) x[j] = fmaf(a.cap, tanhf(s[2 * j + u] * f * a.inv_cap), -lse);
-            if (a.slope != nullptr) x[j] = fmaf(-rp.slope, fabsf((float)(rp.qpos - pos[j])), x[j]);
-            if (masked && (n + sg + 8 * j >= len || pos[j] < rp.lo || pos[j] >= rp.hi))
-              x[j] = -INFINITY;
-            acc[j] += exp2_approx(x[j] * kLog2e);
+          for (int c = 0; c < 4; ++c) x[c] = fmaf(s[c], c & 1 ? r1.f : r0.f, -(c & 1 ? r1 : r0).lse);
+        }
+        if (GEN && a.slope != nullptr) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const RowPar& rp = c & 1 ? r1 : r0;
+            x[c] = fmaf(-rp.slope, fabsf((float)(rp.qpos - pos[c >> 1])), x[c]);
           }
         }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const RowPar& rp = c & 1 ? r1 : r0;
+            if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
+              x[c] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c >> 1] += exp2_approx(x[c] * kLog2e);
       }
     }
 #pragma unroll
@@ -729,11 +761,7 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
       acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 1);
       acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 2);
     }
-    if (t < 2) {
-      const int slot = n + sg + 8 * t;
-      if (slot < a.Ncache)
-        w_out[slot] = (w_in != nullptr ? w_in[slot] : 0.f) + (t == 0 ? acc[0] : acc[1]);
-    }
+    if (mine < a.Ncache) w_out[mine] = w_old + (t == 0 ? acc[0] : acc[1]);
   }
 }
 
@@ -743,13 +771,13 @@ cudaError_t launch_combine(const Kv4AttnArgs& a, cudaStream_t s) {
                     a);
 }
 
-template <int DH, int NB, bool F32>
+template <int DH, int NB, bool F32, bool GEN>
 cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t q_bytes =
       (size_t)NB * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, true>::kBytes;
   constexpr size_t o_bytes = (size_t)kWarps * 8 * NB * DH * 4;
   constexpr size_t smem = q_bytes > o_bytes ? q_bytes : o_bytes;
-  auto kern = k_kv4_attn<DH, NB, F32>;
+  auto kern = k_kv4_attn<DH, NB, F32, GEN>;
   static bool attr_set = false;
   if (!attr_set && smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -763,11 +791,11 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   return launch_combine<DH, F32>(a, s);
 }
 
-template <int DH, bool F32>
+template <int DH, bool F32, bool GEN>
 cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem =
       (size_t)(kWRows / 8) * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, false>::kBytes;
-  auto kern = k_kv4_weight<DH, F32>;
+  auto kern = k_kv4_weight<DH, F32, GEN>;
   static bool attr_set = false;
   if (!attr_set && smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -792,7 +820,7 @@ struct AttnPlan {
 AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   AttnPlan p;
   const int M = T * (Hq / Hkv);
-  p.tc = dtype == PS_BF16 && dh <= 128 && M >= 24;
+  p.tc = dtype == PS_BF16 && dh <= 128 && M > 16;
   if (p.tc) {
     p.nb = 0;
     p.ntile = ceil_div(M, 256);
@@ -855,28 +883,38 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
     if (e != cudaSuccess || a.nsplit == 1) return e;
     return a.dh == 64 ? launch_combine<64, false>(a, s) : launch_combine<128, false>(a, s);
   }
-#define PS_KV4_CASE(DH, NB)                                                          \
-  if (a.dh == DH && p.nb == NB)                                                      \
-    return f32 ? launch_attn<DH, NB, true>(a, s) : launch_attn<DH, NB, false>(a, s);
+  const bool gen = a.slope != nullptr || a.kpos != nullptr;
+#define PS_KV4_CASE(DH, NB)                                           \
+  if (a.dh == DH && p.nb == NB) {                                     \
+    if (f32) return launch_attn<DH, NB, true, true>(a, s);            \
+    return gen ? launch_attn<DH, NB, false, true>(a, s)               \
+               : launch_attn<DH, NB, false, false>(a, s);             \
+  }
   PS_KV4_CASE(64, 1)
   PS_KV4_CASE(64, 2)
-  PS_KV4_CASE(64, 4)
   PS_KV4_CASE(128, 1)
   PS_KV4_CASE(128, 2)
-  PS_KV4_CASE(128, 4)
   PS_KV4_CASE(256, 1)
   PS_KV4_CASE(256, 2)
 #undef PS_KV4_CASE
+  // 32 rows: fp32 queries only, bf16 ones are on the tcgen05 kernel by then
+  if (a.dh == 64 && p.nb == 4 && f32) return launch_attn<64, 4, true, true>(a, s);
+  if (a.dh == 128 && p.nb == 4 && f32) return launch_attn<128, 4, true, true>(a, s);
   return cudaErrorInvalidValue;
 }
 
 cudaError_t kv4_weight_run(const Kv4AttnArgs& a, cudaStream_t s) {
-  const bool f32 = a.dtype == PS_F32;
-  switch (a.dh) {
-    case 64: return f32 ? launch_weight<64, true>(a, s) : launch_weight<64, false>(a, s);
-    case 128: return f32 ? launch_weight<128, true>(a, s) : launch_weight<128, false>(a, s);
-    case 256: return f32 ? launch_weight<256, true>(a, s) : launch_weight<256, false>(a, s);
+  const bool gen = a.cap > 0.f || a.slope != nullptr || a.kpos != nullptr;
+#define PS_KV4_CASE(DH)                                                      \
+  if (a.dh == DH) {                                                          \
+    if (a.dtype == PS_F32) return launch_weight<DH, true, true>(a, s);       \
+    return gen ? launch_weight<DH, false, true>(a, s)                        \
+               : launch_weight<DH, false, false>(a, s);                      \
   }
+  PS_KV4_CASE(64)
+  PS_KV4_CASE(128)
+  PS_KV4_CASE(256)
+#undef PS_KV4_CASE
   return cudaErrorInvalidValue;
 }
 
