@@ -511,7 +511,7 @@ namespace {
 
 // The shape, pointers and tensor scales of a cache.
 ps_status check_kv4(const ps_kv4_cache* c) {
-  PS_REQUIRE(c != nullptr && c->B >= 0 && c->Hkv >= 1 && c->Ncache >= 1 && kv4_dh_ok(c->dh));
+  PS_REQUIRE(c != nullptr && c->B >= 0 && c->Hkv >= 1 && c->Hkv <= 512 && c->Ncache >= 1 && kv4_dh_ok(c->dh));
   PS_REQUIRE(c->B <= 65535 && (long)c->B * c->Hkv <= 65535);
   PS_REQUIRE(std::isnormal(c->kmul) && c->kmul > 0.f && std::isnormal(c->vmul) && c->vmul > 0.f);
   if (c->B > 0) {
@@ -533,10 +533,10 @@ ps_status kv4_rows(ps_handle h, const ps_kv4_cache* c, const void* K, const void
   if (st != PS_OK) return st;
   if (c->B == 0 || R == 0) return PS_OK;
   PS_REQUIRE(ld_ok(ld, (long)c->Hkv * c->dh, dtype));
-  PS_REQUIRE((long)R * c->Hkv <= INT32_MAX);
+  PS_REQUIRE((long)R * c->Hkv <= (1 << 30));
   PS_PTR(K); PS_PTR(V);
   Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)ld, off, rows, cnt,
-                c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul};
+                c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul, 0};
   return launch_status(kv4_rows_run(a, load, static_cast<cudaStream_t>(stream)));
 }
 

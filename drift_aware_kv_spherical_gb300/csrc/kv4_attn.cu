@@ -662,16 +662,45 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   const int sg = slot_at(g);
   uint32_t at = 0, to = (kStages - 1) * R::kStage;  // stage to read, stage to fill
   // slots that some row, that every row of the chunk in shared memory sees
-  int any_lo = 0, any_hi = len, all_lo = 0, all_hi = kpos != nullptr && a.span != nullptr ? -1 : len;
-  for (int st = 0; st < steps; ++st) {
-    const int n = n0 + 64 * st;
+  int any_lo = 0, any_hi = len, all_lo = 0, all_hi = GEN && kpos != nullptr && a.span != nullptr ? -1 : len;
+  auto stage = [&](int ch) {
+    const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
+    __syncthreads();
+    stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
+    __syncthreads();
+    if (a.span != nullptr && kpos == nullptr) {
+      int lo = INT32_MAX, hi = INT32_MIN, lo_all = INT32_MIN, hi_all = INT32_MAX;
+      for (int r = lane; r < rows; r += 32) {
+        const int x = par[r].lo, y = par[r].hi;
+        if (x < y) {
+          lo = min(lo, x);
+          hi = max(hi, y);
+        }
+        lo_all = max(lo_all, x);
+        hi_all = min(hi_all, y);
+      }
+      any_lo = __reduce_min_sync(0xffffffffu, lo);
+      any_hi = __reduce_max_sync(0xffffffffu, hi);
+      all_lo = __reduce_max_sync(0xffffffffu, lo_all);
+      all_hi = min(len, __reduce_min_sync(0xffffffffu, hi_all));
+    }
+    return ceil_div(rows, 8);
+  };
+  int nbs = 0;
+  if (chunks == 1) nbs = stage(0);
+  // the slot that this lane writes
+  int mine = t < 2 ? n0 + sg + 8 * t : INT32_MAX;
+  int n = n0;
+  for (int st = 0; st < steps; ++st, n += 64, mine += t < 2 ? 64 : 0) {
     const bool live = n < len;  // warp-uniform
+    if (chunks == 1 && !live) {
+      if (mine < a.Ncache) w_out[mine] = w_in != nullptr ? w_in[mine] : 0.f;
+      continue;
+    }
     uint32_t kf[KS][4];
     int pos[2] = {n + sg, n + sg + 8};
     float acc[2] = {0.f, 0.f};  // slots sg and sg + 8
-    // the slot that this lane writes, and what is there: asked for early
-    const int mine = t < 2 ? n + sg + 8 * t : INT32_MAX;
-    const float w_old = w_in != nullptr && mine < a.Ncache ? w_in[mine] : 0.f;
+    const float w_old = w_in != nullptr && mine < a.Ncache ? w_in[mine] : 0.f;  // asked for early
     cp_wait<kStages - 2>();
     __syncwarp();
     if (st + kStages - 1 < steps && n + 64 * (kStages - 1) < len) fill.next(ring32 + to, 64);
@@ -689,42 +718,24 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
     to = at;
     at = at + R::kStage == R::kBytes ? 0 : at + R::kStage;
     for (int ch = 0; ch < chunks; ++ch) {
-      const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
-      if (st == 0 || chunks > 1) {
-        __syncthreads();
-        stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
-        __syncthreads();
-        if (a.span != nullptr && kpos == nullptr) {
-          int lo = INT32_MAX, hi = INT32_MIN, lo_all = INT32_MIN, hi_all = INT32_MAX;
-          for (int r = lane; r < rows; r += 32) {
-            const int x = par[r].lo, y = par[r].hi;
-            if (x < y) {
-              lo = min(lo, x);
-              hi = max(hi, y);
-            }
-            lo_all = max(lo_all, x);
-            hi_all = min(hi_all, y);
-          }
-          any_lo = __reduce_min_sync(0xffffffffu, lo);
-          any_hi = __reduce_max_sync(0xffffffffu, hi);
-          all_lo = __reduce_max_sync(0xffffffffu, lo_all);
-          all_hi = min(len, __reduce_min_sync(0xffffffffu, hi_all));
-        }
-      }
+      if (chunks > 1) nbs = stage(ch);
       if (!live || n >= any_hi || n + 16 <= any_lo) continue;
       const bool masked = n < all_lo || n + 16 > all_hi;
-      for (int nb = 0; nb * 8 < rows; ++nb) {
+      const uint4* qp = qs + lane;
+      const RowPar* rp0 = par + 2 * t;
+#pragma unroll 1
+      for (int nb = 0; nb < nbs; ++nb, qp += P * (KS / 2) * 32, rp0 += 8) {
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < KS / 2; ++w)
 #pragma unroll
           for (int p = 0; p < P; ++p) {
-            const uint4 q = qs[((nb * P + p) * (KS / 2) + w) * 32 + lane];
+            const uint4 q = qp[(p * (KS / 2) + w) * 32];
             mma_f16(s, kf[2 * w], q.x, q.y);
             mma_f16(s, kf[2 * w + 1], q.z, q.w);
           }
-        const RowPar& r0 = par[nb * 8 + 2 * t];
-        const RowPar& r1 = par[nb * 8 + 2 * t + 1];
+        const RowPar& r0 = rp0[0];
+        const RowPar& r1 = rp0[1];
         // score - lse of slots sg, sg + 8 (c / 2), rows 2 t, 2 t + 1 (c & 1)
         float x[4];
         if (GEN && a.cap > 0.f) {
@@ -734,8 +745,11 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
             x[c] = fmaf(a.cap, tanhf(s[c] * rp.f * a.inv_cap), -rp.lse);
           }
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = fmaf(s[c], c & 1 ? r1.f : r0.f, -(c & 1 ? r1 : r0).lse);
+          const float f0 = r0.f, l0 = -r0.lse, f1 = r1.f, l1 = -r1.lse;
+          x[0] = fmaf(s[0], f0, l0);
+          x[1] = fmaf(s[1], f1, l1);
+          x[2] = fmaf(s[2], f0, l0);
+          x[3] = fmaf(s[3], f1, l1);
         }
         if (GEN && a.slope != nullptr) {
 #pragma unroll
@@ -763,6 +777,7 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
     }
     if (mine < a.Ncache) w_out[mine] = w_old + (t == 0 ? acc[0] : acc[1]);
   }
+  cp_wait<0>();  // no copy is under way when the CTA leaves
 }
 
 template <int DH, bool F32>
@@ -803,11 +818,14 @@ cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  // rows that fit shared memory are staged once for several 64-slot groups
+  // rows that fit shared memory are staged once for all the 64-slot groups of
+  // a CTA, as many as leave six CTAs an SM
   const int groups = ceil_div(a.Ncache, 64);
   int steps = 1;
-  if (a.M <= kWRows)
-    while (steps < 8 && (long)ceil_div(groups, 2 * steps) * a.B * a.Hkv >= 8 * kSmTarget) steps *= 2;
+  if (a.M <= kWRows) {
+    steps = (int)((long)groups * a.B * a.Hkv / (6 * kSmTarget));
+    steps = steps < 1 ? 1 : steps > 64 ? 64 : steps;
+  }
   return launch_pdl(kern, dim3((unsigned)ceil_div(groups, steps), a.B * a.Hkv), dim3(kThreads),
                     smem, s, a, steps);
 }

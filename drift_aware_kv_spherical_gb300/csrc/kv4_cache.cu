@@ -5,10 +5,9 @@
 //
 // A lane owns one 16-element block of K and the same block of V: their scale,
 // eight code bytes and 64 input bytes (bf16) need no other lane.  A warp takes
-// 32 / (dh / 16) consecutive list entries of one head, so its scale bytes fill
-// whole 32-byte sectors where the entries are consecutive slots, and
-// consecutive warps take the heads of the same entries, whose input is
-// contiguous.
+// 512 / dh consecutive list entries of one head, so its scale bytes fill whole
+// 32-byte sectors where the entries are consecutive slots, and consecutive
+// warps take the heads of the same entries, whose input is contiguous.
 #include "kv4.cuh"
 
 namespace ps {
@@ -55,50 +54,93 @@ __device__ __forceinline__ void dequant_block(uint2 c, uint32_t sc, float mul, f
   }
 }
 
+// The codes of x[0..15] / den.  fl(x / den) by Markstein's theorem: with y =
+// RN(1 / den), q = RN(x y) and the exact remainder r = x - q den, RN(q + r y) is
+// the correctly rounded quotient while nothing over- or underflows.  Three
+// instructions, no branch: bf16 rows hit E2M1's ties exactly so often (x and den
+// have few bits) that a fast path which detects them took its slow one in every
+// warp.
+__device__ __forceinline__ uint2 codes16(const float* x, float den, float y) {
+  float q[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float q0 = __fmul_rn(x[e], y);
+    q[e] = __fmaf_rn(__fmaf_rn(-q0, den, x[e]), y, q0);
+  }
+  return make_uint2(e2m1x8(q), e2m1x8(q + 8));
+}
+
+// One block with the tensor scale S: its codes and scale.
+__device__ __forceinline__ uint32_t encode_block(const float* x, float S, float six_s, uint2* codes) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+  const uint32_t sc = e4m3_code(__fdiv_rn(m, six_s));
+  const float den = __fmul_rn(e4m3_value(sc), S);
+  *codes = make_uint2(0u, 0u);
+  if (den >= 0x1p-90f && den <= 0x1p90f && m < INFINITY) {
+    *codes = codes16(x, den, __frcp_rn(den));
+  } else if (den > 0.f) {  // out of the theorem's range
+    float q[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) q[e] = __fdiv_rn(x[e], den);
+    *codes = make_uint2(e2m1x8(q), e2m1x8(q + 8));
+  }
+  return sc;
+}
+
 // The lane's block: list entry j of sequence b, head h, block blk; false past
 // the list, for rows outside [0, R) and for slots outside the cache.
 struct BlockAt {
   long src, dst;  // elements into K / V; blocks into the cache
 };
-__device__ __forceinline__ bool block_at(const Kv4RowsArgs& a, int rpw, BlockAt* o) {
-  const int bpr = a.dh / 16, lane = threadIdx.x & 31;
-  const long warp = (long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+template <int DH>
+__device__ __forceinline__ bool block_at(const Kv4RowsArgs& a, BlockAt* o) {
+  constexpr int kBlocks = DH / 16, kRows = 32 / kBlocks;  // a row; rows a warp
+  const int lane = threadIdx.x & 31;
+  const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int b = blockIdx.y;
-  const int h = (int)(warp % a.Hkv);
-  const long j = warp / a.Hkv * rpw + lane / bpr;
+  const uint32_t group = (uint32_t)(((uint64_t)warp * a.hkv_recip) >> 40);
+  const int h = (int)(warp - group * a.Hkv);
+  const int j = (int)group * kRows + lane / kBlocks;
   const int cnt = a.cnt != nullptr ? min(a.cnt[b], a.R) : a.R;
   if (j >= cnt) return false;
-  const int r = a.rows != nullptr ? a.rows[(long)b * a.R + j] : (int)j;
+  const int r = a.rows != nullptr ? a.rows[(long)b * a.R + j] : j;
   if (r < 0 || r >= a.R) return false;
   const long slot = (long)r + (a.off != nullptr ? a.off[b] : 0);
   if (slot < 0 || slot >= a.Ncache) return false;
-  const int blk = lane % bpr;
-  o->src = ((long)b * a.R + r) * a.ld + (long)h * a.dh + blk * 16;
-  o->dst = (((long)b * a.Hkv + h) * a.Ncache + slot) * bpr + blk;
+  const int blk = lane % kBlocks;
+  o->src = ((long)b * a.R + r) * a.ld + (long)h * DH + blk * 16;
+  o->dst = (((long)b * a.Hkv + h) * a.Ncache + slot) * kBlocks + blk;
   return true;
 }
 
-template <typename T>
+template <typename T, int DH>
 __global__ void __launch_bounds__(kThreads)
-k_kv4_store(const Kv4RowsArgs a, int rpw) {
+k_kv4_store(const __grid_constant__ Kv4RowsArgs a) {
   pdl_prologue();
   BlockAt at;
-  if (!block_at(a, rpw, &at)) return;
+  if (!block_at<DH>(a, &at)) return;
   float k[16], v[16];
   load_block(static_cast<const T*>(a.K) + at.src, k);
   load_block(static_cast<const T*>(a.V) + at.src, v);
-  quant_block(k, a.kmul, __fmul_rn(6.0f, a.kmul), a.kcode + at.dst * 8, a.kscale + at.dst);
-  quant_block(v, a.vmul, __fmul_rn(6.0f, a.vmul), a.vcode + at.dst * 8, a.vscale + at.dst);
+  uint2 kc, vc;
+  const uint32_t ks = encode_block(k, a.kmul, __fmul_rn(6.0f, a.kmul), &kc);
+  const uint32_t vs = encode_block(v, a.vmul, __fmul_rn(6.0f, a.vmul), &vc);
+  reinterpret_cast<uint2*>(a.kcode)[at.dst] = kc;
+  reinterpret_cast<uint2*>(a.vcode)[at.dst] = vc;
+  a.kscale[at.dst] = (uint8_t)ks;
+  a.vscale[at.dst] = (uint8_t)vs;
 }
 
-template <typename T>
+template <typename T, int DH>
 __global__ void __launch_bounds__(kThreads)
-k_kv4_load(const Kv4RowsArgs a, int rpw) {
+k_kv4_load(const __grid_constant__ Kv4RowsArgs a) {
   pdl_prologue();
   BlockAt at;
-  if (!block_at(a, rpw, &at)) return;
-  const uint2 kc = *reinterpret_cast<const uint2*>(a.kcode + at.dst * 8);
-  const uint2 vc = *reinterpret_cast<const uint2*>(a.vcode + at.dst * 8);
+  if (!block_at<DH>(a, &at)) return;
+  const uint2 kc = reinterpret_cast<const uint2*>(a.kcode)[at.dst];
+  const uint2 vc = reinterpret_cast<const uint2*>(a.vcode)[at.dst];
   const uint32_t ks = a.kscale[at.dst], vs = a.vscale[at.dst];
   float x[16];
   dequant_block(kc, ks, a.kmul, x);
@@ -107,16 +149,26 @@ k_kv4_load(const Kv4RowsArgs a, int rpw) {
   put_block(static_cast<T*>(const_cast<void*>(a.V)) + at.src, x);
 }
 
+template <typename T, int DH>
+cudaError_t launch_rows(const Kv4RowsArgs& a, bool load, cudaStream_t s) {
+  const long warps = (long)ceil_div(a.R, 512 / DH) * a.Hkv;
+  const dim3 grid((unsigned)ceil_div(warps, kThreads / 32), a.B);
+  return launch_pdl(load ? k_kv4_load<T, DH> : k_kv4_store<T, DH>, grid, dim3(kThreads), 0, s, a);
+}
+
 }  // namespace
 
-cudaError_t kv4_rows_run(const Kv4RowsArgs& a, bool load, cudaStream_t s) {
-  const int rpw = 32 / (a.dh / 16);
-  const long warps = (long)ceil_div(a.R, rpw) * a.Hkv;
-  const dim3 grid((unsigned)ceil_div(warps, kThreads / 32), a.B);
-  if (a.dtype == PS_F32)
-    return launch_pdl(load ? k_kv4_load<float> : k_kv4_store<float>, grid, kThreads, 0, s, a, rpw);
-  return launch_pdl(load ? k_kv4_load<__nv_bfloat16> : k_kv4_store<__nv_bfloat16>, grid, kThreads,
-                    0, s, a, rpw);
+cudaError_t kv4_rows_run(Kv4RowsArgs a, bool load, cudaStream_t s) {
+  a.hkv_recip = ((1ull << 40) + a.Hkv - 1) / a.Hkv;
+#define PS_KV4_CASE(DH)                                              \
+  if (a.dh == DH)                                                    \
+    return a.dtype == PS_F32 ? launch_rows<float, DH>(a, load, s)    \
+                             : launch_rows<__nv_bfloat16, DH>(a, load, s);
+  PS_KV4_CASE(64)
+  PS_KV4_CASE(128)
+  PS_KV4_CASE(256)
+#undef PS_KV4_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace ps

@@ -9,6 +9,8 @@
 // slots first.  A last ascending pass turns the three kinds of kept slots
 // (protected, above the threshold, the first equal ones) into a packed list
 // with one block scan per 1024 slots.
+#include <type_traits>
+
 #include "kv4.cuh"
 
 namespace ps {
@@ -126,35 +128,55 @@ k_kv4_select(const Kv4EvictArgs a, int32_t* __restrict__ idx) {
   }
 }
 
-// One thread a 16-byte piece of a kept row's codes; the row's first two
-// threads also move its scales (dh / 16 bytes each of K and V).
+// A thread takes one 16-byte piece of the codes of kRowsEach kept rows, all
+// loads before the first store, so that enough bytes are in flight at scattered
+// addresses; a row's first K and first V thread move its scales too.
+constexpr int kRowsEach = 4;
+
+template <int DH>
 __global__ void __launch_bounds__(256)
-k_kv4_gather(const Kv4EvictArgs a, const int32_t* __restrict__ idx, int pieces) {
+k_kv4_gather(const __grid_constant__ Kv4EvictArgs a, const int32_t* __restrict__ idx) {
+  constexpr int kHalf = DH / 32, kPieces = 2 * kHalf;  // of K, of K and V
+  constexpr int kRows = 256 / kPieces;                 // rows a pass of the CTA
+  using Scale = std::conditional_t<DH == 64, uint32_t, std::conditional_t<DH == 128, uint2, uint4>>;
   pdl_prologue();
   const int bh = blockIdx.y, b = bh / a.Hkv;
   const int n = min(max(a.len != nullptr ? a.len[b] : a.Ncache, 0), a.Ncache);
   const int kept = min(n, a.keep);
-  const int j = (int)(((long)blockIdx.x * 256 + threadIdx.x) / pieces);
-  const int p = (int)(((long)blockIdx.x * 256 + threadIdx.x) % pieces);
-  if (j >= kept) return;
-  const long src = (long)bh * a.Ncache + idx[(long)bh * a.keep + j];
-  const long dst = (long)bh * a.Ndst + j;
-  const int half = pieces / 2, q = p % half;  // pieces of K, then of V
-  const uint8_t* c = p < half ? a.kcode : a.vcode;
-  uint8_t* cd = p < half ? a.kcode_dst : a.vcode_dst;
-  reinterpret_cast<uint4*>(cd)[dst * half + q] =
-      __ldcs(reinterpret_cast<const uint4*>(c) + src * half + q);
-  if (q == 0) {
-    const uint8_t* sc = p < half ? a.kscale : a.vscale;
-    uint8_t* sd = p < half ? a.kscale_dst : a.vscale_dst;
-    if (half == 2) {  // dh 64, 128, 256: 4, 8, 16 scale bytes
-      reinterpret_cast<uint32_t*>(sd)[dst] = reinterpret_cast<const uint32_t*>(sc)[src];
-    } else if (half == 4) {
-      reinterpret_cast<uint2*>(sd)[dst] = reinterpret_cast<const uint2*>(sc)[src];
-    } else {
-      reinterpret_cast<uint4*>(sd)[dst] = reinterpret_cast<const uint4*>(sc)[src];
-    }
+  const int p = threadIdx.x % kPieces, q = p % kHalf;
+  const bool is_v = p >= kHalf;
+  const int j0 = blockIdx.x * (kRows * kRowsEach) + threadIdx.x / kPieces;
+  const uint4* c = reinterpret_cast<const uint4*>(is_v ? a.vcode : a.kcode);
+  uint4* cd = reinterpret_cast<uint4*>(is_v ? a.vcode_dst : a.kcode_dst);
+  const Scale* sc = reinterpret_cast<const Scale*>(is_v ? a.vscale : a.kscale);
+  Scale* sd = reinterpret_cast<Scale*>(is_v ? a.vscale_dst : a.kscale_dst);
+  long src[kRowsEach];
+#pragma unroll
+  for (int i = 0; i < kRowsEach; ++i) {
+    const int j = j0 + i * kRows;
+    src[i] = j < kept ? (long)bh * a.Ncache + idx[(long)bh * a.keep + j] : -1;
   }
+  uint4 v[kRowsEach];
+  Scale s[kRowsEach];
+#pragma unroll
+  for (int i = 0; i < kRowsEach; ++i) {
+    if (src[i] < 0) continue;
+    v[i] = __ldcs(c + src[i] * kHalf + q);
+    if (q == 0) s[i] = sc[src[i]];
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsEach; ++i) {
+    if (src[i] < 0) continue;
+    const long dst = (long)bh * a.Ndst + j0 + i * kRows;
+    cd[dst * kHalf + q] = v[i];
+    if (q == 0) sd[dst] = s[i];
+  }
+}
+
+template <int DH>
+cudaError_t launch_gather(const Kv4EvictArgs& a, const int32_t* idx, cudaStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.keep, 256 / (DH / 16) * kRowsEach), a.B * a.Hkv);
+  return launch_pdl(k_kv4_gather<DH>, grid, dim3(256), 0, s, a, idx);
 }
 
 }  // namespace
@@ -170,9 +192,12 @@ cudaError_t kv4_evict_run(const Kv4EvictArgs& a, cudaStream_t s) {
   int32_t* idx = c.take<int32_t>((size_t)a.B * a.Hkv * a.keep);
   cudaError_t e = launch_pdl(k_kv4_select, dim3(a.B * a.Hkv), dim3(kST), 0, s, a, idx);
   if (e != cudaSuccess) return e;
-  const int pieces = 2 * (a.dh / 32);
-  const dim3 grid((unsigned)ceil_div((long)a.keep * pieces, 256), a.B * a.Hkv);
-  return launch_pdl(k_kv4_gather, grid, dim3(256), 0, s, a, idx, pieces);
+  switch (a.dh) {
+    case 64: return launch_gather<64>(a, idx, s);
+    case 128: return launch_gather<128>(a, idx, s);
+    case 256: return launch_gather<256>(a, idx, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace ps

@@ -107,8 +107,9 @@ struct Kv4RowsArgs {  // store: K, V -> cache; load: cache -> K, V
   const int32_t* off; const int32_t* rows; const int32_t* cnt;
   uint8_t* kcode; uint8_t* kscale; uint8_t* vcode; uint8_t* vscale;
   float kmul, vmul;
+  uint64_t hkv_recip;  // ceil(2^40 / Hkv), set by kv4_rows_run
 };
-cudaError_t kv4_rows_run(const Kv4RowsArgs& a, bool load, cudaStream_t s);
+cudaError_t kv4_rows_run(Kv4RowsArgs a, bool load, cudaStream_t s);
 
 struct Kv4AttnArgs {
   const uint8_t* kcode; const uint8_t* kscale; const uint8_t* vcode; const uint8_t* vscale;

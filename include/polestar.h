@@ -476,9 +476,8 @@ int ps_schedule_step(const ps_schedule_params* p, ps_schedule_state* s,
  * head for dh = 128, against 512 in bf16.  A slot that was never stored may
  * hold any bytes; calls never let it reach a result.
  *
- * ps_kv4_attn and ps_kv4_weight also need B * Hkv <= 65535; every call needs
- * B >= 0 (0: no-op), Hkv >= 1, Ncache >= 1 and 16-byte aligned codes, scales,
- * K, V, Q and O.
+ * Every call needs B >= 0 (0: no-op), 1 <= Hkv <= 512, B * Hkv <= 65535,
+ * Ncache >= 1 and 16-byte aligned codes, scales, K, V, Q and O.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint8_t* kcode;
