@@ -34,6 +34,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kGrow = 4.f;      // log2 growth of a maximum before O is rescaled
+constexpr int kMaxCluster = 8;    // CTAs of a portable cluster
 constexpr float kNoMax = -1e30f;  // a maximum that every score outgrows
 // Rows [m0, m0 + rows) of (b, hkv) into shared memory as B fragments
 // [row / 8][part][ks / 2][lane] (uint4: two steps' pairs), with their constants;
@@ -286,12 +287,14 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   using R = Ring<DH, true>;
   uint4* qs = smem4;                               // NB * P * KS / 2 * 32
   float* obuf = reinterpret_cast<float*>(smem4);   // kWarps * kRows * DH, after the loop
+  float* cbuf = obuf + kWarps * kRows * DH;        // kRows * DH, the CTA's sums
+  __shared__ float cml[2 * kRows];
   __shared__ RowPar par[kRows];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int tile = blockIdx.x % a.ntile;
-  const int split = blockIdx.x / a.ntile % a.nsplit;
-  const int bh = blockIdx.x / a.ntile / a.nsplit;
+  const int split = blockIdx.x % a.nsplit;
+  const int tile = blockIdx.x / a.nsplit % a.ntile;
+  const int bh = blockIdx.x / a.nsplit / a.ntile;
   const int b = bh / a.Hkv, hkv = bh % a.Hkv, m0 = tile * kRows;
   const int rows = min(kRows, a.M - m0);
   const int len = kv4_len(a, b);
@@ -323,7 +326,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     n_hi = (int)min((long)n_hi, (long)n_lo + share);
   }
 
-  if (a.nsplit > 1 && n_lo >= n_hi) {  // an empty share
+  if (a.nsplit > 1 && !a.cluster && n_lo >= n_hi) {  // an empty share
     if (tid < rows) {
       const size_t at = ((size_t)bh * a.M + m0 + tid) * a.nsplit + split;
       a.pml[2 * at] = -INFINITY;
@@ -571,7 +574,13 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       l += c * s_l[w][r];
       acc.x += c * v.x; acc.y += c * v.y; acc.z += c * v.z; acc.w += c * v.w;
     }
-    if (a.nsplit > 1) {
+    if (a.cluster) {
+      *reinterpret_cast<float4*>(cbuf + r * DH + d) = acc;
+      if (d == 0) {
+        cml[2 * r] = mx;
+        cml[2 * r + 1] = l;
+      }
+    } else if (a.nsplit > 1) {
       const size_t at = ((size_t)bh * a.M + m) * a.nsplit + split;
       if (l != 0.f) *reinterpret_cast<float4*>(a.po + at * DH + d) = acc;
       if (d == 0) {
@@ -581,6 +590,38 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     } else {
       kv4_finish<F32>(a, b, hkv, m, DH, d, acc, mx, l);
     }
+  }
+  if (a.cluster) {
+    // The shares of these rows are the CTAs of a thread-block cluster: each
+    // joins its part of the elements from all of them, in order.
+    tc::cluster_sync_all();
+    const uint32_t cb = tc::smem_u32(cbuf), cm = tc::smem_u32(cml);
+    for (int e = tid + split * kThreads; e < rows * (DH / 4); e += kThreads * a.nsplit) {
+      const int r = e / (DH / 4), d = e % (DH / 4) * 4;
+      float ms[kMaxCluster], ls[kMaxCluster], mx = -INFINITY, l = 0.f;
+      float4 v[kMaxCluster];
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        if (q >= a.nsplit) break;
+        const uint32_t mq = tc::cluster_map(cm, q) + r * 8;
+        ms[q] = tc::ld_dsmem_f32(mq);
+        ls[q] = tc::ld_dsmem_f32(mq + 4);
+        v[q] = tc::ld_dsmem_v4(tc::cluster_map(cb, q) + (r * DH + d) * 4);
+      }
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q)
+        if (q < a.nsplit) mx = fmaxf(mx, ms[q]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        if (q >= a.nsplit) break;
+        const float c = ms[q] == -INFINITY ? 1.f : exp2_approx(ms[q] - mx);
+        l += c * ls[q];
+        acc.x += c * v[q].x; acc.y += c * v[q].y; acc.z += c * v[q].z; acc.w += c * v[q].w;
+      }
+      kv4_finish<F32>(a, b, hkv, m0 + r, DH, d, acc, mx, l);
+    }
+    tc::cluster_sync_all();  // no CTA leaves while another still reads its sums
   }
 }
 
@@ -790,7 +831,7 @@ template <int DH, int NB, bool F32, bool GEN>
 cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t q_bytes =
       (size_t)NB * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, true>::kBytes;
-  constexpr size_t o_bytes = (size_t)kWarps * 8 * NB * DH * 4;
+  constexpr size_t o_bytes = (size_t)(kWarps + 1) * 8 * NB * DH * 4;
   constexpr size_t smem = q_bytes > o_bytes ? q_bytes : o_bytes;
   auto kern = k_kv4_attn<DH, NB, F32, GEN>;
   static bool attr_set = false;
@@ -800,8 +841,22 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  const long grid = (long)a.B * a.Hkv * a.nsplit * a.ntile;
-  cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, a);
+  const unsigned grid = (unsigned)((long)a.B * a.Hkv * a.nsplit * a.ntile);
+  if (a.cluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.nsplit;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_ex(cfg, kern, a);
+  }
+  cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess || a.nsplit == 1) return e;
   return launch_combine<DH, F32>(a, s);
 }
@@ -868,19 +923,24 @@ AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   return p;
 }
 
+// Few shares are joined inside a thread-block cluster, without a second kernel.
+bool in_cluster(const AttnPlan& p) { return !p.tc && p.nsplit > 1 && p.nsplit <= kMaxCluster; }
+
 }  // namespace
 
 size_t kv4_attn_ws(int B, int N, int Hq, int Hkv, int dh, int T) {
   // either type's: the size does not name it
-  const int a = attn_plan(PS_BF16, B, N, Hq, Hkv, dh, T).nsplit;
-  const int b = attn_plan(PS_F32, B, N, Hq, Hkv, dh, T).nsplit;
-  const int nsplit = a > b ? a : b;
-  if (nsplit == 1) return 0;
-  Carver c(nullptr);
-  const size_t rows = (size_t)B * T * Hq * nsplit;
-  c.take<float>(rows * dh);
-  c.take<float>(rows * 2);
-  return c.bytes();
+  size_t most = 0;
+  for (int dtype : {PS_F32, PS_BF16}) {
+    const AttnPlan p = attn_plan(dtype, B, N, Hq, Hkv, dh, T);
+    if (p.nsplit == 1 || in_cluster(p)) continue;
+    Carver c(nullptr);
+    const size_t rows = (size_t)B * T * Hq * p.nsplit;
+    c.take<float>(rows * dh);
+    c.take<float>(rows * 2);
+    if (c.bytes() > most) most = c.bytes();
+  }
+  return most;
 }
 
 size_t kv4_weight_ws(int, int, int, int, int, int) { return 0; }
@@ -889,7 +949,8 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
   const AttnPlan p = attn_plan(a.dtype, a.B, a.Ncache, a.Hq, a.Hkv, a.dh, a.T);
   a.ntile = p.ntile;
   a.nsplit = p.nsplit;
-  if (a.nsplit > 1) {
+  a.cluster = in_cluster(p);
+  if (a.nsplit > 1 && !a.cluster) {
     Carver c(a.ws);
     const size_t rows = (size_t)a.B * a.T * a.Hq * a.nsplit;
     a.po = c.take<float>(rows * a.dh);

@@ -122,6 +122,7 @@ struct Kv4AttnArgs {
   void* O; float* lse;                                    // attention
   const float* lse_in; const float* w_in; float* w_out;   // weight
   void* ws; int ntile, nsplit; float* po; float* pml;     // row tiles, shares, their partials
+  bool cluster;                                           // shares joined in a cluster
   int num_sms; int* status;
 };
 size_t kv4_attn_ws(int B, int N, int Hq, int Hkv, int dh, int T);

@@ -134,8 +134,9 @@ class Library:
 
     def handle(self, device=None):
         """A process-wide handle for `device` (created on first use)."""
-        dev = torch.cuda.current_device() if device is None else int(device)
+        dev = torch.cuda.current_device() if device is None else device
         if dev not in self._handles:
+            dev = int(dev)
             h = _p()
             st = self.cdll.ps_create(dev, ctypes.byref(h))
             if st != PS_OK:
@@ -176,7 +177,7 @@ def _check(st, where):
 
 
 def _ws(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
 def ps_workspace_bytes(op, B=0, N=0, d=0, C=0, Hq=0, Hkv=0, dh=0, k=0, P=0, V=0):
@@ -408,6 +409,7 @@ class Kv4Cache:
         self.buffers = (kcode, kscale, vcode, vscale)
         self.kmul, self.vmul = float(kmul), float(vmul)
         self.device = kcode.device
+        self.index = self.device.index  # of the device
         self._c = self._pack.pack(*(t.data_ptr() for t in self.buffers), self.B, self.Hkv,
                                   self.N, self.dh, self.kmul, self.vmul)
 
@@ -419,10 +421,23 @@ class Kv4Cache:
         return cls(*mk, kmul=kmul, vmul=vmul)
 
 
+# The current stream of a device as an integer, without building a Stream
+# object (0.1 us against 3 us of a call that a decode loop makes per layer).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _kv4_stream(stream, c):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(c.index)
+    return _stream(stream)
+
+
 def _plain(t, dtype, shape, null=False):
     """Pointer of a contiguous device tensor of this dtype and shape."""
-    if t is None and null:
-        return 0
+    if t is None:
+        if null:
+            return 0
+        raise ValueError(f"expected a {dtype} device tensor of shape {tuple(shape)}, got None")
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"expected a contiguous {dtype} device tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
@@ -432,9 +447,14 @@ def _plain(t, dtype, shape, null=False):
 def _rows_ld(t, B, H, dh):
     """(rows, elements between rows) of t [B][R][H][dh], whose rows may be
     parts of wider ones."""
-    if t.dim() != 4 or t.shape[0] != B or t.shape[2] != H or t.shape[3] != dh or not t.is_cuda:
-        raise ValueError(f"expected a device tensor [{B}][rows][{H}][{dh}], got {tuple(t.shape)}")
-    R = t.shape[1]
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"expected a device tensor [{B}][rows][heads][{dh}], got {tuple(shape)}")
+    b, R, h, d = shape
+    if b != B or h != H or d != dh or not t.is_cuda:
+        raise ValueError(f"expected a device tensor [{B}][rows][{H}][{dh}], got {tuple(shape)}")
+    if t.is_contiguous():
+        return R, H * dh
     sb, sr, sh, sd = t.stride()
     ok = sd == 1 and (sh == dh or H == 1)
     if R > 1:
@@ -449,13 +469,13 @@ def _rows_ld(t, B, H, dh):
 
 def _kv4_rows(name, c, K, V, off, rows, cnt, stream):
     R, ld = _rows_ld(K, c.B, c.Hkv, c.dh)
-    if V.dtype != K.dtype or V.stride() != K.stride() or V.shape != K.shape or not V.is_cuda:
-        raise ValueError("K and V need one dtype, shape and stride")
+    if V.dtype != K.dtype or V.shape != K.shape or _rows_ld(V, c.B, c.Hkv, c.dh) != (R, ld):
+        raise ValueError("K and V need one dtype, shape and row stride")
     lib = _lib()
     st = getattr(lib.cdll, name)(
-        lib.handle(c.device.index), c._c, K.data_ptr(), V.data_ptr(), _dtype(K), R, ld,
+        lib.handle(c.index), c._c, K.data_ptr(), V.data_ptr(), _dtype(K), R, ld,
         _plain(off, torch.int32, (c.B,), True), _plain(rows, torch.int32, (c.B, R), True),
-        _plain(cnt, torch.int32, (c.B,), True), _stream(stream))
+        _plain(cnt, torch.int32, (c.B,), True), _kv4_stream(stream, c))
     _check(st, name)
 
 
@@ -474,9 +494,7 @@ _Q_PACK = struct.Struct("6Pq3i2f")
 
 
 def _kv4_query(c, Q, len, span, kpos, qpos, slope, scale, cap):
-    if Q.dim() != 4:
-        raise ValueError(f"expected Q [B][T][Hq][dh], got {tuple(Q.shape)}")
-    Hq = Q.shape[2]
+    Hq = Q.shape[2] if Q.dim() == 4 else 0
     T, ld = _rows_ld(Q, c.B, Hq, c.dh)
     i32 = torch.int32
     return T, Hq, _Q_PACK.pack(
@@ -493,10 +511,10 @@ def ps_kv4_attn(c, Q, O, lse=None, *, scale, len=None, span=None, kpos=None, qpo
     lib = _lib()
     T, Hq, q = _kv4_query(c, Q, len, span, kpos, qpos, slope, scale, cap)
     w, wn = _ws(ws)
-    st = lib.cdll.ps_kv4_attn(lib.handle(c.device.index), c._c, q,
+    st = lib.cdll.ps_kv4_attn(lib.handle(c.index), c._c, q,
                               _plain(O, Q.dtype, (c.B, T, Hq, c.dh)),
                               _plain(lse, torch.float32, (c.B, T, Hq), True), w, wn,
-                              _stream(stream))
+                              _kv4_stream(stream, c))
     _check(st, "ps_kv4_attn")
 
 
@@ -508,10 +526,10 @@ def ps_kv4_weight(c, Q, lse, w_in, w_out, *, scale, len=None, span=None, kpos=No
     T, Hq, q = _kv4_query(c, Q, len, span, kpos, qpos, slope, scale, cap)
     shape = (c.B, c.Hkv, c.N)
     w, wn = _ws(ws)
-    st = lib.cdll.ps_kv4_weight(lib.handle(c.device.index), c._c, q,
+    st = lib.cdll.ps_kv4_weight(lib.handle(c.index), c._c, q,
                                 _plain(lse, torch.float32, (c.B, T, Hq)),
                                 _plain(w_in, torch.float32, shape, True),
-                                _plain(w_out, torch.float32, shape), w, wn, _stream(stream))
+                                _plain(w_out, torch.float32, shape), w, wn, _kv4_stream(stream, c))
     _check(st, "ps_kv4_weight")
 
 
@@ -525,10 +543,10 @@ def ps_kv4_evict(src, dst, w, w_dst, len_dst, keep, sink=0, recent=0, len=None, 
     a, b = (src.B, src.Hkv, src.N), (src.B, src.Hkv, dst.N)
     wsp, wn = _ws(ws)
     st = lib.cdll.ps_kv4_evict(
-        lib.handle(src.device.index), src._c, dst._c, _plain(w, f32, a),
+        lib.handle(src.index), src._c, dst._c, _plain(w, f32, a),
         _plain(len, i32, (src.B,), True), _plain(kpos, i32, a, True), int(keep), int(sink),
         int(recent), _plain(w_dst, f32, b), _plain(kpos_dst, i32, b, True),
-        _plain(len_dst, i32, (src.B,)), wsp, wn, _stream(stream))
+        _plain(len_dst, i32, (src.B,)), wsp, wn, _kv4_stream(stream, src))
     _check(st, "ps_kv4_evict")
 
 

@@ -311,7 +311,8 @@ def test_store_lists_and_skipped_entries():
 EVICT = [(1, 1, 64, 5, 3, 0, 0, "rand"), (2, 3, 128, 1500, 700, 4, 32, "rand"),
          (2, 2, 128, 2048, 1024, 0, 0, "ties"), (1, 2, 256, 300, 299, 1, 298, "rand"),
          (3, 1, 128, 700, 650, 10, 20, "nan"), (1, 4, 64, 5000, 17, 17, 0, "rand"),
-         (2, 2, 128, 1025, 400, 3, 5, "zero"), (1, 1, 128, 9000, 4096, 4, 64, "neg")]
+         (2, 2, 128, 1025, 400, 3, 5, "zero"), (1, 1, 128, 9000, 4096, 4, 64, "neg"),
+         (1, 2, 64, 20000, 7000, 4, 100, "ties"), (2, 1, 64, 16384, 16000, 0, 9, "rand")]
 
 
 @pytest.mark.parametrize("B,Hkv,dh,N,keep,sink,recent,kind", EVICT)
