@@ -673,8 +673,76 @@ k_kv4_combine(const __grid_constant__ Kv4AttnArgs a) {
 // on timing.
 constexpr int kWRows = 64;
 
-// GEN: capped scores, a distance bias or explicit positions.
+// The slots that some row, and that every row, of those in shared memory sees.
+struct SeenRange {
+  int any_lo, any_hi, all_lo, all_hi;
+};
+__device__ __forceinline__ SeenRange seen_range(const RowPar* par, int rows, int len) {
+  int lo = INT32_MAX, hi = INT32_MIN, lo_all = INT32_MIN, hi_all = INT32_MAX;
+  for (int r = threadIdx.x & 31; r < rows; r += 32) {
+    const int x = par[r].lo, y = par[r].hi;
+    if (x < y) {
+      lo = min(lo, x);
+      hi = max(hi, y);
+    }
+    lo_all = max(lo_all, x);
+    hi_all = min(hi_all, y);
+  }
+  SeenRange s;
+  s.any_lo = __reduce_min_sync(0xffffffffu, lo);
+  s.any_hi = min(len, __reduce_max_sync(0xffffffffu, hi));
+  s.all_lo = __reduce_max_sync(0xffffffffu, lo_all);
+  s.all_hi = min(len, __reduce_min_sync(0xffffffffu, hi_all));
+  return s;
+}
+
+// acc[j] += sum over nbs blocks of 8 rows of exp(score - lse), slots n + sg + 8 j.
 template <int DH, bool F32, bool GEN>
+__device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)[4], const uint4* qp,
+                                      const RowPar* rp, int nbs, int n_sg, int len, const int* pos,
+                                      bool masked, float* acc) {
+  constexpr int KS = DH / 16, P = F32 ? 2 : 1;
+#pragma unroll 1
+  for (; nbs > 0; --nbs, qp += P * (KS / 2) * 32, rp += 8) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < KS / 2; ++w)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const uint4 q = qp[(p * (KS / 2) + w) * 32];
+        mma_f16(s, kf[2 * w], q.x, q.y);
+        mma_f16(s, kf[2 * w + 1], q.z, q.w);
+      }
+    // score - lse of slots sg, sg + 8 (c / 2), rows 2 t, 2 t + 1 (c & 1)
+    float x[4];
+    const float f0 = rp[0].f, l0 = -rp[0].lse, f1 = rp[1].f, l1 = -rp[1].lse;
+    if (GEN && a.cap > 0.f) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x[c] = fmaf(a.cap, tanhf(s[c] * (c & 1 ? f1 : f0) * a.inv_cap), c & 1 ? l1 : l0);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = fmaf(s[c], c & 1 ? f1 : f0, c & 1 ? l1 : l0);
+    }
+    if (GEN && a.slope != nullptr) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x[c] = fmaf(-rp[c & 1].slope, fabsf((float)(rp[c & 1].qpos - pos[c >> 1])), x[c]);
+    }
+    if (masked) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (n_sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp[c & 1].lo || pos[c >> 1] >= rp[c & 1].hi)
+          x[c] = -INFINITY;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c >> 1] += exp2_approx(x[c] * kLog2e);
+  }
+}
+
+// GEN: capped scores, a distance bias or explicit positions.  ONE: all rows fit
+// shared memory and are staged once.
+template <int DH, bool F32, bool GEN, bool ONE>
 __global__ void __launch_bounds__(kThreads)
 k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   constexpr int KS = DH / 16, P = F32 ? 2 : 1;
@@ -687,66 +755,46 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   const int bh = blockIdx.y, b = bh / a.Hkv, hkv = bh % a.Hkv;
   const int len = kv4_len(a, b), last = a.Ncache - 1;
   const int32_t* kpos = GEN && a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
-  const float* w_in = a.w_in != nullptr ? a.w_in + (long)bh * a.Ncache : nullptr;
-  float* w_out = a.w_out + (long)bh * a.Ncache;
-  const int chunks = ceil_div(a.M, kWRows);
+  const int chunks = ONE ? 1 : ceil_div(a.M, kWRows);
   const int n0 = (blockIdx.x * steps) * 64 + 16 * warp;
+  // the warp's steps that hold slots of the sequence; all warps' for the barriers
+  const int live = max(0, min(steps, ceil_div(len - n0, 64)));
+  const int sg = slot_at(g);
+  // lanes t < 2 write slot sg + 8 t
+  const float* w_in = a.w_in != nullptr ? a.w_in + (long)bh * a.Ncache + n0 + sg + 8 * t : nullptr;
+  float* w_out = a.w_out + (long)bh * a.Ncache + n0 + sg + 8 * t;
+  int room = t < 2 ? a.Ncache - (n0 + sg + 8 * t) : 0;  // > 0: the slot exists
   uint8_t* ring =
       reinterpret_cast<uint8_t*>(qs + (kWRows / 8) * P * (KS / 2) * 32) + warp * R::kBytes;
   const uint32_t ring32 = tc::smem_u32(ring);
   RingFill<DH, false> fill(a, bh, n0);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if (i < steps && n0 + 64 * i < len) fill.next(ring32 + i * R::kStage, 64);
+    if (i < live) fill.next(ring32 + i * R::kStage, 64);
     cp_commit();
   }
-  const int sg = slot_at(g);
   uint32_t at = 0, to = (kStages - 1) * R::kStage;  // stage to read, stage to fill
-  // slots that some row, that every row of the chunk in shared memory sees
-  int any_lo = 0, any_hi = len, all_lo = 0, all_hi = GEN && kpos != nullptr && a.span != nullptr ? -1 : len;
-  auto stage = [&](int ch) {
-    const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
-    __syncthreads();
-    stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
-    __syncthreads();
-    if (a.span != nullptr && kpos == nullptr) {
-      int lo = INT32_MAX, hi = INT32_MIN, lo_all = INT32_MIN, hi_all = INT32_MAX;
-      for (int r = lane; r < rows; r += 32) {
-        const int x = par[r].lo, y = par[r].hi;
-        if (x < y) {
-          lo = min(lo, x);
-          hi = max(hi, y);
-        }
-        lo_all = max(lo_all, x);
-        hi_all = min(hi_all, y);
-      }
-      any_lo = __reduce_min_sync(0xffffffffu, lo);
-      any_hi = __reduce_max_sync(0xffffffffu, hi);
-      all_lo = __reduce_max_sync(0xffffffffu, lo_all);
-      all_hi = min(len, __reduce_min_sync(0xffffffffu, hi_all));
-    }
-    return ceil_div(rows, 8);
-  };
+  const bool spans = a.span != nullptr && kpos == nullptr;
+  SeenRange seen{0, len, 0, kpos != nullptr && a.span != nullptr ? -1 : len};
   int nbs = 0;
-  if (chunks == 1) nbs = stage(0);
-  // the slot that this lane writes
-  int mine = t < 2 ? n0 + sg + 8 * t : INT32_MAX;
+  if constexpr (ONE) {
+    stage_rows<DH, F32>(a, b, hkv, 0, (a.M + 7) & ~7, qs, par);
+    __syncthreads();
+    if (spans) seen = seen_range(par, a.M, len);
+    nbs = ceil_div(a.M, 8);
+  }
+  const int all = ONE ? live : steps;
   int n = n0;
-  for (int st = 0; st < steps; ++st, n += 64, mine += t < 2 ? 64 : 0) {
-    const bool live = n < len;  // warp-uniform
-    if (chunks == 1 && !live) {
-      if (mine < a.Ncache) w_out[mine] = w_in != nullptr ? w_in[mine] : 0.f;
-      continue;
-    }
+  for (int st = 0; st < all; ++st, n += 64) {
     uint32_t kf[KS][4];
     int pos[2] = {n + sg, n + sg + 8};
     float acc[2] = {0.f, 0.f};  // slots sg and sg + 8
-    const float w_old = w_in != nullptr && mine < a.Ncache ? w_in[mine] : 0.f;  // asked for early
+    const float old = w_in != nullptr && room > 0 ? *w_in : 0.f;  // asked for early
     cp_wait<kStages - 2>();
     __syncwarp();
-    if (st + kStages - 1 < steps && n + 64 * (kStages - 1) < len) fill.next(ring32 + to, 64);
+    if (st + kStages - 1 < live) fill.next(ring32 + to, 64);
     cp_commit();
-    if (live) {
+    if (ONE || st < live) {
       RawK<DH> rk;
       read_k<DH>(ring + at, g, t, rk);
 #pragma unroll
@@ -758,57 +806,20 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
     }
     to = at;
     at = at + R::kStage == R::kBytes ? 0 : at + R::kStage;
-    for (int ch = 0; ch < chunks; ++ch) {
-      if (chunks > 1) nbs = stage(ch);
-      if (!live || n >= any_hi || n + 16 <= any_lo) continue;
-      const bool masked = n < all_lo || n + 16 > all_hi;
-      const uint4* qp = qs + lane;
-      const RowPar* rp0 = par + 2 * t;
-#pragma unroll 1
-      for (int nb = 0; nb < nbs; ++nb, qp += P * (KS / 2) * 32, rp0 += 8) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < KS / 2; ++w)
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const uint4 q = qp[(p * (KS / 2) + w) * 32];
-            mma_f16(s, kf[2 * w], q.x, q.y);
-            mma_f16(s, kf[2 * w + 1], q.z, q.w);
-          }
-        const RowPar& r0 = rp0[0];
-        const RowPar& r1 = rp0[1];
-        // score - lse of slots sg, sg + 8 (c / 2), rows 2 t, 2 t + 1 (c & 1)
-        float x[4];
-        if (GEN && a.cap > 0.f) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const RowPar& rp = c & 1 ? r1 : r0;
-            x[c] = fmaf(a.cap, tanhf(s[c] * rp.f * a.inv_cap), -rp.lse);
-          }
-        } else {
-          const float f0 = r0.f, l0 = -r0.lse, f1 = r1.f, l1 = -r1.lse;
-          x[0] = fmaf(s[0], f0, l0);
-          x[1] = fmaf(s[1], f1, l1);
-          x[2] = fmaf(s[2], f0, l0);
-          x[3] = fmaf(s[3], f1, l1);
-        }
-        if (GEN && a.slope != nullptr) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const RowPar& rp = c & 1 ? r1 : r0;
-            x[c] = fmaf(-rp.slope, fabsf((float)(rp.qpos - pos[c >> 1])), x[c]);
-          }
-        }
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const RowPar& rp = c & 1 ? r1 : r0;
-            if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
-              x[c] = -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[c >> 1] += exp2_approx(x[c] * kLog2e);
+    if constexpr (ONE) {
+      if (n < seen.any_hi && n + 16 > seen.any_lo)
+        weigh<DH, F32, GEN>(a, kf, qs + lane, par + 2 * t, nbs, n + sg, len, pos,
+                            n < seen.all_lo || n + 16 > seen.all_hi, acc);
+    } else {
+      for (int ch = 0; ch < chunks; ++ch) {
+        const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
+        __syncthreads();
+        stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
+        __syncthreads();
+        if (spans) seen = seen_range(par, rows, len);
+        if (st < live && n < seen.any_hi && n + 16 > seen.any_lo)
+          weigh<DH, F32, GEN>(a, kf, qs + lane, par + 2 * t, ceil_div(rows, 8), n + sg, len, pos,
+                              n < seen.all_lo || n + 16 > seen.all_hi, acc);
       }
     }
 #pragma unroll
@@ -816,7 +827,16 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
       acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 1);
       acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 2);
     }
-    if (mine < a.Ncache) w_out[mine] = w_old + (t == 0 ? acc[0] : acc[1]);
+    if (room > 0) *w_out = old + (t == 0 ? acc[0] : acc[1]);
+    if (w_in != nullptr) w_in += 64;
+    w_out += 64;
+    room -= 64;
+  }
+  for (int st = all; st < steps; ++st) {  // past the sequence
+    if (room > 0) *w_out = w_in != nullptr ? *w_in : 0.f;
+    if (w_in != nullptr) w_in += 64;
+    w_out += 64;
+    room -= 64;
   }
   cp_wait<0>();  // no copy is under way when the CTA leaves
 }
@@ -861,11 +881,11 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   return launch_combine<DH, F32>(a, s);
 }
 
-template <int DH, bool F32, bool GEN>
+template <int DH, bool F32, bool GEN, bool ONE>
 cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem =
       (size_t)(kWRows / 8) * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, false>::kBytes;
-  auto kern = k_kv4_weight<DH, F32, GEN>;
+  auto kern = k_kv4_weight<DH, F32, GEN, ONE>;
   static bool attr_set = false;
   if (!attr_set && smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -877,7 +897,7 @@ cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
   // a CTA, as many as leave six CTAs an SM
   const int groups = ceil_div(a.Ncache, 64);
   int steps = 1;
-  if (a.M <= kWRows) {
+  if (ONE) {
     steps = (int)((long)groups * a.B * a.Hkv / (6 * kSmTarget));
     steps = steps < 1 ? 1 : steps > 64 ? 64 : steps;
   }
@@ -984,11 +1004,17 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
 
 cudaError_t kv4_weight_run(const Kv4AttnArgs& a, cudaStream_t s) {
   const bool gen = a.cap > 0.f || a.slope != nullptr || a.kpos != nullptr;
-#define PS_KV4_CASE(DH)                                                      \
-  if (a.dh == DH) {                                                          \
-    if (a.dtype == PS_F32) return launch_weight<DH, true, true>(a, s);       \
-    return gen ? launch_weight<DH, false, true>(a, s)                        \
-               : launch_weight<DH, false, false>(a, s);                      \
+  const bool one = a.M <= kWRows;
+#define PS_KV4_CASE(DH)                                                       \
+  if (a.dh == DH) {                                                           \
+    if (a.dtype == PS_F32)                                                    \
+      return one ? launch_weight<DH, true, true, true>(a, s)                  \
+                 : launch_weight<DH, true, true, false>(a, s);                \
+    if (gen)                                                                  \
+      return one ? launch_weight<DH, false, true, true>(a, s)                 \
+                 : launch_weight<DH, false, true, false>(a, s);               \
+    return one ? launch_weight<DH, false, false, true>(a, s)                  \
+               : launch_weight<DH, false, false, false>(a, s);                \
   }
   PS_KV4_CASE(64)
   PS_KV4_CASE(128)
