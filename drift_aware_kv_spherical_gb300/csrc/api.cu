@@ -525,17 +525,17 @@ bool ld_ok(int64_t ld, long least, int dtype) {
 }
 
 ps_status kv4_rows(ps_handle h, const ps_kv4_cache* c, const void* K, const void* V, int dtype,
-                   int R, int64_t ld, const int32_t* off, const int32_t* rows,
+                   int R, int64_t b_ld, int64_t ld, const int32_t* off, const int32_t* rows,
                    const int32_t* cnt, bool load, void* stream) {
   TraceScope trace_scope(h);
   PS_REQUIRE(h != nullptr && dtype_ok(dtype) && R >= 0);
   ps_status st = check_kv4(c);
   if (st != PS_OK) return st;
   if (c->B == 0 || R == 0) return PS_OK;
-  PS_REQUIRE(ld_ok(ld, (long)c->Hkv * c->dh, dtype));
+  PS_REQUIRE(ld_ok(ld, (long)c->Hkv * c->dh, dtype) && ld_ok(b_ld, 0, dtype));
   PS_REQUIRE((long)R * c->Hkv <= (1 << 30));
   PS_PTR(K); PS_PTR(V);
-  Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)ld, off, rows, cnt,
+  Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)b_ld, (long)ld, off, rows, cnt,
                 c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul, 0};
   return launch_status(kv4_rows_run(a, load, static_cast<cudaStream_t>(stream)));
 }
@@ -553,7 +553,7 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
   *none = c->B == 0 || q->T == 0;
   if (*none) return PS_OK;
   PS_REQUIRE((long)c->B * q->T * q->Hq <= INT32_MAX / 64 && q->Hq / c->Hkv <= 4096);
-  PS_REQUIRE(ld_ok(q->q_ld, (long)q->Hq * c->dh, q->dtype));
+  PS_REQUIRE(ld_ok(q->q_ld, (long)q->Hq * c->dh, q->dtype) && ld_ok(q->q_bld, 0, q->dtype));
   PS_PTR(q->Q);
   *a = Kv4AttnArgs{};
   a->kcode = c->kcode; a->kscale = c->kscale; a->vcode = c->vcode; a->vscale = c->vscale;
@@ -561,7 +561,8 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
   a->B = c->B; a->T = q->T; a->Hq = q->Hq; a->Hkv = c->Hkv;
   a->G = q->Hq / c->Hkv; a->M = q->T * a->G;
   a->g_recip = ((1ull << 40) + a->G - 1) / a->G;
-  a->Ncache = c->Ncache; a->dh = c->dh; a->q_ld = (long)q->q_ld;
+  a->Ncache = c->Ncache; a->dh = c->dh;
+  a->q_bld = (long)q->q_bld; a->q_ld = (long)q->q_ld;
   a->len = q->len; a->span = q->span; a->kpos = q->kpos; a->qpos = q->qpos; a->slope = q->slope;
   a->scale = q->scale * c->kmul; a->vmul = c->vmul;
   a->cap = q->cap; a->inv_cap = q->cap > 0.f ? 1.f / q->cap : 0.f;
@@ -572,16 +573,16 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
 }  // namespace
 
 extern "C" ps_status ps_kv4_store(ps_handle h, const ps_kv4_cache* c, const void* K,
-                                  const void* V, int dtype, int R, int64_t ld,
+                                  const void* V, int dtype, int R, int64_t b_ld, int64_t ld,
                                   const int32_t* off, const int32_t* rows, const int32_t* cnt,
                                   void* stream) {
-  return kv4_rows(h, c, K, V, dtype, R, ld, off, rows, cnt, false, stream);
+  return kv4_rows(h, c, K, V, dtype, R, b_ld, ld, off, rows, cnt, false, stream);
 }
 
 extern "C" ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V, int dtype,
-                                 int R, int64_t ld, const int32_t* off, const int32_t* rows,
-                                 const int32_t* cnt, void* stream) {
-  return kv4_rows(h, c, K, V, dtype, R, ld, off, rows, cnt, true, stream);
+                                 int R, int64_t b_ld, int64_t ld, const int32_t* off,
+                                 const int32_t* rows, const int32_t* cnt, void* stream) {
+  return kv4_rows(h, c, K, V, dtype, R, b_ld, ld, off, rows, cnt, true, stream);
 }
 
 extern "C" ps_status ps_kv4_attn(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,

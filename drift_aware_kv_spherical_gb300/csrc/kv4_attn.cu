@@ -52,7 +52,7 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
     if (m < a.M) {
       const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
       const long tok = (long)b * a.T + t;
-      const long at = tok * a.q_ld + (long)h * DH + sub * 8;
+      const long at = (long)b * a.q_bld + (long)t * a.q_ld + (long)h * DH + sub * 8;
       if constexpr (F32) {
         load16(static_cast<const float*>(a.Q) + at, x);
         load16(static_cast<const float*>(a.Q) + at + 4, x + 4);

@@ -543,7 +543,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
         range = tc_range(row);
         if (act) {
           row.f = stage_q<DH>(in ? static_cast<const __nv_bfloat16*>(a.Q) +
-                                       ((long)w.b * a.T + t) * a.q_ld + (long)h * DH
+                                       (long)w.b * a.q_bld + (long)t * a.q_ld + (long)h * DH
                                  : nullptr,
                               a.scale, qs, qr + lane);
           tc::fence_proxy_async_smem();
@@ -588,7 +588,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
           const int mn = wn.tile * 2 * kTile + r0 + lane, tn = row_token(a, mn);
           if (mn < a.M)
             l2_prefetch(static_cast<const __nv_bfloat16*>(a.Q) +
-                            ((long)wn.b * a.T + tn) * a.q_ld +
+                            (long)wn.b * a.q_bld + (long)tn * a.q_ld +
                             (long)(wn.hkv * a.G + (mn - tn * a.G)) * DH,
                         DH * 2);
         }

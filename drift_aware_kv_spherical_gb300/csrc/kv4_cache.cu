@@ -110,7 +110,7 @@ __device__ __forceinline__ bool block_at(const Kv4RowsArgs& a, BlockAt* o) {
   const long slot = (long)r + (a.off != nullptr ? a.off[b] : 0);
   if (slot < 0 || slot >= a.Ncache) return false;
   const int blk = lane % kBlocks;
-  o->src = ((long)b * a.R + r) * a.ld + (long)h * DH + blk * 16;
+  o->src = (long)b * a.b_ld + (long)r * a.ld + (long)h * DH + blk * 16;
   o->dst = (((long)b * a.Hkv + h) * a.Ncache + slot) * kBlocks + blk;
   return true;
 }

@@ -103,7 +103,7 @@ cudaError_t refresh_run(const RefreshArgs& a, cudaStream_t s);
 // the 4-bit KV cache (kv4_cache.cu, kv4_attn.cu, kv4_evict.cu); every array
 // pointer as in include/polestar.h
 struct Kv4RowsArgs {  // store: K, V -> cache; load: cache -> K, V
-  const void* K; const void* V; int dtype; int B, R, Hkv, Ncache, dh; long ld;
+  const void* K; const void* V; int dtype; int B, R, Hkv, Ncache, dh; long b_ld, ld;
   const int32_t* off; const int32_t* rows; const int32_t* cnt;
   uint8_t* kcode; uint8_t* kscale; uint8_t* vcode; uint8_t* vscale;
   float kmul, vmul;
@@ -113,7 +113,7 @@ cudaError_t kv4_rows_run(Kv4RowsArgs a, bool load, cudaStream_t s);
 
 struct Kv4AttnArgs {
   const uint8_t* kcode; const uint8_t* kscale; const uint8_t* vcode; const uint8_t* vscale;
-  const void* Q; int dtype; int B, T, Hq, Hkv, G, M, Ncache, dh; long q_ld;
+  const void* Q; int dtype; int B, T, Hq, Hkv, G, M, Ncache, dh; long q_bld, q_ld;
   uint64_t g_recip;     // ceil(2^40 / G)
   const int32_t* len; const int32_t* span; const int32_t* kpos; const int32_t* qpos;
   const float* slope;

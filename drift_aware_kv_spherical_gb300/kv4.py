@@ -1,0 +1,84 @@
+"""A layer's 4-bit KV cache as a decoder keeps it: the packed buffers, how far
+each sequence has filled them, what position each slot holds, and the attention
+weight its slots have drawn.
+
+All arithmetic is in the ps_kv4_* calls (include/polestar.h); this class owns
+their buffers and passes them on.  Until the first eviction slot n holds position
+n; afterwards `kpos` says which, for every KV head.
+"""
+
+import torch
+
+from . import polestar as ps
+
+
+class Kv4Layer:
+    """B sequences, Hkv KV heads of dh, up to N slots each; Hq query heads."""
+
+    def __init__(self, B, N, Hq, Hkv, dh, kmul=1.0, vmul=1.0, device="cuda"):
+        self.Hq = Hq
+        self.cache = ps.Kv4Cache.empty(B, Hkv, N, dh, kmul, vmul, device)
+        self.len = torch.zeros(B, dtype=torch.int32, device=device)
+        self.w = torch.zeros(B, Hkv, N, dtype=torch.float32, device=device)
+        self.kpos = None
+        self._spare = None
+        self._ws = {}
+
+    def _workspace(self, op, **sizes):
+        key = (op, *sorted(sizes.items()))
+        if key not in self._ws:
+            c = self.cache
+            self._ws[key] = ps.workspace(op, device=c.device, B=c.B, N=c.N, Hq=self.Hq, Hkv=c.Hkv,
+                                         dh=c.dh, **sizes)
+        return self._ws[key]
+
+    def store(self, K, V, off=None, rows=None, cnt=None, stream=None):
+        """Rows of K and V [B][R][Hkv][dh] into slots off[b] + r (see
+        ps.ps_kv4_store); `len` is the caller's to set."""
+        ps.ps_kv4_store(self.cache, K, V, off=off, rows=rows, cnt=cnt, stream=stream)
+
+    def append(self, K, V):
+        """K and V of the next T tokens of every sequence, behind what is there."""
+        if self.kpos is not None:
+            raise ValueError("append positions are not tracked after an eviction")
+        self.store(K, V, off=self.len)
+        self.len += K.shape[1]
+
+    def attend(self, Q, O, lse=None, *, scale=None, stream=None, **see):
+        """Attention of Q [B][T][Hq][dh] over the cache into O; `see`: span,
+        qpos, slope, cap as in ps.ps_kv4_attn."""
+        scale = self.cache.dh ** -0.5 if scale is None else scale
+        ps.ps_kv4_attn(self.cache, Q, O, lse, scale=scale, len=self.len, kpos=self.kpos,
+                       ws=self._workspace(ps.OP_KV4_ATTN, P=Q.shape[1]), stream=stream, **see)
+
+    def weigh(self, Q, lse, *, scale=None, stream=None, **see):
+        """Adds the weight that Q's rows put on every slot to `w`; lse as attend
+        wrote it for the same arguments."""
+        scale = self.cache.dh ** -0.5 if scale is None else scale
+        ps.ps_kv4_weight(self.cache, Q, lse, self.w, self.w, scale=scale, len=self.len,
+                         kpos=self.kpos, ws=self._workspace(ps.OP_KV4_WEIGHT, P=Q.shape[1]),
+                         stream=stream, **see)
+
+    def evict(self, keep, sink=0, recent=0, spare=None, stream=None):
+        """Cuts every sequence to `keep` slots: the first `sink`, the last
+        `recent`, the heaviest of the others.  The kept slots move to `spare`, a
+        cache of the same shape (made on the first call when not given), and the
+        old one becomes the next call's spare; layers of one shape can pass one
+        spare on: evict returns it."""
+        c = self.cache
+        i32 = dict(dtype=torch.int32, device=c.device)
+        if spare is not None:
+            self._spare = spare
+        if self._spare is None:
+            self._spare = dict(
+                cache=ps.Kv4Cache.empty(c.B, c.Hkv, c.N, c.dh, c.kmul, c.vmul, c.device),
+                w=torch.zeros_like(self.w), kpos=torch.zeros(c.B, c.Hkv, c.N, **i32),
+                len=torch.zeros(c.B, **i32))
+        d = self._spare
+        ps.ps_kv4_evict(c, d["cache"], self.w, d["w"], d["len"], keep, sink=sink, recent=recent,
+                        len=self.len, kpos=self.kpos, kpos_dst=d["kpos"],
+                        ws=self._workspace(ps.OP_KV4_EVICT, k=keep), stream=stream)
+        kpos = torch.zeros_like(d["kpos"]) if self.kpos is None else self.kpos
+        self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len)
+        self.cache, self.w, self.kpos, self.len = d["cache"], d["w"], d["kpos"], d["len"]
+        return self._spare

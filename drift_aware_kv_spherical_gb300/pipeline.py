@@ -22,6 +22,10 @@ the commit runs every step on the last drift computed, and suffix-block
 tokens commit only where the last layer's top-k position mask selects them
 [Polestar §2.B, suffix block commitment].
 
+With kv4=True each layer also keeps its cache in 4 bits (kv4.Kv4Layer): the
+rows a refresh rewrote are stored there behind it, and a block's attention
+reads that cache (`self.kv4[l].attend`).
+
 scorer selects the drift signal: the proxy's fused KL (default), or one of
 the ablation signals (cosine dissimilarity, entropy) computed by
 ps_drift_score over the same proxy distributions [Polestar §4, ablation
@@ -32,6 +36,7 @@ import torch
 
 from . import polestar as ps
 from . import workloads as wl
+from .kv4 import Kv4Layer
 
 
 class LayerState:
@@ -65,7 +70,7 @@ class Pipeline:
     """Buffers and the per-step call sequence for workload `w`."""
 
     def __init__(self, w, layers=None, device="cuda", offload=False, role=None,
-                 scorer=ps.SCORER_KL):
+                 scorer=ps.SCORER_KL, kv4=False, kmul=1.0, vmul=1.0):
         self.w = w
         self.scorer = scorer
         self.offload = offload
@@ -87,6 +92,12 @@ class Pipeline:
                 st.order = torch.zeros(B, N, dtype=torch.int32, device=device)
                 st.cl_off = torch.zeros(B, C + 1, dtype=torch.int32, device=device)
                 st.Ht = torch.zeros(B, N, d, dtype=torch.bfloat16, device=device)
+        self.kv4 = None
+        if kv4:
+            self.kv4 = [Kv4Layer(B, w.Ncache, w.Hq, w.Hkv, w.dh, kmul, vmul, device)
+                        for _ in range(self.layers)]
+            for layer in self.kv4:  # a window's cache is full once it is built
+                layer.len.fill_(N)
         P = w.P
         self.role = (wl.make_roles(w) if role is None else role).to(device)
         self.all_pos = torch.arange(N, dtype=torch.int32, device=device).repeat(B, 1)
@@ -164,6 +175,7 @@ class Pipeline:
                 main.wait_event(packed)
             ps.ps_refresh_kv(H, self.all_pos, self.all_npos, Wk, Wv, st.Kc, st.Vc, w.Hkv, w.dh,
                              ws=self.ws[ps.OP_REFRESH], stream=stream)
+            self._store_kv4(l, self.all_pos, self.all_npos, stream)
             return
         src = H
         if self.offload:  # the selected clusters' rows, fetched from the host store
@@ -174,6 +186,13 @@ class Pipeline:
             src = st.Ht
         ps.ps_refresh_kv(src, st.pos, st.npos, Wk, Wv, st.Kc, st.Vc, w.Hkv, w.dh,
                          ws=self.ws[ps.OP_REFRESH], stream=stream)
+        self._store_kv4(l, st.pos, st.npos, stream)
+
+    def _store_kv4(self, l, pos, npos, stream):
+        """The rows that a refresh rewrote, into the layer's 4-bit cache."""
+        if self.kv4 is not None:
+            st = self.state[l]
+            self.kv4[l].store(st.Kc, st.Vc, rows=pos, cnt=npos, stream=stream)
 
     def commit_step(self, logits, stream=None):
         w, last = self.w, self.state[-1]

@@ -96,8 +96,8 @@ _SIGS = {
                            _i, _i, _p, _sz, _p]),
     "ps_commit": (_i, [_p, _p, _i, _i, _i, _i, _p, _p, _p, _i, _p, _p, _p, _p, _i,
                        CommitParams, _p, _p, _p, _p, _sz, _p]),
-    "ps_kv4_store": (_i, [_p, _p, _p, _p, _i, _i, _i64, _p, _p, _p, _p]),
-    "ps_kv4_load": (_i, [_p, _p, _p, _p, _i, _i, _i64, _p, _p, _p, _p]),
+    "ps_kv4_store": (_i, [_p, _p, _p, _p, _i, _i, _i64, _i64, _p, _p, _p, _p]),
+    "ps_kv4_load": (_i, [_p, _p, _p, _p, _i, _i, _i64, _i64, _p, _p, _p, _p]),
     "ps_kv4_attn": (_i, [_p, _p, _p, _p, _p, _p, _sz, _p]),
     "ps_kv4_weight": (_i, [_p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "ps_kv4_evict": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
@@ -445,8 +445,8 @@ def _plain(t, dtype, shape, null=False):
 
 
 def _rows_ld(t, B, H, dh):
-    """(rows, elements between rows) of t [B][R][H][dh], whose rows may be
-    parts of wider ones."""
+    """(rows, elements between sequences, elements between rows) of t
+    [B][R][H][dh], whose rows may be parts of wider ones."""
     shape = t.shape
     if len(shape) != 4:
         raise ValueError(f"expected a device tensor [{B}][rows][heads][{dh}], got {tuple(shape)}")
@@ -454,26 +454,20 @@ def _rows_ld(t, B, H, dh):
     if b != B or h != H or d != dh or not t.is_cuda:
         raise ValueError(f"expected a device tensor [{B}][rows][{H}][{dh}], got {tuple(shape)}")
     if t.is_contiguous():
-        return R, H * dh
+        return R, R * H * dh, H * dh
     sb, sr, sh, sd = t.stride()
-    ok = sd == 1 and (sh == dh or H == 1)
-    if R > 1:
-        ok, ld = ok and (sb == R * sr or B == 1), sr
-    else:
-        ld = sb if B > 1 else H * dh
-    if not ok and t.numel() > 0:
-        raise ValueError(f"rows [{H}][{dh}] must be contiguous and equally spaced: strides "
-                         f"{t.stride()}")
-    return R, ld
+    if (sd != 1 or (sh != dh and H > 1)) and t.numel() > 0:
+        raise ValueError(f"rows [{H}][{dh}] must be contiguous: strides {t.stride()}")
+    return R, sb if B > 1 else 0, sr if R > 1 else H * dh
 
 
 def _kv4_rows(name, c, K, V, off, rows, cnt, stream):
-    R, ld = _rows_ld(K, c.B, c.Hkv, c.dh)
-    if V.dtype != K.dtype or V.shape != K.shape or _rows_ld(V, c.B, c.Hkv, c.dh) != (R, ld):
-        raise ValueError("K and V need one dtype, shape and row stride")
+    R, bld, ld = _rows_ld(K, c.B, c.Hkv, c.dh)
+    if V.dtype != K.dtype or V.shape != K.shape or _rows_ld(V, c.B, c.Hkv, c.dh) != (R, bld, ld):
+        raise ValueError("K and V need one dtype, shape and strides")
     lib = _lib()
     st = getattr(lib.cdll, name)(
-        lib.handle(c.index), c._c, K.data_ptr(), V.data_ptr(), _dtype(K), R, ld,
+        lib.handle(c.index), c._c, K.data_ptr(), V.data_ptr(), _dtype(K), R, bld, ld,
         _plain(off, torch.int32, (c.B,), True), _plain(rows, torch.int32, (c.B, R), True),
         _plain(cnt, torch.int32, (c.B,), True), _kv4_stream(stream, c))
     _check(st, name)
@@ -490,17 +484,17 @@ def ps_kv4_load(c, K, V, off=None, rows=None, cnt=None, stream=None):
     _kv4_rows("ps_kv4_load", c, K, V, off, rows, cnt, stream)
 
 
-_Q_PACK = struct.Struct("6Pq3i2f")
+_Q_PACK = struct.Struct("6P2q3i2f")
 
 
 def _kv4_query(c, Q, len, span, kpos, qpos, slope, scale, cap):
     Hq = Q.shape[2] if Q.dim() == 4 else 0
-    T, ld = _rows_ld(Q, c.B, Hq, c.dh)
+    T, bld, ld = _rows_ld(Q, c.B, Hq, c.dh)
     i32 = torch.int32
     return T, Hq, _Q_PACK.pack(
         Q.data_ptr(), _plain(len, i32, (c.B,), True), _plain(span, i32, (c.B, T, 2), True),
         _plain(kpos, i32, (c.B, c.Hkv, c.N), True), _plain(qpos, i32, (c.B, T), True),
-        _plain(slope, torch.float32, (Hq,), True), ld, _dtype(Q), T, Hq, scale, cap)
+        _plain(slope, torch.float32, (Hq,), True), bld, ld, _dtype(Q), T, Hq, scale, cap)
 
 
 def ps_kv4_attn(c, Q, O, lse=None, *, scale, len=None, span=None, kpos=None, qpos=None,

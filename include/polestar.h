@@ -497,20 +497,21 @@ typedef struct {
  * RNE, saturating, 0 where s == 0 (S = kmul or vmul): ps_nvfp4_residual's
  * rounding with a given tensor scale.  Bit-exact.  Infinities saturate, a NaN
  * becomes 6 s S.
- * K, V: element (b, r, h, i) at [(b*R + r)*ld + h*dh + i], f32 or bf16 (dtype);
- *   ld >= Hkv*dh, a multiple of 16 bytes (K and V may be parts of one
- *   projection's output);  off [B], rows [B][R], cnt [B] i32 or NULL.
+ * K, V: element (b, r, h, i) at [b*b_ld + r*ld + h*dh + i], f32 or bf16 (dtype);
+ *   ld >= Hkv*dh and b_ld >= 0, multiples of 16 bytes (K and V may be parts of
+ *   one projection's output);  off [B], rows [B][R], cnt [B] i32 or NULL.
  * A slot named twice in one call holds either row. */
 ps_status ps_kv4_store(ps_handle h, const ps_kv4_cache* c, const void* K,
-                       const void* V, int dtype, int R, int64_t ld,
-                       const int32_t* off, const int32_t* rows,
+                       const void* V, int dtype, int R, int64_t b_ld,
+                       int64_t ld, const int32_t* off, const int32_t* rows,
                        const int32_t* cnt, void* stream);
 
 /* The reverse, with the same list: element = fl(code * s * S) rounded to
  * dtype (bf16: RNE) into K and V; rows not listed are untouched. */
 ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V,
-                      int dtype, int R, int64_t ld, const int32_t* off,
-                      const int32_t* rows, const int32_t* cnt, void* stream);
+                      int dtype, int R, int64_t b_ld, int64_t ld,
+                      const int32_t* off, const int32_t* rows,
+                      const int32_t* cnt, void* stream);
 
 /* Queries of T tokens a sequence and what they see of the cache.
  *   s   = scale * <q, k>                       k as the cache holds it
@@ -520,7 +521,7 @@ ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V,
  * sees slot n iff n < len[b] (len NULL: Ncache) and span[b][t][0] <= pos <
  * span[b][t][1] (span NULL: all): causal is [0, qpos + 1), a prefix mask
  * [0, max(prefix, qpos + 1)), a document mask the document's bounds.
- * Q: element (b, t, h, i) at [(b*T + t)*q_ld + h*dh + i]; query head h reads
+ * Q: element (b, t, h, i) at [b*q_bld + t*q_ld + h*dh + i]; query head h reads
  * KV head h / (Hq / Hkv).  B * T * Hq <= 2^25 - 1, Hq / Hkv <= 4096. */
 typedef struct {
   const void* Q;
@@ -529,7 +530,7 @@ typedef struct {
   const int32_t* kpos;  /* [B][Hkv][Ncache] or NULL                         */
   const int32_t* qpos;  /* [B][T], needed with slope                        */
   const float* slope;   /* [Hq] or NULL                                     */
-  int64_t q_ld;         /* >= Hq*dh, a multiple of 16 bytes                 */
+  int64_t q_bld, q_ld;  /* >= 0 and >= Hq*dh, multiples of 16 bytes         */
   int dtype, T, Hq;     /* PS_F32 or PS_BF16; T >= 0 (0: no-op)             */
   float scale, cap;     /* finite; cap >= 0, 0 for none                     */
 } ps_kv4_query;

@@ -446,7 +446,7 @@ def test_refusals():
             bad_call()
     lib = ps.Library.load()
     assert lib.cdll.ps_kv4_attn(None, c._c, None, None, None, None, 0, None) == ps.PS_ERR_ARG
-    assert lib.cdll.ps_kv4_store(lib.handle(), None, None, None, 0, 1, 256, None, None, None,
+    assert lib.cdll.ps_kv4_store(lib.handle(), None, None, None, 0, 1, 256, 256, None, None, None,
                                  None) == ps.PS_ERR_ARG
     q = ps._kv4_query(c, Q, None, None, None, None, None, 1.0, 0.0)[2]
     off4 = ctypes.c_void_p(O.data_ptr() + 4)
