@@ -96,17 +96,18 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
   }
 }
 
-// A warp's own ring of 16-slot steps in shared memory, filled with cp.async
-// well ahead of use: codes and scales as they lie in the cache.  (Loaded
-// straight into registers one step ahead, too few bytes were in flight: 90 us
-// against 54 with V left out, on 64 K slots x 8 sequences x 4 heads.)
-constexpr int kStages = 4;
+// A warp's own two stages of 32 slots (two 16-slot steps) in shared memory, one
+// filled with cp.async while the other is used: codes and scales as they lie in
+// the cache.  (Loaded straight into registers one step ahead, too few bytes were
+// in flight: 90 us against 54 with V left out, on 64 K slots x 8 sequences x 4
+// heads.)
+constexpr int kStep = 32;
 template <int DH, bool WITH_V>
 struct Ring {
-  static constexpr int kCode = 16 * (DH / 2), kScale = 16 * (DH / 16);
+  static constexpr int kCode = kStep * (DH / 2), kScale = kStep * (DH / 16);
   static constexpr int kV = kCode + kScale;            // V's codes, then its scales
   static constexpr int kStage = WITH_V ? 2 * kV : kV;
-  static constexpr int kBytes = kStages * kStage;
+  static constexpr int kBytes = 2 * kStage;
 };
 
 template <int BYTES>
@@ -126,54 +127,55 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Fills a lane's part of the stages, one 16-slot step after another `stride`
-// slots on: the pieces of codes lane, lane + 32, ...; K's scales of slot lane
-// (lanes 0-15), V's of slot lane - 16.  Zeros past the cache.
+// Fills a lane's part of the stages, kStep slots at a time, `stride` slots on each
+// time: the 16-byte pieces of codes lane, lane + 32, ..., and the scales of slot
+// `lane`.  Zeros past the cache.
 template <int DH, bool WITH_V>
 struct RingFill {
   using R = Ring<DH, WITH_V>;
-  const uint8_t *kc, *vc, *sc;
-  uint32_t scale_at;
-  int left, piece, slot;
+  static constexpr int kPieces = DH / 32;  // of codes a lane
+  const uint8_t *kc, *vc, *ks, *vs;
+  int left;
 
   __device__ __forceinline__ RingFill(const Kv4AttnArgs& a, long bh, int n) {
     const int lane = threadIdx.x & 31;
     const long row = bh * a.Ncache + n;
-    slot = lane & 15;
-    piece = lane / (DH / 32);  // the slot of the lane's first piece
     left = a.Ncache - n;
     kc = a.kcode + row * (DH / 2) + lane * 16;
     vc = a.vcode + row * (DH / 2) + lane * 16;
-    sc = (lane >= 16 ? a.vscale : a.kscale) + (row + slot) * (DH / 16);
-    scale_at = R::kCode + (lane >= 16 ? R::kV : 0) + slot * (DH / 16);
-    if (!WITH_V && lane >= 16) slot = 1 << 30;  // nothing to do
+    ks = a.kscale + (row + lane) * (DH / 16);
+    vs = a.vscale + (row + lane) * (DH / 16);
   }
   __device__ __forceinline__ void next(uint32_t dst, int stride) {
     const int lane = threadIdx.x & 31;
-    const uint32_t d = dst + lane * 16;
-    if (left >= 16) {  // warp-uniform
+    const uint32_t d = dst + lane * 16, sd = dst + R::kCode + lane * (DH / 16);
+    if (left >= kStep) {  // warp-uniform
 #pragma unroll
-      for (int i = 0; i < DH / 64; ++i) {
+      for (int i = 0; i < kPieces; ++i) {
         cp_async<16>(d + 512 * i, kc + 512 * i, true);
         if constexpr (WITH_V) cp_async<16>(d + R::kV + 512 * i, vc + 512 * i, true);
       }
-      if (slot < 16) cp_async<DH / 16>(dst + scale_at, sc, true);
+      cp_async<DH / 16>(sd, ks, true);
+      if constexpr (WITH_V) cp_async<DH / 16>(sd + R::kV, vs, true);
     } else {
 #pragma unroll
-      for (int i = 0; i < DH / 64; ++i) {
-        const bool in = piece + i * (1024 / DH) < left;
+      for (int i = 0; i < kPieces; ++i) {
+        const bool in = lane / (DH / 32) + i * (1024 / DH) < left;
         cp_async<16>(d + 512 * i, in ? kc + 512 * i : kc - lane * 16, in);
         if constexpr (WITH_V)
           cp_async<16>(d + R::kV + 512 * i, in ? vc + 512 * i : vc - lane * 16, in);
       }
-      if (slot < 16) {
-        const bool in = slot < left;
-        cp_async<DH / 16>(dst + scale_at, in ? sc : sc - slot * (DH / 16), in);
-      }
+      const bool in = lane < left;
+      const int back = in ? 0 : lane * (DH / 16);
+      cp_async<DH / 16>(sd, ks - back, in);
+      if constexpr (WITH_V) cp_async<DH / 16>(sd + R::kV, vs - back, in);
     }
     kc += (long)stride * (DH / 2);
-    if constexpr (WITH_V) vc += (long)stride * (DH / 2);
-    sc += (long)stride * (DH / 16);
+    ks += (long)stride * (DH / 16);
+    if constexpr (WITH_V) {
+      vc += (long)stride * (DH / 2);
+      vs += (long)stride * (DH / 16);
+    }
     left -= stride;
   }
 };
@@ -184,7 +186,7 @@ struct RingFill {
 // twice).
 __device__ __forceinline__ int slot_at(int r) { return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1); }
 
-// What a lane reads of a stage: K of slots slot_at(g) and slot_at(g) + 8,
+// What a lane reads of step h of a stage: K of slots slot_at(g) and slot_at(g) + 8,
 // elements [t dh/4, (t+1) dh/4); V of slots t + 4 j, elements [g dh/8, (g+1)
 // dh/8); the block scales that go with them.
 template <int DH>
@@ -199,12 +201,12 @@ struct RawV {
 };
 
 template <int DH>
-__device__ __forceinline__ void read_k(const uint8_t* st, int g, int t, RawK<DH>& o) {
+__device__ __forceinline__ void read_k(const uint8_t* st, int h, int g, int t, RawK<DH>& o) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int slot = slot_at(g) + 8 * j;
+    const int slot = 16 * h + slot_at(g) + 8 * j;
     const uint8_t* p = st + slot * (DH / 2) + t * (DH / 8);
-    const uint8_t* q = st + 16 * (DH / 2) + slot * (DH / 16) + t * (DH / 64);
+    const uint8_t* q = st + kStep * (DH / 2) + slot * (DH / 16) + t * (DH / 64);
     if constexpr (DH == 64) {
       const uint2 v = *reinterpret_cast<const uint2*>(p);
       o.c[j][0] = v.x; o.c[j][1] = v.y;
@@ -223,12 +225,12 @@ __device__ __forceinline__ void read_k(const uint8_t* st, int g, int t, RawK<DH>
 }
 
 template <int DH>
-__device__ __forceinline__ void read_v(const uint8_t* st, int g, int t, RawV<DH>& o) {
+__device__ __forceinline__ void read_v(const uint8_t* st, int h, int g, int t, RawV<DH>& o) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int slot = t + 4 * j;
+    const int slot = 16 * h + t + 4 * j;
     const uint8_t* p = st + slot * (DH / 2) + g * (DH / 16);
-    const uint8_t* q = st + 16 * (DH / 2) + slot * (DH / 16);
+    const uint8_t* q = st + kStep * (DH / 2) + slot * (DH / 16);
     if constexpr (DH == 64) {
       o.c[j][0] = *reinterpret_cast<const uint32_t*>(p);
       o.s[j] = q[g >> 1];
@@ -360,27 +362,24 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       lrow[nb][u] = 0.f;
     }
   }
-  RingFill<DH, true> fill(a, bh, n_lo + 16 * warp);
-  int ahead = n_lo + 16 * warp;
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (ahead < n_hi) fill.next(ring32 + i * R::kStage, 16 * kWarps);
-    ahead += 16 * kWarps;
-    cp_commit();
-  }
+  RingFill<DH, true> fill(a, bh, n_lo + kStep * warp);
+  if (n_lo + kStep * warp < n_hi) fill.next(ring32, kStep * kWarps);
+  cp_commit();
   const int sg = slot_at(g);
-  uint32_t at = 0, to = (kStages - 1) * R::kStage;  // stage to read, stage to fill
-  for (int n = n_lo + 16 * warp; n < n_hi; n += 16 * kWarps) {
-    cp_wait<kStages - 2>();
-    __syncwarp();  // the step has arrived, and the one before it has been read by every lane
-    if (ahead < n_hi) fill.next(ring32 + to, 16 * kWarps);
-    ahead += 16 * kWarps;
+  uint32_t at = 0;  // the stage to read
+  for (int n2 = n_lo + kStep * warp; n2 < n_hi; n2 += kStep * kWarps) {
+    cp_wait<0>();
+    __syncwarp();  // the stage has arrived, and the other has been read by every lane
+    if (n2 + kStep * kWarps < n_hi) fill.next(ring32 + (at ^ R::kStage), kStep * kWarps);
     cp_commit();
     const uint8_t* st = ring + at;
-    to = at;
-    at = at + R::kStage == R::kBytes ? 0 : at + R::kStage;
+    at ^= R::kStage;
+#pragma unroll
+    for (int half = 0; half < kStep / 16; ++half) {
+    const int n = n2 + 16 * half;
+    if (n >= n_hi) break;
     RawK<DH> rk;
-    read_k<DH>(st, g, t, rk);
+    read_k<DH>(st, half, g, t, rk);
     // S^T: slots sg and sg + 8 (c / 2), rows 2 t and 2 t + 1 (c & 1) of block nb
     float s[NB][4];
 #pragma unroll
@@ -489,7 +488,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     }
     // O^T += V^T P^T
     RawV<DH> rv;
-    read_v<DH>(st + R::kV, g, t, rv);
+    read_v<DH>(st + R::kV, half, g, t, rv);
 #pragma unroll
     for (int w = 0; w < DH / 64; ++w) {
       uint32_t v[2][2][4];  // [even, odd element][slots t and t + 4, t + 8 and t + 12][byte]
@@ -527,6 +526,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
           }
         }
       }
+    }
     }
   }
 
@@ -672,6 +672,7 @@ k_kv4_combine(const __grid_constant__ Kv4AttnArgs a) {
 // every slot's sum is one warp's, in row order, so the result does not depend
 // on timing.
 constexpr int kWRows = 64;
+constexpr int kGroup = kStep * kWarps;  // slots that a CTA takes at a time
 
 // The slots that some row, and that every row, of those in shared memory sees.
 struct SeenRange {
@@ -756,9 +757,9 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
   const int len = kv4_len(a, b), last = a.Ncache - 1;
   const int32_t* kpos = GEN && a.kpos != nullptr ? a.kpos + (long)bh * a.Ncache : nullptr;
   const int chunks = ONE ? 1 : ceil_div(a.M, kWRows);
-  const int n0 = (blockIdx.x * steps) * 64 + 16 * warp;
+  const int n0 = (blockIdx.x * steps) * kGroup + kStep * warp;
   // the warp's steps that hold slots of the sequence; all warps' for the barriers
-  const int live = max(0, min(steps, ceil_div(len - n0, 64)));
+  const int live = max(0, min(steps, ceil_div(len - n0, kGroup)));
   const int sg = slot_at(g);
   // lanes t < 2 write slot sg + 8 t
   const float* w_in = a.w_in != nullptr ? a.w_in + (long)bh * a.Ncache + n0 + sg + 8 * t : nullptr;
@@ -768,12 +769,9 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
       reinterpret_cast<uint8_t*>(qs + (kWRows / 8) * P * (KS / 2) * 32) + warp * R::kBytes;
   const uint32_t ring32 = tc::smem_u32(ring);
   RingFill<DH, false> fill(a, bh, n0);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i < live) fill.next(ring32 + i * R::kStage, 64);
-    cp_commit();
-  }
-  uint32_t at = 0, to = (kStages - 1) * R::kStage;  // stage to read, stage to fill
+  if (live > 0) fill.next(ring32, kGroup);
+  cp_commit();
+  uint32_t at = 0;  // the stage to read
   const bool spans = a.span != nullptr && kpos == nullptr;
   SeenRange seen{0, len, 0, kpos != nullptr && a.span != nullptr ? -1 : len};
   int nbs = 0;
@@ -784,59 +782,68 @@ k_kv4_weight(const __grid_constant__ Kv4AttnArgs a, int steps) {
     nbs = ceil_div(a.M, 8);
   }
   const int all = ONE ? live : steps;
-  int n = n0;
-  for (int st = 0; st < all; ++st, n += 64) {
-    uint32_t kf[KS][4];
-    int pos[2] = {n + sg, n + sg + 8};
-    float acc[2] = {0.f, 0.f};  // slots sg and sg + 8
-    const float old = w_in != nullptr && room > 0 ? *w_in : 0.f;  // asked for early
-    cp_wait<kStages - 2>();
+  int n2 = n0;
+  for (int st = 0; st < all; ++st, n2 += kGroup) {
+    float old[kStep / 16];  // asked for early
+#pragma unroll
+    for (int h = 0; h < kStep / 16; ++h)
+      old[h] = w_in != nullptr && room > 16 * h ? w_in[16 * h] : 0.f;
+    cp_wait<0>();
     __syncwarp();
-    if (st + kStages - 1 < live) fill.next(ring32 + to, 64);
+    if (st + 1 < live) fill.next(ring32 + (at ^ R::kStage), kGroup);
     cp_commit();
-    if (ONE || st < live) {
-      RawK<DH> rk;
-      read_k<DH>(ring + at, g, t, rk);
 #pragma unroll
-      for (int w = 0; w < KS / 2; ++w) dequant_k<DH>(rk, w, kf[2 * w], kf[2 * w + 1]);
-      if (GEN && kpos != nullptr) {
-        pos[0] = __ldg(kpos + min(pos[0], last));
-        pos[1] = __ldg(kpos + min(pos[1], last));
+    for (int h = 0; h < kStep / 16; ++h) {
+      const int n = n2 + 16 * h;
+      uint32_t kf[KS][4];
+      int pos[2] = {n + sg, n + sg + 8};
+      float acc[2] = {0.f, 0.f};  // slots sg and sg + 8
+      const bool here = n < len;  // warp-uniform
+      if (here) {
+        RawK<DH> rk;
+        read_k<DH>(ring + at, h, g, t, rk);
+#pragma unroll
+        for (int w = 0; w < KS / 2; ++w) dequant_k<DH>(rk, w, kf[2 * w], kf[2 * w + 1]);
+        if (GEN && kpos != nullptr) {
+          pos[0] = __ldg(kpos + min(pos[0], last));
+          pos[1] = __ldg(kpos + min(pos[1], last));
+        }
       }
-    }
-    to = at;
-    at = at + R::kStage == R::kBytes ? 0 : at + R::kStage;
-    if constexpr (ONE) {
-      if (n < seen.any_hi && n + 16 > seen.any_lo)
-        weigh<DH, F32, GEN>(a, kf, qs + lane, par + 2 * t, nbs, n + sg, len, pos,
-                            n < seen.all_lo || n + 16 > seen.all_hi, acc);
-    } else {
-      for (int ch = 0; ch < chunks; ++ch) {
-        const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
-        __syncthreads();
-        stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
-        __syncthreads();
-        if (spans) seen = seen_range(par, rows, len);
-        if (st < live && n < seen.any_hi && n + 16 > seen.any_lo)
-          weigh<DH, F32, GEN>(a, kf, qs + lane, par + 2 * t, ceil_div(rows, 8), n + sg, len, pos,
+      if constexpr (ONE) {
+        if (here && n < seen.any_hi && n + 16 > seen.any_lo)
+          weigh<DH, F32, GEN>(a, kf, qs + lane, par + 2 * t, nbs, n + sg, len, pos,
                               n < seen.all_lo || n + 16 > seen.all_hi, acc);
+      } else {
+        for (int ch = 0; ch < chunks; ++ch) {
+          const int m0 = ch * kWRows, rows = min(kWRows, a.M - m0);
+          __syncthreads();
+          stage_rows<DH, F32>(a, b, hkv, m0, (rows + 7) & ~7, qs, par);
+          __syncthreads();
+          if (spans) seen = seen_range(par, rows, len);
+          if (here && n < seen.any_hi && n + 16 > seen.any_lo)
+            weigh<DH, F32, GEN>(a, kf, qs + lane, par + 2 * t, ceil_div(rows, 8), n + sg, len, pos,
+                                n < seen.all_lo || n + 16 > seen.all_hi, acc);
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 1);
-      acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 2);
+      for (int j = 0; j < 2; ++j) {
+        acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 1);
+        acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 2);
+      }
+      if (room > 16 * h) w_out[16 * h] = old[h] + (t == 0 ? acc[0] : acc[1]);
     }
-    if (room > 0) *w_out = old + (t == 0 ? acc[0] : acc[1]);
-    if (w_in != nullptr) w_in += 64;
-    w_out += 64;
-    room -= 64;
+    at ^= R::kStage;
+    if (w_in != nullptr) w_in += kGroup;
+    w_out += kGroup;
+    room -= kGroup;
   }
   for (int st = all; st < steps; ++st) {  // past the sequence
-    if (room > 0) *w_out = w_in != nullptr ? *w_in : 0.f;
-    if (w_in != nullptr) w_in += 64;
-    w_out += 64;
-    room -= 64;
+#pragma unroll
+    for (int h = 0; h < kStep / 16; ++h)
+      if (room > 16 * h) w_out[16 * h] = w_in != nullptr ? w_in[16 * h] : 0.f;
+    if (w_in != nullptr) w_in += kGroup;
+    w_out += kGroup;
+    room -= kGroup;
   }
   cp_wait<0>();  // no copy is under way when the CTA leaves
 }
@@ -893,12 +900,12 @@ cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  // rows that fit shared memory are staged once for all the 64-slot groups of
-  // a CTA, as many as leave six CTAs an SM
-  const int groups = ceil_div(a.Ncache, 64);
+  // rows that fit shared memory are staged once for all the slot groups of
+  // a CTA, as many as leave eight CTAs an SM
+  const int groups = ceil_div(a.Ncache, kGroup);
   int steps = 1;
   if (ONE) {
-    steps = (int)((long)groups * a.B * a.Hkv / (6 * kSmTarget));
+    steps = (int)((long)groups * a.B * a.Hkv / (8 * kSmTarget));
     steps = steps < 1 ? 1 : steps > 64 ? 64 : steps;
   }
   return launch_pdl(kern, dim3((unsigned)ceil_div(groups, steps), a.B * a.Hkv), dim3(kThreads),
@@ -936,7 +943,7 @@ AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   p.ntile = ceil_div(M, 8 * p.nb);
   const long base = (long)B * Hkv * p.ntile;
   const int most = ceil_div(N, 128);  // at least 128 slots a share
-  long want = ceil_div(6 * kSmTarget, base);
+  long want = ceil_div(7 * kSmTarget, base);
   if (want > most) want = most;
   if (want > 256) want = 256;
   p.nsplit = (int)(want < 1 ? 1 : want);
