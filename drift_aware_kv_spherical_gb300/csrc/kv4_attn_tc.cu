@@ -209,18 +209,36 @@ __device__ __forceinline__ void put_row(uint8_t* op, int r, const RawRow<DH>& v)
 }
 
 // ---------------------------------------------------------------- queries
-// A softmax thread stages its own row as row r of the f16 operand at qs (zero
-// where src is null) and returns its score factor.  The lanes of a load lie in
-// different rows, but no lane needs another's maximum: staged by DH / 8 lanes a
-// row the same work took three times the instructions.
+// The 32 query rows of a softmax warp into their place in the operand, as they
+// are (bf16, the size of the f16 they become): cp.async in whole rows.  `src` is
+// the lane's own row, null past the last one: zeros (never stored, but a vote of
+// the warp must not hang on what was there).
 template <int DH>
-__device__ __forceinline__ float stage_q(const __nv_bfloat16* src, float scale, uint8_t* qs,
-                                         int r) {
-  uint4 v[DH / 8];
+__device__ __forceinline__ void fetch_q(const void* any, const __nv_bfloat16* src, uint32_t qs,
+                                        int r) {
+  constexpr int LN = DH / 8, RP = 32 / LN;  // lanes a row, rows a pass
+  const int lane = threadIdx.x & 31, sub = lane % LN;
 #pragma unroll
-  for (int c = 0; c < DH / 8; ++c)
-    v[c] = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + c)
-                          : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < 32 / RP; ++i) {
+    const int rr = i * RP + lane / LN;
+    const unsigned long long from =
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), rr);
+    const void* at = from != 0 ? reinterpret_cast<const void*>(from + sub * 16) : any;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + sw128(r + rr, sub)),
+                 "l"(at), "r"(from != 0 ? 16 : 0)
+                 : "memory");
+  }
+}
+// The lane's row (row r of the operand at qs) from bf16 to f16 in place; returns
+// its score factor.  (Read from global memory by the lanes themselves, 32 rows a
+// load, the same took three times as long.)
+template <int DH>
+__device__ __forceinline__ float stage_q(float scale, uint8_t* qs, int r) {
+  uint4 v[DH / 8];
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < DH / 8; ++c) v[c] = *reinterpret_cast<const uint4*>(qs + sw128(r, c));
   __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);  // NaN elements do not count
 #pragma unroll
   for (int c = 0; c < DH / 8; ++c) {
@@ -542,10 +560,11 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
         TcRow row = tc_row(a, in, w.b, t, h);
         range = tc_range(row);
         if (act) {
-          row.f = stage_q<DH>(in ? static_cast<const __nv_bfloat16*>(a.Q) +
-                                       (long)w.b * a.q_bld + (long)t * a.q_ld + (long)h * DH
-                                 : nullptr,
-                              a.scale, qs, qr + lane);
+          fetch_q<DH>(a.Q, in ? static_cast<const __nv_bfloat16*>(a.Q) + (long)w.b * a.q_bld +
+                               (long)t * a.q_ld + (long)h * DH
+                         : nullptr,
+                      tc::smem_u32(qs), qr);
+          row.f = stage_q<DH>(a.scale, qs, qr + lane);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(q_full + g);
