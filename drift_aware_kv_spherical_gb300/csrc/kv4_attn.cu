@@ -263,8 +263,29 @@ __device__ __forceinline__ void dequant_k(const RawK<DH>& r, int w, uint32_t* a0
   }
 }
 
-// Codes of word w of slots a and b (a = 2 j2) interleaved before they are
-// converted: byte q of *even holds element 2 q of both, of *odd element 2 q + 1.
+// s += two steps' products of K with the queries: hi (and for fp32 queries lo).
+// The tensor cores truncate what they add to an accumulator, by up to 2^-23 of
+// it each time, and a chain of 16 of them showed in fp32 weights (1.4e-6): fp32
+// products of 32 elements are added by a rounding instruction.
+template <bool F32>
+__device__ __forceinline__ void add_products(float* s, const uint32_t* a0, const uint32_t* a1,
+                                             const uint4& hi, const uint4& lo) {
+  if constexpr (F32) {
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_f16(d, a0, lo.x, lo.y);
+    mma_f16(d, a1, lo.z, lo.w);
+    mma_f16(d, a0, hi.x, hi.y);
+    mma_f16(d, a1, hi.z, hi.w);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[c] += d[c];
+  } else {
+    mma_f16(s, a0, hi.x, hi.y);
+    mma_f16(s, a1, hi.z, hi.w);
+  }
+}
+
+// Codes of word w of slots a and b interleaved before they are converted: byte q
+// of *even holds element 2 q of both, of *odd element 2 q + 1.
 __device__ __forceinline__ void pair_codes(uint32_t a, uint32_t b, uint32_t* even, uint32_t* odd) {
   *even = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
   *odd = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
@@ -392,12 +413,10 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       dequant_k<DH>(rk, w, a0, a1);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const uint4 q = qs[((nb * P + p) * (KS / 2) + w) * 32 + lane];
-          mma_f16(s[nb], a0, q.x, q.y);
-          mma_f16(s[nb], a1, q.z, q.w);
-        }
+{
+        const uint4* q = qs + (nb * P * (KS / 2) + w) * 32 + lane;
+        add_products<F32>(s[nb], a0, a1, q[0], q[(P - 1) * (KS / 2) * 32]);
+      }
     }
     const bool masked = n < all_lo || n + 16 > all_hi;
     int pos[2] = {n + sg, n + sg + 8};
@@ -513,9 +532,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
         for (int nb = 0; nb < NB; ++nb) {
           float* d = o[nb][4 * w + q];
           if constexpr (F32) {
-            // the tensor cores truncate what they add to an accumulator: over
-            // thousands of steps that shows in fp32, so each step's product is
-            // added by a rounding instruction
+            // added by a rounding instruction, as the scores
             float e[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16(e, av, ph[nb][0], ph[nb][1]);
             mma_f16(e, av, pl[nb][0], pl[nb][1]);
@@ -708,12 +725,7 @@ __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < KS / 2; ++w)
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint4 q = qp[(p * (KS / 2) + w) * 32];
-        mma_f16(s, kf[2 * w], q.x, q.y);
-        mma_f16(s, kf[2 * w + 1], q.z, q.w);
-      }
+      add_products<F32>(s, kf[2 * w], kf[2 * w + 1], qp[w * 32], qp[((P - 1) * (KS / 2) + w) * 32]);
     // score - lse of slots sg, sg + 8 (c / 2), rows 2 t, 2 t + 1 (c & 1)
     float x[4];
     const float f0 = rp[0].f, l0 = -rp[0].lse, f1 = rp[1].f, l1 = -rp[1].lse;
