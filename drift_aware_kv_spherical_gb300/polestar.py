@@ -463,7 +463,8 @@ def _rows_ld(t, B, H, dh):
 
 def _kv4_rows(name, c, K, V, off, rows, cnt, stream):
     R, bld, ld = _rows_ld(K, c.B, c.Hkv, c.dh)
-    if V.dtype != K.dtype or V.shape != K.shape or _rows_ld(V, c.B, c.Hkv, c.dh) != (R, bld, ld):
+    if (V.dtype != K.dtype or V.shape != K.shape or not V.is_cuda or
+            (V.stride() != K.stride() and _rows_ld(V, c.B, c.Hkv, c.dh) != (R, bld, ld))):
         raise ValueError("K and V need one dtype, shape and strides")
     lib = _lib()
     st = getattr(lib.cdll, name)(
