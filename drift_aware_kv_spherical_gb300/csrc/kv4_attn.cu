@@ -337,14 +337,11 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     all_lo = __reduce_max_sync(0xffffffffu, row ? lo : INT32_MIN);
     all_hi = min(len, __reduce_min_sync(0xffffffffu, row ? hi : INT32_MAX));
   }
-  // This CTA's share, whole 64-slot groups: of the slots seen where spans pick
-  // them, else of the cache, so that all shares take as long and sequences of
-  // unequal length just have fewer of them.
+  // This CTA's share of the slots seen, whole 64-slot groups
   if (n_lo >= n_hi) {
     n_lo = n_hi = 0;
   } else if (a.nsplit > 1) {
-    const int of = a.span != nullptr ? n_hi - n_lo : a.Ncache;
-    const int share = ceil_div(ceil_div(of, 64), a.nsplit) * 64;
+    const int share = ceil_div(ceil_div(n_hi - n_lo, 64), a.nsplit) * 64;
     n_lo = (int)min((long)n_hi, n_lo + (long)split * share);
     n_hi = (int)min((long)n_hi, (long)n_lo + share);
   }
@@ -913,12 +910,14 @@ cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
     attr_set = true;
   }
   // rows that fit shared memory are staged once for all the slot groups of
-  // a CTA, as many as leave eight CTAs an SM
+  // a CTA, as many as leave five CTAs an SM, which is what its registers hold
+  // (against eight: a token on 64 K slots 7.6 us for 9.3, on 4 sequences of 12 K
+  // 6.0 for 7.3, on 8 of 32 K 18.6 for 19.1, 32-token blocks on 4 K 25.7 for 24.3)
   const int groups = ceil_div(a.Ncache, kGroup);
   int steps = 1;
   if (ONE) {
-    steps = (int)((long)groups * a.B * a.Hkv / (8 * kSmTarget));
-    steps = steps < 1 ? 1 : steps > 64 ? 64 : steps;
+    steps = ceil_div((long)groups * a.B * a.Hkv, 5 * kSmTarget);
+    if (steps > 64) steps = 64;
   }
   return launch_pdl(kern, dim3((unsigned)ceil_div(groups, steps), a.B * a.Hkv), dim3(kThreads),
                     smem, s, a, steps);
@@ -955,7 +954,11 @@ AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   p.ntile = ceil_div(M, 8 * p.nb);
   const long base = (long)B * Hkv * p.ntile;
   const int most = ceil_div(N, 128);  // at least 128 slots a share
-  long want = ceil_div(7 * kSmTarget, base);
+  // CTAs that run side by side, 4 a SM of 8 rows and 2 of more: no second round
+  // of them that leaves SMs idle.  Against 7 a SM in rounds: 8 sequences of 64 K
+  // slots 59 us for 71 (lengths of 1/2 to 1: 51 for 50), of 6000 slots 14.5 for
+  // 20; 16 rows and 32 K slots 53 for 73; with 5 and 3 a SM 62, 16 and 68.
+  long want = (p.nb == 1 ? 4 : 2) * kSmTarget / base;
   if (want > most) want = most;
   if (want > 256) want = 256;
   p.nsplit = (int)(want < 1 ? 1 : want);
