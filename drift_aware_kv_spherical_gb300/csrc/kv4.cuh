@@ -125,25 +125,6 @@ __device__ __forceinline__ void row_scale(float mx, float scale, float* up, floa
   *f = fmaxf(fabsf(scale) * __uint_as_float((uint32_t)(127 - ex) << 23), FLT_MIN);
 }
 
-// The score of a raw product in natural units, before the mask.
-template <bool ACC>
-__device__ __forceinline__ float kv4_score(const Kv4AttnArgs& a, float raw, float f, float slope,
-                                           int qpos, int pos) {
-  float x = raw * f;
-  if (a.cap > 0.f) {
-    if constexpr (ACC) {
-      x = a.cap * tanhf(x * a.inv_cap);
-    } else {
-      // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7, which the cap
-      // scales to under 1e-5 of a score, far below P's own rounding
-      const float e = exp2_approx(x * a.inv_cap * (2.f * kLog2e));
-      x = a.cap * (1.f - 2.f * rcp_approx(e + 1.f));
-    }
-  }
-  if (a.slope != nullptr) x -= slope * fabsf((float)(qpos - pos));
-  return x;
-}
-
 // lse of a row whose sum l is of 2^(x - mx + kPShift), x its log2-unit scores
 // (mx = -inf: nothing but NaN was seen, or nothing at all and l == 0).
 __device__ __forceinline__ float row_lse(float mx, float l) {

@@ -685,6 +685,7 @@ k_kv4_combine(const __grid_constant__ Kv4AttnArgs a) {
 // while all rows of the head pass by (kWRows at a time through shared memory);
 // every slot's sum is one warp's, in row order, so the result does not depend
 // on timing.
+constexpr int kTcWeight = 64;
 constexpr int kWRows = 64;
 constexpr int kGroup = kStep * kWarps;  // slots that a CTA takes at a time
 
@@ -1025,6 +1026,7 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
 }
 
 cudaError_t kv4_weight_run(const Kv4AttnArgs& a, cudaStream_t s) {
+  if (a.dtype == PS_BF16 && a.dh <= 128 && a.M > kTcWeight) return kv4_weight_tc_launch(a, s);
   const bool gen = a.cap > 0.f || a.slope != nullptr || a.kpos != nullptr;
   const bool one = a.M <= kWRows;
 #define PS_KV4_CASE(DH)                                                       \

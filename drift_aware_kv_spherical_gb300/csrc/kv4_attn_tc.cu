@@ -25,8 +25,7 @@
 // to that.
 // Every mbarrier wait is bounded (tc::mbar_wait); after a timeout the CTA waits
 // for the MMAs it issued, frees TMEM and returns with the status word set.
-#include "kv4.cuh"
-#include "tc.cuh"
+#include "kv4_tc.cuh"
 
 namespace ps {
 namespace {
@@ -46,23 +45,6 @@ struct TcSmem {
   static constexpr uint32_t kBar = kWork + 8 * 64;
   static constexpr size_t kBytes = 1024 + kBar + 256;
 };
-
-// Byte offset of 16-byte chunk c (of DH / 8) of row r in an operand.
-__device__ __forceinline__ uint32_t sw128(int r, int c) {
-  return (uint32_t)(c >> 3) * 16384u + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-}
-
-// One lane of a converged warp.  The MMAs below are issued under this and not
-// under `lane == 0`: the operands of tcgen05.mma live in uniform registers, and
-// under a thread-indexed branch each instruction took 120 clocks to issue
-// (measured; 64 elected, the rate of the tensor cores at this size).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 
 // D(tmem) (+)= A . B, f16 operands: A from shared memory, or from TMEM.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -165,25 +147,6 @@ __device__ __forceinline__ void l2_prefetch(const void* p, int bytes) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + o));
 }
 
-// Codes and scales of one slot's row (K or V).
-template <int DH>
-struct RawRow {
-  uint4 c[DH / 32];
-  uint2 s;
-};
-template <int DH>
-__device__ __forceinline__ void load_row(const uint8_t* codes, const uint8_t* scales, long slot,
-                                         RawRow<DH>& o) {
-  const uint4* p = reinterpret_cast<const uint4*>(codes + slot * (DH / 2));
-#pragma unroll
-  for (int i = 0; i < DH / 32; ++i) o.c[i] = __ldg(p + i);
-  if constexpr (DH == 128) {
-    o.s = __ldg(reinterpret_cast<const uint2*>(scales + slot * 8));
-  } else {
-    o.s.x = __ldg(reinterpret_cast<const uint32_t*>(scales + slot * 4));
-    o.s.y = 0;
-  }
-}
 // The row as f16 into row r of an operand: 16-byte chunks, eight elements each,
 // two to a scale, two scales to a conversion.
 template <int DH>
@@ -209,26 +172,6 @@ __device__ __forceinline__ void put_row(uint8_t* op, int r, const RawRow<DH>& v)
 }
 
 // ---------------------------------------------------------------- queries
-// The 32 query rows of a softmax warp into their place in the operand, as they
-// are (bf16, the size of the f16 they become): cp.async in whole rows.  `src` is
-// the lane's own row, null past the last one: zeros (never stored, but a vote of
-// the warp must not hang on what was there).
-template <int DH>
-__device__ __forceinline__ void fetch_q(const void* any, const __nv_bfloat16* src, uint32_t qs,
-                                        int r) {
-  constexpr int LN = DH / 8, RP = 32 / LN;  // lanes a row, rows a pass
-  const int lane = threadIdx.x & 31, sub = lane % LN;
-#pragma unroll
-  for (int i = 0; i < 32 / RP; ++i) {
-    const int rr = i * RP + lane / LN;
-    const unsigned long long from =
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), rr);
-    const void* at = from != 0 ? reinterpret_cast<const void*>(from + sub * 16) : any;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + sw128(r + rr, sub)),
-                 "l"(at), "r"(from != 0 ? 16 : 0)
-                 : "memory");
-  }
-}
 // The lane's row (row r of the operand at qs) from bf16 to f16 in place; returns
 // its score factor.  (Read from global memory by the lanes themselves, 32 rows a
 // load, the same took three times as long.)

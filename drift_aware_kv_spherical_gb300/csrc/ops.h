@@ -130,6 +130,7 @@ size_t kv4_weight_ws(int B, int N, int Hq, int Hkv, int dh, int T);
 cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s);
 // the tcgen05 kernel (bf16 queries, dh 64 or 128); ntile and nsplit as planned
 cudaError_t kv4_attn_tc_launch(const Kv4AttnArgs& a, cudaStream_t s);
+cudaError_t kv4_weight_tc_launch(const Kv4AttnArgs& a, cudaStream_t s);
 cudaError_t kv4_weight_run(const Kv4AttnArgs& a, cudaStream_t s);
 
 struct Kv4EvictArgs {

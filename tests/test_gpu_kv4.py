@@ -479,3 +479,46 @@ def test_graph_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip((O, lse, w), want))
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,dh,N,mask,cap,bias", [
+    (1, 65, 1, 1, 128, 1, "none", 0, False),
+    (1, 128, 3, 3, 64, 256, "none", 0, False),
+    (2, 129, 2, 1, 128, 257, "len", 0, False),
+    (1, 1500, 2, 2, 64, 700, "causal", 0, False),
+    (1, 2049, 1, 1, 128, 300, "none", 0, False),
+    (3, 401, 7, 1, 128, 1025, "documents", 0, False),
+    (1, 333, 4, 2, 64, 5000, "documents", 0.75, True),
+    (2, 200, 4, 4, 128, 511, "causal", 40.0, False),
+    (1, 500, 4, 2, 128, 600, "kpos", 10.0, True),
+])
+def test_weight_of_many_rows(B, T, Hq, Hkv, dh, N, mask, cap, bias):
+    """Rows and slots that end inside tiles, rows split over CTAs, steps that see
+    nothing; the sum over all rows of a head is as good as its terms."""
+    seed = T + N
+    length, span, qpos, kpos = _masks(mask, B, T, N, Hkv, seed)
+    c, K, V = _cache(B, Hkv, N, dh, seed, junk_from=length)
+    Q, Qn = _query(B, T, Hq, dh, BF16, seed, 1.0)
+    scale = dh ** -0.5
+    slope = (0.5 ** np.arange(1, Hq + 1)).astype(np.float32) if bias else None
+    s = oracle.kv4_scores(Qn, K, scale, length, span, kpos, qpos if bias else None, slope, cap)
+    _, lref = oracle.kv4_attention(s, V)
+    lse = torch.from_numpy(lref).float().cuda()
+    opt = dict(scale=scale, len=_i32(length), span=_i32(span), kpos=_i32(kpos),
+               qpos=_i32(qpos) if bias else None,
+               slope=torch.from_numpy(slope).cuda() if bias else None, cap=float(cap))
+    w = Guarded((B, Hkv, N), F32, fill=7)
+    w0 = torch.rand(B, Hkv, N, device="cuda")
+    ps.ps_kv4_weight(c, Q, lse, None, w.t, **opt)
+    ref = oracle.kv4_weight(s, lse.double().cpu().numpy(), Hkv)
+    dist = 0.0 if not bias else float(np.abs(qpos).max() + (N if kpos is None else kpos.max()))
+    ds, _ = _tol(Qn, K, V, scale, cap, BF16)
+    ds += 2.0 ** -22 * dist
+    lim = ref * (np.expm1(2 * ds + 2.0 ** -21 * np.abs(lref[np.isfinite(lref)]).max(initial=0))
+                 + 2.0 ** -18) + 1e-30
+    got = w.t.double().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= lim), np.max(np.abs(got - ref) / lim)
+    assert w.intact()
+    w1 = w0.clone()
+    ps.ps_kv4_weight(c, Q, lse, w1, w1, **opt)
+    assert torch.equal(w1, w0 + w.t)
