@@ -38,7 +38,8 @@ struct StepRows {
                          // where slots are positions
   int lo[kTile];         // positions seen: lo + [0, num)
   uint32_t num[kTile];
-  int last, any_lo, any_hi, all_lo, all_hi;  // slots that some, that every row sees
+  int cols;                            // columns in use, a multiple of 32; 0: the end
+  int any_lo, any_hi, all_lo, all_hi;  // slots that some, that every row sees
   int pad[3];
 };
 
@@ -138,18 +139,19 @@ __device__ __forceinline__ float weigh32(const Kv4AttnArgs& a, float* s, const S
   return s0 + s1;
 }
 
-// A step's 128 columns; `free` is arrived at once they have been read.
+// A step's columns; `free` is arrived at once they have been read.
 template <bool GEN, bool MASKED>
 __device__ __forceinline__ float weigh_step(const Kv4AttnArgs& a, uint32_t col,
                                             const StepRows& rows, int pos, float dpos,
                                             uint64_t* free) {
+  const int cols = rows.cols;
   float sum = 0.f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kTile; c0 += 32) {
+  for (int c0 = 0; c0 < cols; c0 += 32) {
     float s[32];
     tc::tmem_ld32_nowait(col + c0, reinterpret_cast<uint32_t*>(s));
     tc::tmem_wait_ld();
-    if (c0 == kTile - 32) {
+    if (c0 == cols - 32) {
       tc::fence_before_sync();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) tc::mbar_arrive(free);
@@ -233,7 +235,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after_sync();
       const StepRows& rows = steps[st];
-      if (rows.last) break;
+      if (rows.cols == 0) break;
       if (lo < rows.any_hi && hi > rows.any_lo) {
         const float x = lo >= rows.all_lo && hi <= rows.all_hi
                             ? weigh_step<GEN, false>(a, col, rows, pos, dpos, s_empty + half)
@@ -313,7 +315,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
         rows.qpos[p] = by_pos ? qpos : __float_as_int((float)(qpos - n0));
       }
       if (p == 0) {
-        rows.last = 0;
+        rows.cols = min((a.M - m0 + 31) & ~31, kTile);
         rows.any_lo = any_lo;
         rows.any_hi = any_hi;
         rows.all_lo = all_lo;
@@ -332,12 +334,11 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
       const int st = i % kStages;
       ok = tc::mbar_wait(empty + st, ((i / kStages) & 1) ^ 1, a.status, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
-      if (p == 0) steps[st].last = 1;
+      if (p == 0) steps[st].cols = 0;
       publish(st);
     }
   } else {
     // ------------------------------------------------------------ MMAs
-    constexpr uint32_t kId = tc::idesc_bf16(128, kTile, false);
     const uint32_t kb = tc::smem_u32(smem), qb = kb + SM::kQ;
     bool ok = tc::mbar_wait(k_full, 0, a.status, abort_flag);
     for (int i = 0, ends = 0; ends < 2; ++i) {
@@ -347,9 +348,10 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
-      const int end = *static_cast<volatile int*>(&steps[st].last);
+      const int cols = *static_cast<volatile int*>(&steps[st].cols);
+      const uint32_t id = tc::idesc_bf16(128, cols, false);
       if (elect_one()) {
-        if (!end) {
+        if (cols > 0) {
 #pragma unroll
           for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -357,13 +359,13 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
               const uint32_t off = (kk / 4) * 16384u + (kk % 4) * 32u;
               tc::mma_bf16(tmem + half * 256 + g * kTile,
                            tc::desc_sw128(kb + g * SM::kOp + off, 16, 1024),
-                           tc::desc_sw128(qb + st * SM::kOp + off, 16, 1024), kId, kk > 0);
+                           tc::desc_sw128(qb + st * SM::kOp + off, 16, 1024), id, kk > 0);
             }
         }
         tc::mma_commit(s_full + half);
       }
       __syncwarp();
-      ends += end;
+      ends += cols == 0;
     }
     if (!ok) {  // wait for the MMAs issued before TMEM is freed
       if (elect_one()) tc::mma_commit(drain);
