@@ -167,8 +167,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
   using SM = WSmem<DH>;
   pdl_prologue();
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_raw + (-tc::smem_u32(smem_raw) & 1023);  // known to be shared memory
   StepRows* steps = reinterpret_cast<StepRows*>(smem + SM::kRows);
   float* sums = reinterpret_cast<float*>(smem + SM::kSum);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBar);
