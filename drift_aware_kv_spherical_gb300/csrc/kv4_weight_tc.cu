@@ -6,14 +6,14 @@
 // thread sums its slot's weights over the columns and no sum crosses threads.  A
 // CTA takes 256 slots of one KV head (two 128-slot tiles, dequantised once: code
 // times scale is exact in bf16, so the queries stay as they are) and passes all
-// rows by them, 128 at a time.  21 warps:
+// rows by them, 128 at a time.  19 warps:
 //   0-15   four groups of four: a group reads one slot tile's products of every
 //          second step, so that one step's exponentials run under the next one's
 //          MMAs.  Warps 0-7 dequantise the slots first
-//   16-19  the queries, by cp.async into a ring of four operands, and what the
+//   16, 17 the queries, by cp.async into a ring of four operands, and what the
 //          rows bring: their lse, span, position and slope.  With spans, steps
 //          whose rows see none of the 256 slots are left out
-//   20     issues the MMAs: two 128 x 128 products a step into one half of TMEM
+//   18     issues the MMAs: two 128 x 128 products a step into one half of TMEM
 // Where there are few blocks of slots, the rows are split over the CTAs of a
 // cluster, whose sums are added in rank order: the result does not depend on
 // timing.
@@ -24,7 +24,7 @@
 namespace ps {
 namespace {
 
-constexpr int kWThreads = 672;
+constexpr int kWThreads = 608;
 constexpr int kTile = 128;    // rows a step; slots of a slot tile
 constexpr int kSlots = 256;   // slots of a CTA
 constexpr int kStages = 4;    // query operands
@@ -161,6 +161,40 @@ __device__ __forceinline__ float weigh_step(const Kv4AttnArgs& a, uint32_t col,
   return sum;
 }
 
+// The same for 128 columns that every row sees: the next 32 are on their way from
+// TMEM (about 280 clocks) while these are summed.
+__device__ __forceinline__ float weigh_all(const Kv4AttnArgs& a, uint32_t col, const StepRows& rows,
+                                           uint64_t* free) {
+  float s[2][32], sum = 0.f;
+  tc::tmem_ld32_nowait(col, reinterpret_cast<uint32_t*>(s[0]));
+#pragma unroll
+  for (int k = 0; k < kTile / 32; ++k) {
+    tc::tmem_wait_ld();
+    if (k + 1 < kTile / 32) {
+      tc::tmem_ld32_nowait(col + 32 * (k + 1), reinterpret_cast<uint32_t*>(s[(k + 1) & 1]));
+    } else {
+      tc::fence_before_sync();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) tc::mbar_arrive(free);
+    }
+    sum += weigh32<false, false>(a, s[k & 1], rows, 32 * k, 0, 0.f);
+  }
+  return sum;
+}
+
+// Whether a phase is over, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 template <int DH, bool GEN>
 __global__ void __launch_bounds__(kWThreads, 1)
 k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
@@ -171,9 +205,9 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
   StepRows* steps = reinterpret_cast<StepRows*>(smem + SM::kRows);
   float* sums = reinterpret_cast<float*>(smem + SM::kSum);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBar);
-  uint64_t *empty = full + kStages, *s_full = full + 2 * kStages, *s_empty = s_full + 2;
-  uint64_t *k_full = s_full + 4, *drain = s_full + 5;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 6);
+  uint64_t *empty = full + kStages, *s_full = full + 2 * kStages;  // [half][slot tile]
+  uint64_t *s_empty = s_full + 4, *k_full = s_full + 8, *drain = s_full + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 11);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -190,19 +224,20 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(full + i, 4);
+      tc::mbar_init(full + i, 2);
       tc::mbar_init(empty + i, 8);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(s_full + i, 1);
-      tc::mbar_init(s_empty + i, 8);
+      tc::mbar_init(s_empty + i, 4);
     }
-    tc::mbar_init(k_full, 8);
+    tc::mbar_init(k_full, 4);
+    tc::mbar_init(k_full + 1, 4);
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 20) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == 18) tc::tmem_alloc(tmem_slot, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -217,7 +252,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
       put_row_bf16<DH>(smem + g * SM::kOp, tid & 127, k);
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(k_full);
+      if (lane == 0) tc::mbar_arrive(k_full + g);
     }
     const int w0 = g * kTile + (warp & 3) * 32;  // the warp's first slot in the block
     const int lo = n0 + w0, hi = min(lo + 32, len);
@@ -226,33 +261,36 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
     const float dpos = (float)(w0 + lane);
     const uint32_t col = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * 256 +
                          g * kTile;
+    uint64_t *mine = s_full + half * 2 + g, *free = s_empty + half * 2 + g;
     float sum = 0.f, low = 0.f;  // low: what the sum's rounding has lost
     for (int i = half;; i += 2) {
       const int st = i % kStages;
       const bool ok = tc::mbar_wait(full + st, (i / kStages) & 1, a.status, abort_flag) &&
-                      tc::mbar_wait(s_full + half, (i >> 1) & 1, a.status, abort_flag);
+                      tc::mbar_wait(mine, (i >> 1) & 1, a.status, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after_sync();
       const StepRows& rows = steps[st];
       if (rows.cols == 0) break;
       if (lo < rows.any_hi && hi > rows.any_lo) {
-        const float x = lo >= rows.all_lo && hi <= rows.all_hi
-                            ? weigh_step<GEN, false>(a, col, rows, pos, dpos, s_empty + half)
-                            : weigh_step<GEN, true>(a, col, rows, pos, dpos, s_empty + half);
+        const bool all = lo >= rows.all_lo && hi <= rows.all_hi;
+        float x;
+        if (!GEN && all && rows.cols == kTile) x = weigh_all(a, col, rows, free);
+        else if (all) x = weigh_step<GEN, false>(a, col, rows, pos, dpos, free);
+        else x = weigh_step<GEN, true>(a, col, rows, pos, dpos, free);
         const float y = x + low, t = sum + y;
         low = y - (t - sum);
         sum = t;
       } else if (lane == 0) {
-        tc::mbar_arrive(s_empty + half);
+        tc::mbar_arrive(free);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(empty + st);
     }
     sums[half * kSlots + w0 + lane] = sum;
     tc::fence_before_sync();
-  } else if (warp < 20) {
+  } else if (warp < 18) {
     // ------------------------------------------------------------ queries
-    const int p = tid - 512;
+    const int p = tid - 512;  // of rows p and p + 64
     const bool by_pos = GEN && a.kpos != nullptr;
     const int tiles = (a.M + kTile - 1) / kTile, each = (tiles + a.nsplit - 1) / a.nsplit;
     const int end = min(tiles, (split + 1) * each);
@@ -263,6 +301,30 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(full + st);
     };
+    // What the lane's rows bring, asked for a step ahead: rows lane + 32 k of the
+    // step for the spans, p and p + 64 (k = warp, warp + 2) for the rest
+    float lse[2], slope[2];
+    int2 span[4];
+    int qpos[2];
+    auto ask = [&](int r) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        span[k] = make_int2(0, INT32_MAX);
+        const int m = r * kTile + lane + 32 * k, t = row_token(a, m);
+        if (r < end && m < a.M && a.span != nullptr)
+          span[k] = __ldg(reinterpret_cast<const int2*>(a.span) + (long)b * a.T + t);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int m = r * kTile + p + 64 * k, t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
+        const bool in = r < end && m < a.M;
+        const long tok = (long)b * a.T + t;
+        lse[k] = in ? __ldg(a.lse_in + tok * a.Hq + h) : INFINITY;
+        slope[k] = GEN && in && a.slope != nullptr ? __ldg(a.slope + h) : 0.f;
+        qpos[k] = GEN && in && a.qpos != nullptr ? __ldg(a.qpos + tok) : 0;
+      }
+    };
+    ask(split * each);
     for (int r = split * each; r < end; ++r) {
       const int m0 = r * kTile;
       int any_lo = 0, any_hi = len, all_lo = 0, all_hi = len;
@@ -270,48 +332,60 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
         if (by_pos) {
           all_hi = -1;
         } else {
-          const int t0 = row_token(a, m0), t1 = row_token(a, min(m0 + kTile, a.M) - 1);
           int lo = INT32_MAX, hi = INT32_MIN, lo2 = INT32_MIN, hi2 = INT32_MAX;
-#pragma unroll 4
-          for (int t = t0 + lane; t <= t1; t += 32) {
-            const int2 x = __ldg(reinterpret_cast<const int2*>(a.span) + (long)b * a.T + t);
-            if (x.x < x.y) {
-              lo = min(lo, x.x);
-              hi = max(hi, x.y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (m0 + lane + 32 * k >= a.M) continue;
+            if (span[k].x < span[k].y) {
+              lo = min(lo, span[k].x);
+              hi = max(hi, span[k].y);
             }
-            lo2 = max(lo2, x.x);
-            hi2 = min(hi2, x.y);
+            lo2 = max(lo2, span[k].x);
+            hi2 = min(hi2, span[k].y);
           }
           any_lo = __reduce_min_sync(0xffffffffu, lo);
           any_hi = min(len, __reduce_max_sync(0xffffffffu, hi));
           all_lo = __reduce_max_sync(0xffffffffu, lo2);
           all_hi = min(len, __reduce_min_sync(0xffffffffu, hi2));
-          if (any_lo >= n0 + kSlots || any_hi <= n0) continue;
+          if (any_lo >= n0 + kSlots || any_hi <= n0) {
+            ask(r + 1);
+            continue;
+          }
         }
       }
-      const int m = m0 + p, st = i % kStages;
-      const bool in = m < a.M;
-      const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
-      const long tok = (long)b * a.T + t;
-      const float nlse = in ? -__ldg(a.lse_in + tok * a.Hq + h) : -INFINITY;
-      const int2 span = in && a.span != nullptr
-                            ? __ldg(reinterpret_cast<const int2*>(a.span) + tok)
-                            : make_int2(0, INT32_MAX);
-      ok = tc::mbar_wait(empty + st, ((i / kStages) & 1) ^ 1, a.status, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      fetch_q<DH>(a.Q, in ? static_cast<const __nv_bfloat16*>(a.Q) + (long)b * a.q_bld +
-                           (long)t * a.q_ld + (long)h * DH
-                     : nullptr,
-                  tc::smem_u32(smem + SM::kQ + st * SM::kOp), p & ~31);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      const int st = i % kStages;
+      const uint32_t ph = ((i / kStages) & 1) ^ 1;
       StepRows& rows = steps[st];
-      rows.nlse[p] = nlse;
-      rows.lo[p] = span.x;
-      rows.num[p] = span.x < span.y ? (uint32_t)span.y - (uint32_t)span.x : 0u;
-      if constexpr (GEN) {
-        const int qpos = in && a.qpos != nullptr ? __ldg(a.qpos + tok) : 0;
-        rows.slope[p] = in && a.slope != nullptr ? __ldg(a.slope + h) : 0.f;
-        rows.qpos[p] = by_pos ? qpos : __float_as_int((float)(qpos - n0));
+      // no stage free: what is under way is handed over first
+      if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test(empty + st, ph))) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        publish(pending);
+        pending = -1;
+      }
+      ok = tc::mbar_wait(empty + st, ph, a.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = p + 64 * k, m = m0 + c;
+        const bool in = m < a.M;
+        const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
+        fetch_q<DH>(a.Q, in ? static_cast<const __nv_bfloat16*>(a.Q) + (long)b * a.q_bld +
+                             (long)t * a.q_ld + (long)h * DH
+                       : nullptr,
+                    tc::smem_u32(smem + SM::kQ + st * SM::kOp), c & ~31);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = p + 64 * k;
+        const int2 seen = p < 32 ? span[2 * k] : span[2 * k + 1];
+        rows.nlse[c] = -lse[k];
+        rows.lo[c] = seen.x;
+        rows.num[c] = seen.x < seen.y ? (uint32_t)seen.y - (uint32_t)seen.x : 0u;
+        if constexpr (GEN) {
+          rows.slope[c] = slope[k];
+          rows.qpos[c] = by_pos ? qpos[k] : __float_as_int((float)(qpos[k] - n0));
+        }
       }
       if (p == 0) {
         rows.cols = min((a.M - m0 + 31) & ~31, kTile);
@@ -320,6 +394,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
         rows.all_lo = all_lo;
         rows.all_hi = all_hi;
       }
+      ask(r + 1);
       if (pending >= 0) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         publish(pending);
@@ -339,20 +414,23 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
   } else {
     // ------------------------------------------------------------ MMAs
     const uint32_t kb = tc::smem_u32(smem), qb = kb + SM::kQ;
-    bool ok = tc::mbar_wait(k_full, 0, a.status, abort_flag);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = tc::mbar_wait(bar, parity, a.status, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+    };
     for (int i = 0, ends = 0; ends < 2; ++i) {
       const int st = i % kStages, half = i & 1;
-      if (ok) ok = tc::mbar_wait(full + st, (i / kStages) & 1, a.status, abort_flag);
-      if (ok) ok = tc::mbar_wait(s_empty + half, ((i >> 1) & 1) ^ 1, a.status, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const int cols = *static_cast<volatile int*>(&steps[st].cols);
+      wait(full + st, (i / kStages) & 1);
+      const int cols = ok ? *static_cast<volatile int*>(&steps[st].cols) : 0;
       const uint32_t id = tc::idesc_bf16(128, cols, false);
-      if (elect_one()) {
-        if (cols > 0) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < 2; ++g) {
+        if (i == 0) wait(k_full + g, 0);
+        wait(s_empty + half * 2 + g, ((i >> 1) & 1) ^ 1);
+        if (ok && elect_one()) {
+          if (cols > 0) {
 #pragma unroll
             for (int kk = 0; kk < DH / 16; ++kk) {
               const uint32_t off = (kk / 4) * 16384u + (kk % 4) * 32u;
@@ -360,9 +438,12 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
                            tc::desc_sw128(kb + g * SM::kOp + off, 16, 1024),
                            tc::desc_sw128(qb + st * SM::kOp + off, 16, 1024), id, kk > 0);
             }
+          }
+          tc::mma_commit(s_full + half * 2 + g);
         }
-        tc::mma_commit(s_full + half);
+        __syncwarp();
       }
+      if (!ok) break;
       __syncwarp();
       ends += cols == 0;
     }
@@ -375,7 +456,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
     __syncwarp();
   }
   __syncthreads();
-  if (warp == 20) {
+  if (warp == 18) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
