@@ -248,6 +248,7 @@ __device__ __forceinline__ TcRow tc_row(const Kv4AttnArgs& a, bool in, int b, in
 // What the rows of a softmax warp see of 64 slots.  A row that sees nothing at
 // all has no say (its sum is dropped at the end).  Taken once an item, so that
 // a step compares two numbers and does not vote.
+enum TcScore { kPlain, kCap, kAny };
 enum TcSeen { kNone, kSome, kAll };
 struct TcRange {
   int any_lo, any_hi, all_lo, all_hi;  // slots that some, that every row sees
@@ -267,6 +268,47 @@ __device__ __forceinline__ TcSeen tc_seen(const TcRange& r, int n0) {
   return n0 >= r.all_lo && n0 <= r.all_hi ? kAll : kSome;
 }
 
+// Capped scores: cap tanh(score / cap).
+template <int C>
+__device__ __forceinline__ float abs_max(const float* s) {
+  float t4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < C; c += 2)
+    t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
+  return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+}
+// Whether the series below does for scores up to `top` (log2 units).
+__device__ __forceinline__ bool cap_small(const Kv4AttnArgs& a, float top) {
+  return top * (a.inv_cap * kLn2) <= 0.2f;
+}
+// tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7.  x: raw product.
+__device__ __forceinline__ float cap_score(const Kv4AttnArgs& a, float x, float f) {
+  const float e = exp2_approx(x * (2.f * f * a.inv_cap * kLog2e));
+  return a.cap * kLog2e * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
+}
+// s[0..C): raw products, f their factor -> log2-unit scores.
+template <int C>
+__device__ __forceinline__ void cap_scores(const Kv4AttnArgs& a, float* s, float f, bool small) {
+  if (small) {
+    // tanh y = y (1 - y^2/3 + 2 y^4/15 - 17 y^6/315 + ...): the next term is
+    // under 2^-24 of y here.  y = score / cap = u kc, u the score in log2 units
+    const float kc = a.inv_cap * kLn2, k2 = kc * kc, f2 = f * kLog2e;
+    const float c1 = k2 * (-1.f / 3.f), c2 = k2 * k2 * (2.f / 15.f),
+                c3 = k2 * k2 * k2 * (-17.f / 315.f);
+    const uint64_t ff = f2_pack(f2, f2), cc1 = f2_pack(c1, c1), cc2 = f2_pack(c2, c2),
+                   cc3 = f2_pack(c3, c3);
+#pragma unroll
+    for (int c = 0; c < C; c += 2) {
+      const uint64_t u = f2_mul(f2_pack(s[c], s[c + 1]), ff), z = f2_mul(u, u);
+      const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, cc3, cc2), cc1));
+      f2_unpack(f2_fma(u, q, u), s[c], s[c + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = cap_score(a, s[c], f);
+  }
+}
+
 // s[0..C): raw products of C slots from n0 on -> log2-unit scores (GEN), and
 // -inf where the row does not see the slot.  pos: explicit positions, or null.
 template <bool GEN, int C>
@@ -277,34 +319,7 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, volati
     const float f2 = row.f * kLog2e;
     const uint64_t ff = f2_pack(f2, f2);
     if (a.cap > 0.f) {
-      float t4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < C; c += 2)
-        t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
-      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-      // y = score / cap = u kc, u the score in log2 units
-      const float kc = a.inv_cap * kLn2, k2 = kc * kc;
-      if (__all_sync(0xffffffffu, top * f2 * kc <= 0.2f)) {
-        // tanh y = y (1 - y^2/3 + 2 y^4/15 - 17 y^6/315 + ...): the next term
-        // is under 2^-24 of y here
-        const float c1 = k2 * (-1.f / 3.f), c2 = k2 * k2 * (2.f / 15.f),
-                    c3 = k2 * k2 * k2 * (-17.f / 315.f);
-        const uint64_t cc1 = f2_pack(c1, c1), cc2 = f2_pack(c2, c2), cc3 = f2_pack(c3, c3);
-#pragma unroll
-        for (int c = 0; c < C; c += 2) {
-          const uint64_t u = f2_mul(f2_pack(s[c], s[c + 1]), ff), z = f2_mul(u, u);
-          const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, cc3, cc2), cc1));
-          f2_unpack(f2_fma(u, q, u), s[c], s[c + 1]);
-        }
-      } else {
-        // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
-        const float fe = 2.f * row.f * a.inv_cap * kLog2e, cap2 = a.cap * kLog2e;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float e = exp2_approx(s[c] * fe);
-          s[c] = cap2 * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
-        }
-      }
+      cap_scores<C>(a, s, row.f, __all_sync(0xffffffffu, cap_small(a, abs_max<C>(s) * f2)));
     } else {
 #pragma unroll
       for (int c = 0; c < C; c += 2)
@@ -342,15 +357,20 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, volati
 // them (64 slots at a time: p_full[0], p_full[1]), the rows' maximum and sum,
 // and O at o_col rescaled where the maximum has outgrown it.  FAST: every row
 // sees every slot (its own copy of the code: tests inside the passes cost a
-// fifth of the step).
-template <int DH, bool GEN, bool FAST>
+// fifth of the step).  Scores that are only capped rise with the product: the
+// maximum is taken of products and the cap applied on the way to P (LATE), not
+// stored back between the passes.
+template <int DH, int GEN, bool FAST>
 __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int* row, float f2,
                                              int n0, TcSeen seen0, TcSeen seen1, const int* ps,
                                              uint32_t s_col, uint32_t o_col, bool has_o,
                                              uint64_t* p_full, float& m_used, float& l) {
   // The maximum; scores that are more than raw products go back to TMEM for the
   // second pass (32 at a time then: their arithmetic needs registers too).
-  constexpr int C = GEN ? 32 : 64;
+  constexpr bool LATE = FAST && GEN == kCap;
+  constexpr int C = GEN && !LATE ? 32 : 64;
+  const float rf = LATE ? __int_as_float(row[0]) : 0.f;
+  float top = 0.f;
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains: one would wait on itself
 #pragma unroll 1
   for (int k = 0; k < 128; k += C) {
@@ -361,16 +381,19 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
     for (int q = 0; q < C; q += 32)
       tc::tmem_ld32_nowait(s_col + k + q, reinterpret_cast<uint32_t*>(s) + q);
     tc::tmem_wait_ld();
-    if (GEN || !FAST) {
-      tc_scores<GEN, C>(a, s, row, n0 + k, seen, ps != nullptr ? ps + k : nullptr);
+    if (LATE) top = fmaxf(top, abs_max<C>(s));
+    if ((GEN || !FAST) && !LATE) {
+      tc_scores<GEN != 0, C>(a, s, row, n0 + k, seen, ps != nullptr ? ps + k : nullptr);
 #pragma unroll
       for (int q = 0; q < C; q += 32) tc::tmem_st32(s_col + k + q, reinterpret_cast<uint32_t*>(s) + q);
     }
 #pragma unroll
     for (int c = 0; c < C; c += 2) m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
   }
-  if (GEN || !FAST) tc::tmem_wait_st();
-  const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f2;
+  if ((GEN || !FAST) && !LATE) tc::tmem_wait_st();
+  const float m_raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  const float m_tile = LATE ? cap_score(a, m_raw, rf) : m_raw * f2;
+  const bool small = LATE && __all_sync(0xffffffffu, cap_small(a, top * rf * kLog2e));
   const bool grow = m_tile > m_used + kGrow;
   if (__any_sync(0xffffffffu, grow)) {
     const float m_new = grow ? m_tile : m_used;
@@ -404,6 +427,7 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
       tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
       tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
       tc::tmem_wait_ld();
+      if constexpr (LATE) cap_scores<64>(a, s, rf, small);
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         float x0, x1;
@@ -424,8 +448,8 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
   l += s0 + s1;
 }
 
-// GEN: capped scores, a distance bias or explicit positions.
-template <int DH, bool GEN>
+// GEN: kCap, capped scores; kAny, a distance bias or explicit positions too.
+template <int DH, int GEN>
 __global__ void __launch_bounds__(kTcThreads, 1)
 k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
   using SM = TcSmem<DH>;
@@ -444,7 +468,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler too
-  const bool by_pos = GEN && a.kpos != nullptr;
+  const bool by_pos = GEN == kAny && a.kpos != nullptr;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -770,7 +794,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
   }
 }
 
-template <int DH, bool GEN>
+template <int DH, int GEN>
 cudaError_t launch_tc(const Kv4AttnArgs& a, cudaStream_t s) {
   auto kern = k_kv4_attn_tc<DH, GEN>;
   static bool attr_set = false;
@@ -788,9 +812,16 @@ cudaError_t launch_tc(const Kv4AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t kv4_attn_tc_launch(const Kv4AttnArgs& a, cudaStream_t s) {
-  const bool gen = a.cap > 0.f || a.slope != nullptr || a.kpos != nullptr;
-  if (a.dh == 64) return gen ? launch_tc<64, true>(a, s) : launch_tc<64, false>(a, s);
-  if (a.dh == 128) return gen ? launch_tc<128, true>(a, s) : launch_tc<128, false>(a, s);
+  const int gen = a.slope != nullptr || a.kpos != nullptr ? kAny : a.cap > 0.f ? kCap : kPlain;
+#define PS_KV4_TC(DH, GEN) \
+  if (a.dh == DH && gen == GEN) return launch_tc<DH, GEN>(a, s);
+  PS_KV4_TC(64, kPlain)
+  PS_KV4_TC(64, kCap)
+  PS_KV4_TC(64, kAny)
+  PS_KV4_TC(128, kPlain)
+  PS_KV4_TC(128, kCap)
+  PS_KV4_TC(128, kAny)
+#undef PS_KV4_TC
   return cudaErrorInvalidValue;
 }
 

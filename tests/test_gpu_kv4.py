@@ -522,3 +522,11 @@ def test_weight_of_many_rows(B, T, Hq, Hkv, dh, N, mask, cap, bias):
     w1 = w0.clone()
     ps.ps_kv4_weight(c, Q, lse, w1, w1, **opt)
     assert torch.equal(w1, w0 + w.t)
+
+
+@pytest.mark.parametrize("T,dh,N,mask,cap", [(150, 128, 700, "none", 30.0), (40, 64, 1100, "len", 0.5),
+                                             (300, 128, 513, "causal", 3.0),
+                                             (77, 64, 640, "documents", 50.0)])
+def test_capped_scores_of_many_rows(T, dh, N, mask, cap):
+    """Capped scores without a bias: small ones, and ones at the cap."""
+    test_attention_and_weight(2, T, 6, 2, dh, N, BF16, mask, cap, False)
