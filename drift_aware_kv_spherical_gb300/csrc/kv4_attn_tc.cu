@@ -279,7 +279,7 @@ __device__ __forceinline__ float abs_max(const float* s) {
 }
 // Whether the series below does for scores up to `top` (log2 units).
 __device__ __forceinline__ bool cap_small(const Kv4AttnArgs& a, float top) {
-  return top * (a.inv_cap * kLn2) <= 0.2f;
+  return top * (a.inv_cap * kLn2) <= kTanhTop;
 }
 // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7.  x: raw product.
 __device__ __forceinline__ float cap_score(const Kv4AttnArgs& a, float x, float f) {
@@ -290,19 +290,7 @@ __device__ __forceinline__ float cap_score(const Kv4AttnArgs& a, float x, float 
 template <int C>
 __device__ __forceinline__ void cap_scores(const Kv4AttnArgs& a, float* s, float f, bool small) {
   if (small) {
-    // tanh y = y (1 - y^2/3 + 2 y^4/15 - 17 y^6/315 + ...): the next term is
-    // under 2^-24 of y here.  y = score / cap = u kc, u the score in log2 units
-    const float kc = a.inv_cap * kLn2, k2 = kc * kc, f2 = f * kLog2e;
-    const float c1 = k2 * (-1.f / 3.f), c2 = k2 * k2 * (2.f / 15.f),
-                c3 = k2 * k2 * k2 * (-17.f / 315.f);
-    const uint64_t ff = f2_pack(f2, f2), cc1 = f2_pack(c1, c1), cc2 = f2_pack(c2, c2),
-                   cc3 = f2_pack(c3, c3);
-#pragma unroll
-    for (int c = 0; c < C; c += 2) {
-      const uint64_t u = f2_mul(f2_pack(s[c], s[c + 1]), ff), z = f2_mul(u, u);
-      const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, cc3, cc2), cc1));
-      f2_unpack(f2_fma(u, q, u), s[c], s[c + 1]);
-    }
+    cap_series<C>(s, f * kLog2e, a.inv_cap * kLn2);
   } else {
 #pragma unroll
     for (int c = 0; c < C; ++c) s[c] = cap_score(a, s[c], f);

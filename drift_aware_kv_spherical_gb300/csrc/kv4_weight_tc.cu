@@ -82,29 +82,20 @@ __device__ __forceinline__ float weigh32(const Kv4AttnArgs& a, float* s, const S
                                          int c0, int pos, float dpos) {
   const uint64_t f = f2_pack(a.scale, a.scale);
   if constexpr (GEN) {
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), f), s[c], s[c + 1]);
     if (a.cap > 0.f) {
       float top = 0.f;
 #pragma unroll
       for (int c = 0; c < 32; c += 2) top = max3(top, fabsf(s[c]), fabsf(s[c + 1]));
-      const float k2 = a.inv_cap * a.inv_cap;
-      if (__all_sync(0xffffffffu, top * a.inv_cap <= 0.2f)) {
-        // tanh y = y (1 - y^2/3 + 2 y^4/15 - 17 y^6/315 + ...): the next term is
-        // under 2^-24 of y here
-        const float c1 = k2 * (-1.f / 3.f), c2 = k2 * k2 * (2.f / 15.f),
-                    c3 = k2 * k2 * k2 * (-17.f / 315.f);
-        const uint64_t cc1 = f2_pack(c1, c1), cc2 = f2_pack(c2, c2), cc3 = f2_pack(c3, c3);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const uint64_t u = f2_pack(s[c], s[c + 1]), z = f2_mul(u, u);
-          const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, cc3, cc2), cc1));
-          f2_unpack(f2_fma(u, q, u), s[c], s[c + 1]);
-        }
+      if (__all_sync(0xffffffffu, top * fabsf(a.scale) * a.inv_cap <= kTanhTop)) {
+        cap_series<32>(s, a.scale, a.inv_cap);
       } else {
+        const float k = a.scale * a.inv_cap;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = a.cap * tanhf(s[c] * a.inv_cap);
+        for (int c = 0; c < 32; ++c) s[c] = a.cap * tanhf(s[c] * k);
       }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), f), s[c], s[c + 1]);
     }
     if (a.slope != nullptr) {
 #pragma unroll
