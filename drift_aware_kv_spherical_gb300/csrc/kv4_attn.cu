@@ -1,6 +1,6 @@
 // Attention over a 4-bit KV cache, and the weight it puts on each slot.
 //
-//   k_kv4_attn     online-softmax attention of 8, 16 or 32 rows of one KV head's
+//   k_kv4_attn     online-softmax attention of 8 or 16 rows of one KV head's
 //                  queries over a share of its slots
 //   k_kv4_combine  the shares of a row joined
 //   k_kv4_weight   column sums of exp(s - lse), K only
@@ -8,12 +8,13 @@
 // The rows of a KV head are its T tokens times the G = Hq / Hkv query heads it
 // serves (row t G + j), so a head's K and V are read once for all of them.
 //
-// A warp works alone on 16 slots at a time, straight from global memory into
+// A warp works alone on 16 slots at a time, from its own cp.async ring into
 // m16n8k16 operand fragments (f16, fp32 accumulators), the slots as the 16 and
-// the query rows as the 8, since one token has few rows:
+// the query rows as the 8, since one token has few rows (the rows as the 16 took
+// 118 us where this takes 94, without the ring):
 //   S^T = K Q^T  the 16 contraction indices of a step may be any 16 elements as
 //     long as Q and K agree: lane (g, t) = (lane / 4, lane % 4) takes elements
-//     [t dh/4, (t+1) dh/4) of slots g and g + 8, one contiguous load each, and
+//     [t dh/4, (t+1) dh/4) of slots g and g + 8, one contiguous piece each, and
 //     step ks uses elements 4 ks .. 4 ks + 3 of them.  Q is laid out in that
 //     order in shared memory.
 //   O^T = V^T P^T  P^T needs the slots where S^T has the rows: one 8 x 8
@@ -25,6 +26,14 @@
 // bf16 queries are exact in f16 down to 2^-25 of the row's largest; fp32
 // queries and P take two f16 terms (hi + lo).  P carries a factor 2^kPShift,
 // which keeps small weights out of f16's subnormals.
+//
+// What bounds k_kv4_attn: the codes are read once, 0.56 bytes an element, and
+// cost two conversions and a product an f16 pair, so a long cache is held up by
+// instructions and the ring's waits before memory: 8 tokens on 64 K slots of 4
+// heads (302 MB) 59 us, 5.1 TB/s, 75 % of a copy's rate; few slots by the launch
+// and the length of one warp's chain (1024 slots: 6 us).  k_kv4_weight reads K
+// alone and is bound by its instructions: 8 tokens on 32 K slots (84 MB with the
+// weights) 21 us, 4 TB/s.
 #include "kv4.cuh"
 #include "tc.cuh"
 
@@ -394,153 +403,152 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
     at ^= R::kStage;
 #pragma unroll
     for (int half = 0; half < kStep / 16; ++half) {
-    const int n = n2 + 16 * half;
-    if (n >= n_hi) break;
-    RawK<DH> rk;
-    read_k<DH>(st, half, g, t, rk);
-    // S^T: slots sg and sg + 8 (c / 2), rows 2 t and 2 t + 1 (c & 1) of block nb
-    float s[NB][4];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[nb][c] = 0.f;
-#pragma unroll
-    for (int w = 0; w < KS / 2; ++w) {
-      uint32_t a0[4], a1[4];
-      dequant_k<DH>(rk, w, a0, a1);
+      const int n = n2 + 16 * half;
+      if (n >= n_hi) break;
+      RawK<DH> rk;
+      read_k<DH>(st, half, g, t, rk);
+      // S^T: slots sg and sg + 8 (c / 2), rows 2 t and 2 t + 1 (c & 1) of block nb
+      float s[NB][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-{
-        const uint4* q = qs + (nb * P * (KS / 2) + w) * 32 + lane;
-        add_products<F32>(s[nb], a0, a1, q[0], q[(P - 1) * (KS / 2) * 32]);
-      }
-    }
-    const bool masked = n < all_lo || n + 16 > all_hi;
-    int pos[2] = {n + sg, n + sg + 8};
-    if (GEN && kpos != nullptr) {
-      pos[0] = __ldg(kpos + min(pos[0], last));
-      pos[1] = __ldg(kpos + min(pos[1], last));
-    }
-    uint32_t ph[NB][2], pl[NB][F32 ? 2 : 1];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      // the four scores less sub
-      auto scores = [&](const float* sub, float* x) {
-        if (F32) {
+        for (int c = 0; c < 4; ++c) s[nb][c] = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float raw = s[nb][c] * fa[nb][c & 1];
-            x[c] = fmaf(capped ? a.cap * tanhf(raw * a.inv_cap) : raw, kLog2e, -sub[c & 1]);
-          }
-        } else if (capped) {  // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            x[c] = fmaf(-2.f * cap2, rcp_approx(exp2_approx(s[nb][c] * fa[nb][c & 1]) + 1.f),
-                        cap2 - sub[c & 1]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = fmaf(s[nb][c], fa[nb][c & 1], -sub[c & 1]);
-        }
-        if (GEN && a.slope != nullptr) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
-            x[c] = fmaf(-rp.slope * kLog2e, fabsf((float)(rp.qpos - pos[c >> 1])), x[c]);
-          }
-        }
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
-            if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
-              x[c] = -INFINITY;
-          }
-        }
-      };
-      float x[4];
-      scores(base[nb], x);
-      // The running maximum follows only when some row has outgrown it by
-      // 2^kGrow; until then P carries a factor up to that.
-      if (__any_sync(0xffffffffu,
-                     fmaxf(fmaxf(x[0], x[2]), fmaxf(x[1], x[3])) > kPShift + kGrow)) {
-        const float zero[2] = {0.f, 0.f};
-        scores(zero, x);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float mx = fmaxf(x[u], x[2 + u]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) - kPShift;
-          if (mx > base[nb][u] + kGrow) {
-            const float corr = exp2_approx(base[nb][u] - mx);
-            base[nb][u] = mx;
-            lrow[nb][u] *= corr;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              o[nb][i][u] *= corr;
-              o[nb][i][2 + u] *= corr;
-            }
-          }
-          x[u] -= base[nb][u];
-          x[2 + u] -= base[nb][u];
-        }
-      }
-      float p[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        p[c] = exp2_approx(x[c]);
-        lrow[nb][c & 1] += p[c];
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {  // slots 8 j .. 8 j + 7: (slot, rows) -> (row, slots)
-        const __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
-        ph[nb][j] = transpose8(h2_bits(h));
-        if constexpr (F32) {
-          const float2 back = __half22float2(h);
-          pl[nb][j] =
-              transpose8(h2_bits(__floats2half2_rn(p[2 * j] - back.x, p[2 * j + 1] - back.y)));
-        }
-      }
-    }
-    // O^T += V^T P^T
-    RawV<DH> rv;
-    read_v<DH>(st + R::kV, half, g, t, rv);
-#pragma unroll
-    for (int w = 0; w < DH / 64; ++w) {
-      uint32_t v[2][2][4];  // [even, odd element][slots t and t + 4, t + 8 and t + 12][byte]
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t even, odd;
-        pair_codes(rv.c[2 * j][w], rv.c[2 * j + 1][w], &even, &odd);
-        const int sh = DH == 256 ? 8 * (w / 2) : 0;
-        const __half2 sc =
-            e4m3x2_f16(((rv.s[2 * j] >> sh) & 0xffu) | ((rv.s[2 * j + 1] >> sh) & 0xffu) << 8);
-        e2m1x8_f16(even, v[0][j]);
-        e2m1x8_f16(odd, v[1][j]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[e][j][q] = h2_bits(__hmul2(h2_of(v[e][j][q]), sc));
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t av[4] = {v[0][0][q], v[1][0][q], v[0][1][q], v[1][1][q]};
+      for (int w = 0; w < KS / 2; ++w) {
+        uint32_t a0[4], a1[4];
+        dequant_k<DH>(rk, w, a0, a1);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          float* d = o[nb][4 * w + q];
-          if constexpr (F32) {
-            // added by a rounding instruction, as the scores
-            float e[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(e, av, ph[nb][0], ph[nb][1]);
-            mma_f16(e, av, pl[nb][0], pl[nb][1]);
+          const uint4* q = qs + (nb * P * (KS / 2) + w) * 32 + lane;
+          add_products<F32>(s[nb], a0, a1, q[0], q[(P - 1) * (KS / 2) * 32]);
+        }
+      }
+      const bool masked = n < all_lo || n + 16 > all_hi;
+      int pos[2] = {n + sg, n + sg + 8};
+      if (GEN && kpos != nullptr) {
+        pos[0] = __ldg(kpos + min(pos[0], last));
+        pos[1] = __ldg(kpos + min(pos[1], last));
+      }
+      uint32_t ph[NB][2], pl[NB][F32 ? 2 : 1];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) d[c] += e[c];
+      for (int nb = 0; nb < NB; ++nb) {
+        // the four scores less sub
+        auto scores = [&](const float* sub, float* x) {
+          if (F32) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float raw = s[nb][c] * fa[nb][c & 1];
+              x[c] = fmaf(capped ? a.cap * tanhf(raw * a.inv_cap) : raw, kLog2e, -sub[c & 1]);
+            }
+          } else if (capped) {  // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              x[c] = fmaf(-2.f * cap2, rcp_approx(exp2_approx(s[nb][c] * fa[nb][c & 1]) + 1.f),
+                          cap2 - sub[c & 1]);
           } else {
-            mma_f16(d, av, ph[nb][0], ph[nb][1]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[c] = fmaf(s[nb][c], fa[nb][c & 1], -sub[c & 1]);
+          }
+          if (GEN && a.slope != nullptr) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
+              x[c] = fmaf(-rp.slope * kLog2e, fabsf((float)(rp.qpos - pos[c >> 1])), x[c]);
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
+              if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
+                x[c] = -INFINITY;
+            }
+          }
+        };
+        float x[4];
+        scores(base[nb], x);
+        // The running maximum follows only when some row has outgrown it by
+        // 2^kGrow; until then P carries a factor up to that.
+        if (__any_sync(0xffffffffu,
+                       fmaxf(fmaxf(x[0], x[2]), fmaxf(x[1], x[3])) > kPShift + kGrow)) {
+          const float zero[2] = {0.f, 0.f};
+          scores(zero, x);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float mx = fmaxf(x[u], x[2 + u]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) - kPShift;
+            if (mx > base[nb][u] + kGrow) {
+              const float corr = exp2_approx(base[nb][u] - mx);
+              base[nb][u] = mx;
+              lrow[nb][u] *= corr;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[nb][i][u] *= corr;
+                o[nb][i][2 + u] *= corr;
+              }
+            }
+            x[u] -= base[nb][u];
+            x[2 + u] -= base[nb][u];
+          }
+        }
+        float p[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          p[c] = exp2_approx(x[c]);
+          lrow[nb][c & 1] += p[c];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // slots 8 j .. 8 j + 7: (slot, rows) -> (row, slots)
+          const __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
+          ph[nb][j] = transpose8(h2_bits(h));
+          if constexpr (F32) {
+            const float2 back = __half22float2(h);
+            pl[nb][j] =
+                transpose8(h2_bits(__floats2half2_rn(p[2 * j] - back.x, p[2 * j + 1] - back.y)));
           }
         }
       }
-    }
+      // O^T += V^T P^T
+      RawV<DH> rv;
+      read_v<DH>(st + R::kV, half, g, t, rv);
+#pragma unroll
+      for (int w = 0; w < DH / 64; ++w) {
+        uint32_t v[2][2][4];  // [even, odd element][slots t and t + 4, t + 8 and t + 12][byte]
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t even, odd;
+          pair_codes(rv.c[2 * j][w], rv.c[2 * j + 1][w], &even, &odd);
+          const int sh = DH == 256 ? 8 * (w / 2) : 0;
+          const __half2 sc =
+              e4m3x2_f16(((rv.s[2 * j] >> sh) & 0xffu) | ((rv.s[2 * j + 1] >> sh) & 0xffu) << 8);
+          e2m1x8_f16(even, v[0][j]);
+          e2m1x8_f16(odd, v[1][j]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[e][j][q] = h2_bits(__hmul2(h2_of(v[e][j][q]), sc));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t av[4] = {v[0][0][q], v[1][0][q], v[0][1][q], v[1][1][q]};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float* d = o[nb][4 * w + q];
+            if constexpr (F32) {
+              // added by a rounding instruction, as the scores
+              float e[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(e, av, ph[nb][0], ph[nb][1]);
+              mma_f16(e, av, pl[nb][0], pl[nb][1]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) d[c] += e[c];
+            } else {
+              mma_f16(d, av, ph[nb][0], ph[nb][1]);
+            }
+          }
+        }
+      }
     }
   }
 
@@ -685,6 +693,9 @@ k_kv4_combine(const __grid_constant__ Kv4AttnArgs a) {
 // while all rows of the head pass by (kWRows at a time through shared memory);
 // every slot's sum is one warp's, in row order, so the result does not depend
 // on timing.
+// Rows from which k_kv4_weight_tc takes over.  It pays more a slot and less a row:
+// 4 x 32 heads, 4096 slots: 64 rows 71 us there and 42 here, 96 rows 67 and 121;
+// 2 x 8 heads, 16 K slots: 36 and 22, 35 and 65.
 constexpr int kTcWeight = 64;
 constexpr int kWRows = 64;
 constexpr int kGroup = kStep * kWarps;  // slots that a CTA takes at a time
@@ -714,8 +725,8 @@ __device__ __forceinline__ SeenRange seen_range(const RowPar* par, int rows, int
 
 // acc[j] += sum over nbs blocks of 8 rows of exp(score - lse), slots n + sg + 8 j.
 template <int DH, bool F32, bool GEN>
-__device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)[4], const uint4* qp,
-                                      const RowPar* rp, int nbs, int n_sg, int len, const int* pos,
+__device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)[4],
+                                      const uint4* qp, const RowPar* rp, int nbs, int n_sg, int len, const int* pos,
                                       bool masked, float* acc) {
   constexpr int KS = DH / 16, P = F32 ? 2 : 1;
 #pragma unroll 1
@@ -932,7 +943,10 @@ struct AttnPlan {
 AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
   AttnPlan p;
   const int M = T * (Hq / Hkv);
-  p.tc = dtype == PS_BF16 && dh <= 128 && M > 16;
+  // From 33 rows on the tcgen05 kernel reads the slots fewer times.  4 x 32 heads,
+  // 768 slots: 32 rows 17.2 us there and 15.6 here, 48 rows 17.2 and 28; 4 x 8
+  // heads, 4096 slots: 32 rows 23.5 and 19.5, 64 rows 24 and 31.
+  p.tc = dtype == PS_BF16 && dh <= 128 && M > 32;
   if (p.tc) {
     p.nb = 0;
     p.ntile = ceil_div(M, 256);
@@ -951,7 +965,10 @@ AttnPlan attn_plan(int dtype, int B, int N, int Hq, int Hkv, int dh, int T) {
     }
     return p;
   }
-  p.nb = M <= 8 ? 1 : M <= 16 || dh > 128 ? 2 : 4;
+  // 16-row tiles from 9 rows on: 16 rows, 4 x 8 heads, 4096 slots 15.6 us against
+  // 16.2 as two of 8, 64 fp32 rows 42 against 57; 8 rows in a 16-row tile 14.5
+  // against 13.4.  (32-row tiles for fp32: 70, too few warps an SM.)
+  p.nb = M <= 8 ? 1 : 2;
   p.ntile = ceil_div(M, 8 * p.nb);
   const long base = (long)B * Hkv * p.ntile;
   const int most = ceil_div(N, 128);  // at least 128 slots a share
@@ -1019,9 +1036,6 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
   PS_KV4_CASE(256, 1)
   PS_KV4_CASE(256, 2)
 #undef PS_KV4_CASE
-  // 32 rows: fp32 queries only, bf16 ones are on the tcgen05 kernel by then
-  if (a.dh == 64 && p.nb == 4 && f32) return launch_attn<64, 4, true, true>(a, s);
-  if (a.dh == 128 && p.nb == 4 && f32) return launch_attn<128, 4, true, true>(a, s);
   return cudaErrorInvalidValue;
 }
 

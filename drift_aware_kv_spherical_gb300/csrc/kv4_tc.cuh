@@ -43,9 +43,9 @@ __device__ __forceinline__ void load_row(const uint8_t* codes, const uint8_t* sc
     o.s.y = 0;
   }
 }
-// 32 query rows of a warp into their place in an operand, as they are (bf16): cp.async in whole rows.  `src` is
-// the lane's own row, null past the last one: zeros (never stored, but a vote of
-// the warp must not hang on what was there).
+// 32 query rows of a warp into their place in an operand, as they are (bf16):
+// cp.async in whole rows.  `src` is the lane's own row, null past the last one:
+// zeros (never stored, but a vote of the warp must not hang on what was there).
 template <int DH>
 __device__ __forceinline__ void fetch_q(const void* any, const __nv_bfloat16* src, uint32_t qs,
                                         int r) {
