@@ -1,8 +1,8 @@
 // Attention over a 4-bit KV cache for many query rows a KV head, on the
 // tcgen05 tensor cores.
 //
-// A CTA an SM takes items in turn: 256 rows (two tiles of 128) of one KV head
-// against a share of its slots, 128 slots a step.  13 warps:
+// A CTA an SM takes item after item: 256 rows (two tiles of 128) of one KV head
+// against a share of its slots, 128 slots a step.  14 warps:
 //   0-3, 4-7  softmax of row tile 0 / 1: a thread a row.  Reads its 128 scores
 //             from TMEM, keeps the running maximum and sum in registers, writes
 //             P (f16) over the scores, 64 slots at a time, and rescales O in
@@ -30,7 +30,8 @@
 namespace ps {
 namespace {
 
-constexpr int kTcThreads = 416;
+constexpr int kTcThreads = 448;
+constexpr int kRing = 4;            // items known and not yet taken by every warp
 constexpr int kTile = 128;          // slots a step; rows of a row tile
 constexpr float kGrow = 8.f;        // log2 growth of a maximum before O is rescaled
 constexpr float kTcShift = 4.f;     // log2 of the factor that P carries: P <= 2^12 in f16
@@ -41,9 +42,10 @@ struct TcSmem {
   static constexpr uint32_t kK = 2 * kOp,  // Q at 0
                             kV = 4 * kOp, kPos = 6 * kOp;
   static constexpr uint32_t kRow = kPos + 4 * kTile * 4;           // TcRow [256]
-  static constexpr uint32_t kWork = kRow + 2 * kTile * 24;         // TcWork, TcStride [8 warps]
-  static constexpr uint32_t kBar = kWork + 8 * 64;
-  static constexpr size_t kBytes = 1024 + kBar + 256;
+  static constexpr uint32_t kWork = kRow + 2 * kTile * 24;         // TcWork [8 warps]
+  static constexpr uint32_t kBar = kWork + 8 * 32;
+  static constexpr uint32_t kItems = kBar + 256;  // TcWork [kRing], then a claim's 16 bytes
+  static constexpr size_t kBytes = 1024 + kItems + kRing * 32 + 16;
 };
 
 // D(tmem) (+)= A . B, f16 operands: A from shared memory, or from TMEM.
@@ -66,33 +68,43 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) {
 }
 
 // ---------------------------------------------------------------- work items
-// An item: 256 rows of one KV head against one share of its slots.  A CTA takes
-// every gridDim.x-th; the mixed-radix step between two of its items saves the
-// divisions.
+// An item: 256 rows of one KV head against one share of its slots; an item is a
+// CTA of the grid.  The CTAs that run claim those not yet begun, one ahead, so
+// that items of unequal length (spans, ragged lengths) leave no SM idle: every
+// 152nd item in turn took 8-45 % longer on packed documents of random lengths.
 struct TcWork {
   int item, split, tile, hkv, b;
   int n_lo, nt;  // first slot, steps
   int two;       // the second row tile holds rows
 };
-struct TcStride {
-  int split, tile, hkv, b;
-};
-__device__ __forceinline__ TcStride tc_digits(const Kv4AttnArgs& a, int n) {
-  TcStride d;
-  d.split = n % a.nsplit;
-  n /= a.nsplit;
-  d.tile = n % a.ntile;
-  n /= a.ntile;
-  d.hkv = n % a.Hkv;
-  d.b = n / a.Hkv;
-  return d;
+
+// A claim asked for: 16 bytes at `to` and `bar` completed.
+__device__ __forceinline__ void claim_ask(uint4* to, uint64_t* bar) {
+  tc::mbar_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(tc::smem_u32(to)),
+      "r"(tc::smem_u32(bar))
+      : "memory");
+}
+// The claimed item, or -1: none is left.
+__device__ __forceinline__ int claim_get(const uint4* from) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(tc::smem_u32(from))
+      : "memory");
+  return got ? (int)x : -1;
 }
 
 // The slots of w, for a whole warp: those within the rows' spans.
-__device__ __forceinline__ void tc_slots(const Kv4AttnArgs& a, TcWork& w, int items) {
-  w.n_lo = w.nt = 0;
-  w.two = 0;
-  if (w.item >= items) return;
+__device__ __forceinline__ void tc_slots(const Kv4AttnArgs& a, TcWork& w) {
   const int m0 = w.tile * 2 * kTile;
   w.two = a.M - m0 > kTile;
   int n_lo = 0;
@@ -121,25 +133,41 @@ __device__ __forceinline__ void tc_slots(const Kv4AttnArgs& a, TcWork& w, int it
   }
   w.nt = (n + kTile - 1) / kTile;
 }
-__device__ __forceinline__ TcWork tc_first(const Kv4AttnArgs& a, int items) {
-  const TcStride d = tc_digits(a, blockIdx.x);
-  TcWork w{(int)blockIdx.x, d.split, d.tile, d.hkv, d.b, 0, 0, 0};
-  tc_slots(a, w, items);
+__device__ __forceinline__ TcWork tc_item(const Kv4AttnArgs& a, int item) {
+  TcWork w{item, 0, 0, 0, 0, 0, 0, 0};
+  if (item < 0) return w;
+  int n = item;
+  w.split = n % a.nsplit;
+  n /= a.nsplit;
+  w.tile = n % a.ntile;
+  n /= a.ntile;
+  w.hkv = n % a.Hkv;
+  w.b = n / a.Hkv;
+  tc_slots(a, w);
   return w;
 }
-__device__ __forceinline__ TcWork tc_next(const Kv4AttnArgs& a, TcWork w, const TcStride& d,
-                                          int items) {
-  w.item += gridDim.x;
-  w.split += d.split;
-  w.tile += d.tile;
-  w.hkv += d.hkv;
-  w.b += d.b;
-  if (w.split >= a.nsplit) { w.split -= a.nsplit; ++w.tile; }
-  if (w.tile >= a.ntile) { w.tile -= a.ntile; ++w.hkv; }
-  if (w.hkv >= a.Hkv) { w.hkv -= a.Hkv; ++w.b; }
-  tc_slots(a, w, items);
-  return w;
-}
+
+// The items of a CTA, for a warp of any role; warp 13 claims them and works out
+// what they are.
+struct TcItems {
+  uint64_t *full, *empty;  // an item: known, taken by every warp
+  const TcWork* ring;
+  int n = 0;  // taken
+  // the next item (.item -1: the end); false after a timeout
+  __device__ __forceinline__ bool take(const Kv4AttnArgs& a, volatile int* abort_flag, TcWork* w) {
+    const int k = n % kRing;
+    const bool ok = tc::mbar_wait(full + k, (n / kRing) & 1, a.status, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    *w = ring[k];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(empty + k);
+    ++n;
+    return true;
+  }
+  __device__ __forceinline__ bool ready() const {
+    return __all_sync(0xffffffffu, tc::mbar_test(full + n % kRing, (n / kRing) & 1));
+  }
+};
 
 // ---------------------------------------------------------------- slots
 __device__ __forceinline__ void l2_prefetch(const void* p, int bytes) {
@@ -439,7 +467,7 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
 // GEN: kCap, capped scores; kAny, a distance bias or explicit positions too.
 template <int DH, int GEN>
 __global__ void __launch_bounds__(kTcThreads, 1)
-k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
+k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
   using SM = TcSmem<DH>;
   pdl_prologue();
   extern __shared__ uint8_t smem_raw[];
@@ -451,7 +479,10 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
   uint64_t *s_full = k_full + 8, *o_full = k_full + 10, *q_full = k_full + 12;
   uint64_t* p_full = k_full + 14;  // [row tile][half of the slots]
   uint64_t* drain = k_full + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 19);
+  uint64_t *c_full = k_full + 19, *c_empty = c_full + kRing, *c_ask = c_empty + kRing;
+  uint64_t* c_done = c_ask + 1;
+  TcWork* ring = reinterpret_cast<TcWork*>(smem + SM::kItems);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -471,6 +502,12 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
       tc::mbar_init(p_full + 2 + i, 4);
     }
     tc::mbar_init(drain, 1);
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(c_full + i, 1);
+      tc::mbar_init(c_empty + i, 13);
+    }
+    tc::mbar_init(c_ask, 4);
+    tc::mbar_init(c_done, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
@@ -479,6 +516,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  TcItems next{c_full, c_empty, ring};
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -489,17 +527,17 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
     uint8_t* qs = smem + g * SM::kOp;         // the row tile's operand
     const int qr = (warp & 3) * 32;           // the warp's first row in it
     volatile int* rowp = reinterpret_cast<volatile int*>(smem + SM::kRow) + 6 * tid;
-    volatile int* keep = reinterpret_cast<volatile int*>(smem + SM::kWork) + warp * 16;
+    volatile int* keep = reinterpret_cast<volatile int*>(smem + SM::kWork) + warp * 8;
     bool ok = true;
     int it = 0, rounds = 0, all = 0;  // the row tile's steps and items, both row tiles' steps
     int nt;
     {
-      if (lane == 0) sm_put(keep + 8, tc_digits(a, gridDim.x));
-      const TcWork w = tc_first(a, items);
+      TcWork w{-1, 0, 0, 0, 0, 0, 0, 0};
+      ok = next.take(a, abort_flag, &w);
       if (lane == 0) sm_put(keep, w);
       __syncwarp();
     }
-    while (ok && keep[0] < items) {
+    while (ok && keep[0] >= 0) {
       TcRange range;
       float f2;
       bool act;
@@ -530,7 +568,8 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; act && j < nt; ++j, ++it) {
         const int n0 = n_lo + j * kTile;
-        if (!tc::mbar_wait(s_full + g, it & 1, a.status, abort_flag)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(s_full + g, it & 1, a.status, abort_flag));
+        if (!ok) break;
         tc::fence_after_sync();
         const TcSeen seen0 = by_pos ? kSome : tc_seen(range, n0);
         const TcSeen seen1 = by_pos ? kSome : tc_seen(range, n0 + 64);
@@ -554,11 +593,12 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
         m_used = -INFINITY;
       }
       {
-        const TcWork wn = tc_next(a, w, sm_get<TcStride>(keep + 8), items);
+        TcWork wn{-1, 0, 0, 0, 0, 0, 0, 0};
+        if (ok) ok = next.take(a, abort_flag, &wn);
         __syncwarp();
         if (lane == 0) sm_put(keep, wn);
         __syncwarp();
-        if (wn.item < items) {  // the next item's queries into L2 while this one is finished
+        if (wn.item >= 0) {  // the next item's queries into L2 while this one is finished
           const int mn = wn.tile * 2 * kTile + r0 + lane, tn = row_token(a, mn);
           if (mn < a.M)
             l2_prefetch(static_cast<const __nv_bfloat16*>(a.Q) +
@@ -568,7 +608,8 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
         }
       }
       if (act && ok) {
-        ok = tc::mbar_wait(o_full + g, rounds & 1, a.status, abort_flag);
+        ok = __all_sync(0xffffffffu,
+                        tc::mbar_wait(o_full + g, rounds & 1, a.status, abort_flag));
         tc::fence_after_sync();
         ++rounds;
       }
@@ -647,33 +688,50 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
     // ------------------------------------------------------------ slots
     const int p = tid - 256, last = a.Ncache - 1;
     RawRow<DH> rk, rv;
-    // the first item from x on with slots to read
-    const TcStride stride = tc_digits(a, gridDim.x);
-    auto busy = [&](TcWork x) {
-      while (x.item < items && x.nt == 0) x = tc_next(a, x, stride, items);
-      return x;
+    bool ok = true;
+    auto ask = [&] {  // for the next item
+      if (lane == 0) tc::mbar_arrive(c_ask);
+    };
+    // the next item with slots to read (-1: the end)
+    auto take = [&](TcWork* x) {
+      do {
+        ok = next.take(a, abort_flag, x);
+        if (!ok) x->item = -1;
+        if (ok && x->item >= 0 && x->nt <= 2) ask();
+      } while (x->item >= 0 && x->nt == 0);
     };
     auto load = [&](const TcWork& x, int j, const uint8_t* c, const uint8_t* s, RawRow<DH>& o) {
       const long base = (long)(x.b * a.Hkv + x.hkv) * a.Ncache;
       load_row<DH>(c, s, base + min((long)x.n_lo + (long)j * kTile + p, (long)last), o);
     };
-    TcWork w = busy(tc_first(a, items));
+    TcWork w;
+    take(&w);
     int j = 0;
-    if (w.item < items) {
+    if (w.item >= 0) {
       load(w, 0, a.kcode, a.kscale, rk);
       load(w, 0, a.vcode, a.vscale, rv);
     }
-    for (int it = 0; w.item < items; ++it) {
+    for (int it = 0; w.item >= 0; ++it) {
       const int st = it & 1;
       const uint32_t ph = ((it >> 1) & 1) ^ 1;
       TcWork wn = w;
       int jn = j + 1;
+      // the next item is asked for two steps before this one's end, and its first
+      // slots loaded under the last step if the answer is there
+      if (w.nt > 2 && jn == w.nt - 2) ask();
+      bool known = true;
       if (jn == w.nt) {
-        wn = busy(tc_next(a, w, stride, items));
+        known = next.ready();
         jn = 0;
+        if (known) {
+          ok = next.take(a, abort_flag, &wn);
+          if (ok && wn.item >= 0 && wn.nt <= 2) ask();
+          known = ok && (wn.item < 0 || wn.nt > 0);
+        }
       }
-      const bool more = wn.item < items;
-      if (!tc::mbar_wait(k_empty + st, ph, a.status, abort_flag)) break;
+      const bool more = known && wn.item >= 0;
+      if (ok) ok = tc::mbar_wait(k_empty + st, ph, a.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
       if (by_pos)
         pos_ring[(it & 3) * kTile + p] =
             a.kpos[(long)(w.b * a.Hkv + w.hkv) * a.Ncache + min(w.n_lo + j * kTile + p, last)];
@@ -682,14 +740,56 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(k_full + st);
       if (more) load(wn, jn, a.kcode, a.kscale, rk);
-      if (!tc::mbar_wait(v_empty + st, ph, a.status, abort_flag)) break;
+      ok = tc::mbar_wait(v_empty + st, ph, a.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
       put_row<DH>(smem + SM::kV + st * SM::kOp, p, rv);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(v_full + st);
       if (more) load(wn, jn, a.vcode, a.vscale, rv);
+      if (!known) {
+        take(&wn);
+        if (wn.item >= 0) {
+          load(wn, 0, a.kcode, a.kscale, rk);
+          load(wn, 0, a.vcode, a.vscale, rv);
+        }
+      }
       w = wn;
       j = jn;
+    }
+  } else if (warp == 13) {
+    // ------------------------------------------------------------ claims
+    uint4* claim = reinterpret_cast<uint4*>(ring + kRing);
+    int item = blockIdx.x;
+    for (int k = 0;; ++k) {
+      const int at = k % kRing;
+      const TcWork w = tc_item(a, item);
+      bool ok = tc::mbar_wait(c_empty + at, ((k / kRing) & 1) ^ 1, a.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        ring[at] = w;
+        tc::mbar_arrive(c_full + at);
+      }
+      if (item < 0) break;
+      ok = tc::mbar_wait(c_ask, k & 1, a.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        tc::fence_proxy_async_smem();  // the last claim has been read
+        claim_ask(claim, c_done);
+      }
+      __syncwarp();
+      // waits for the answer whatever else happens: it is written to this CTA
+      const uint64_t t0 = tc::globaltimer();
+      while (!(ok = tc::mbar_try_wait(c_done, k & 1)) &&
+             tc::globaltimer() - t0 < tc::kWaitLimitNs) {
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        set_status(a.status, PS_ERR_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+      item = claim_get(claim);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ MMAs
@@ -751,20 +851,22 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a, const int items) {
       }
       __syncwarp();
     };
-    const TcStride stride = tc_digits(a, gridDim.x);
-    TcWork w = tc_first(a, items);
-    while (ok && w.item < items) {
-      const TcWork wn = tc_next(a, w, stride, items);
+    TcWork w, wn;
+    ok = next.take(a, abort_flag, &w);
+    while (ok && w.item >= 0) {
       if (w.nt > 0) {
         wait(k_full + (it & 1), it >> 1);
         first_s(0, i0++, !w.two);
         if (w.two) first_s(1, i1++, true);
       }
+      bool known = false;
       for (int j = 0; ok && j < w.nt; ++j, ++it) {
+        if (j + 1 == w.nt && next.ready()) known = ok = next.take(a, abort_flag, &wn);
         wait(v_full + (it & 1), it >> 1);
         row_tile(0, c0++, !w.two, j == 0, j + 1 < w.nt);
         if (w.two) row_tile(1, c1++, true, j == 0, j + 1 < w.nt);
       }
+      if (ok && !known) ok = next.take(a, abort_flag, &wn);
       w = wn;
     }
     if (!__all_sync(0xffffffffu, ok)) {  // wait for the MMAs issued before TMEM is freed
@@ -792,9 +894,8 @@ cudaError_t launch_tc(const Kv4AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  const int items = a.B * a.Hkv * a.ntile * a.nsplit;
-  const int grid = items < a.num_sms ? items : a.num_sms;
-  return launch_pdl(kern, dim3((unsigned)grid), dim3(kTcThreads), TcSmem<DH>::kBytes, s, a, items);
+  const unsigned items = (unsigned)(a.B * a.Hkv * a.ntile * a.nsplit);
+  return launch_pdl(kern, dim3(items), dim3(kTcThreads), TcSmem<DH>::kBytes, s, a);
 }
 
 }  // namespace

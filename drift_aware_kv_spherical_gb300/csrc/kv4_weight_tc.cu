@@ -173,19 +173,6 @@ __device__ __forceinline__ float weigh_all(const Kv4AttnArgs& a, uint32_t col, c
   return sum;
 }
 
-// Whether a phase is over, without waiting for it.
-__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(tc::smem_u32(b)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 template <int DH, bool GEN>
 __global__ void __launch_bounds__(kWThreads, 1)
 k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
@@ -348,7 +335,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
       const uint32_t ph = ((i / kStages) & 1) ^ 1;
       StepRows& rows = steps[st];
       // no stage free: what is under way is handed over first
-      if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test(empty + st, ph))) {
+      if (pending >= 0 && !__all_sync(0xffffffffu, tc::mbar_test(empty + st, ph))) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         publish(pending);
         pending = -1;
