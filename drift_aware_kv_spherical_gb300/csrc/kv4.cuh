@@ -89,6 +89,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Small capped scores: for |y| <= kTanhTop, tanh y = y (1 + z p(z)), z = y^2, p
+// interpolated at the Chebyshev nodes of [0, kTanhTop^2]; relative error 4.3e-8.
+constexpr float kTanhTop = 0.3f;
+constexpr float kTanh0 = -0.33333286f, kTanh1 = 0.13323874f, kTanh2 = -0.051132676f;
+__device__ __forceinline__ float tanh_small(float y) {
+  const float z = y * y;
+  return fmaf(y, z * fmaf(z, fmaf(z, kTanh2, kTanh1), kTanh0), y);
+}
+
 // D += A B, m16n8k16, f16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(

@@ -308,6 +308,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
+// Four scores capped to fp32's precision, for a whole warp.
+__device__ __forceinline__ void cap4(const Kv4AttnArgs& a, float* x) {
+  float y[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) y[c] = x[c] * a.inv_cap;
+  const float top = max3(fmaxf(fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
+  if (__all_sync(0xffffffffu, top <= kTanhTop)) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = a.cap * tanh_small(y[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = a.cap * tanhf(y[c]);
+  }
+}
+
 // GEN: a distance bias or explicit positions.
 template <int DH, int NB, bool F32, bool GEN>
 __global__ void __launch_bounds__(kThreads, DH <= 128 && NB == 1 && !F32 ? 5 : 1)
@@ -435,11 +450,12 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
         // the four scores less sub
         auto scores = [&](const float* sub, float* x) {
           if (F32) {
+            float y[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float raw = s[nb][c] * fa[nb][c & 1];
-              x[c] = fmaf(capped ? a.cap * tanhf(raw * a.inv_cap) : raw, kLog2e, -sub[c & 1]);
-            }
+            for (int c = 0; c < 4; ++c) y[c] = s[nb][c] * fa[nb][c & 1];
+            if (capped) cap4(a, y);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[c] = fmaf(y[c], kLog2e, -sub[c & 1]);
           } else if (capped) {  // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -742,8 +758,10 @@ __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)
     const float f0 = rp[0].f, l0 = -rp[0].lse, f1 = rp[1].f, l1 = -rp[1].lse;
     if (GEN && a.cap > 0.f) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        x[c] = fmaf(a.cap, tanhf(s[c] * (c & 1 ? f1 : f0) * a.inv_cap), c & 1 ? l1 : l0);
+      for (int c = 0; c < 4; ++c) x[c] = s[c] * (c & 1 ? f1 : f0);
+      cap4(a, x);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] += c & 1 ? l1 : l0;
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] = fmaf(s[c], c & 1 ? f1 : f0, c & 1 ? l1 : l0);

@@ -26,10 +26,11 @@
 // to that.
 //
 // What bounds it: a step's chain of product, two passes over 64 scores from TMEM
-// and P back, of which two row tiles hide only half: 4096 rows x 32 heads x 2 on
-// 4096 slots 419 us, 1.31 PFLOP/s, 68 % of a large library product's rate (the
-// tensor cores are busy half the time, exponentials a quarter).  Caps and biases
-// add score arithmetic to the chain: 198 and 253 us where plain scores take 118.
+// and P back, of which two row tiles hide only half.  4096 rows x 32 heads x 2 on
+// 4096 slots 419 us, 1.31 PFLOP/s, 68 % of a large library product's rate; the
+// tensor cores are busy half the time, the exponentials' unit a quarter.  Caps and
+// biases lengthen the chain: 2048 rows x 32 heads on 4096 slots 123 us plain, 198
+// capped, 254 with a bias too.
 // Every mbarrier wait is bounded (tc::mbar_wait); after a timeout the CTA waits
 // for the MMAs it issued, frees TMEM and returns with the status word set.
 #include "kv4_tc.cuh"

@@ -63,14 +63,11 @@ __device__ __forceinline__ void fetch_q(const void* any, const __nv_bfloat16* sr
   }
 }
 
-// Small capped scores, s[c] -> u tanh(y) / y with u = f s[c] and y = k u, where
-// |y| <= kTanhTop: tanh y = y (1 + z p(z)), z = y^2, p interpolated at the
-// Chebyshev nodes of [0, kTanhTop^2]; relative error 4.3e-8.
-constexpr float kTanhTop = 0.3f;
+// The same for C of them, two at a time: s[c] -> u tanh(y) / y, u = f s[c], y = k u.
 template <int C>
 __device__ __forceinline__ void cap_series(float* s, float f, float k) {
   const float k2 = k * k;
-  const float c0 = k2 * -0.33333286f, c1 = k2 * k2 * 0.13323874f, c2 = k2 * k2 * k2 * -0.051132676f;
+  const float c0 = k2 * kTanh0, c1 = k2 * k2 * kTanh1, c2 = k2 * k2 * k2 * kTanh2;
   const uint64_t ff = f2_pack(f, f), cc0 = f2_pack(c0, c0), cc1 = f2_pack(c1, c1),
                  cc2 = f2_pack(c2, c2);
 #pragma unroll
