@@ -530,3 +530,19 @@ def test_weight_of_many_rows(B, T, Hq, Hkv, dh, N, mask, cap, bias):
 def test_capped_scores_of_many_rows(T, dh, N, mask, cap):
     """Capped scores without a bias: small ones, and ones at the cap."""
     test_attention_and_weight(2, T, 6, 2, dh, N, BF16, mask, cap, False)
+
+
+@pytest.mark.parametrize("T", [1, 20, 90])
+def test_queries_of_part_of_a_sequence(T):
+    """Q as some tokens of a longer [B][T'][Hq][dh]: a stride between sequences."""
+    B, Hq, Hkv, dh, N = 3, 4, 2, 64, 300
+    c, _, _ = _cache(B, Hkv, N, dh, 8)
+    Q, _ = _query(B, T + 9, Hq, dh, BF16, 8)
+    part = Q[:, 5:5 + T]
+    O, lse = _attn(c, part, scale=0.125)
+    O2, lse2 = _attn(c, part.contiguous(), scale=0.125)
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    w, w2 = torch.zeros(B, Hkv, N, device="cuda"), torch.zeros(B, Hkv, N, device="cuda")
+    ps.ps_kv4_weight(c, part, lse, None, w, scale=0.125)
+    ps.ps_kv4_weight(c, part.contiguous(), lse, None, w2, scale=0.125)
+    assert torch.equal(w, w2)
