@@ -61,24 +61,34 @@ class Kv4Layer:
 
     def evict(self, keep, sink=0, recent=0, spare=None, stream=None):
         """Cuts every sequence to `keep` slots: the first `sink`, the last
-        `recent`, the heaviest of the others.  The kept slots move to `spare`, a
-        cache of the same shape (made on the first call when not given), and the
-        old one becomes the next call's spare; layers of one shape can pass one
-        spare on: evict returns it."""
+        `recent`, the heaviest of the others.  The kept slots move to `spare`,
+        the buffers that an earlier eviction of a layer of this shape left
+        behind (not given: this layer's own ones, made on the first call), and
+        the old ones are returned as the next call's spare.  Layers of one shape
+        can pass one spare on, round after round:
+
+            for layer in layers:
+                spare = layer.evict(keep, spare=spare)
+
+        A spare serves one eviction, which empties it."""
         c = self.cache
         i32 = dict(dtype=torch.int32, device=c.device)
-        if spare is not None:
-            self._spare = spare
-        if self._spare is None:
-            self._spare = dict(
-                cache=ps.Kv4Cache.empty(c.B, c.Hkv, c.N, c.dh, c.kmul, c.vmul, c.device),
-                w=torch.zeros_like(self.w), kpos=torch.zeros(c.B, c.Hkv, c.N, **i32),
-                len=torch.zeros(c.B, **i32))
-        d = self._spare
-        ps.ps_kv4_evict(c, d["cache"], self.w, d["w"], d["len"], keep, sink=sink, recent=recent,
-                        len=self.len, kpos=self.kpos, kpos_dst=d["kpos"],
+        if spare is None:
+            spare = self._spare     # empty once another layer has taken it
+            if not spare:
+                spare = dict(
+                    cache=ps.Kv4Cache.empty(c.B, c.Hkv, c.N, c.dh, c.kmul, c.vmul, c.device),
+                    w=torch.zeros_like(self.w), kpos=torch.zeros(c.B, c.Hkv, c.N, **i32),
+                    len=torch.zeros(c.B, **i32))
+        elif not spare:
+            raise ValueError("an eviction has taken this spare already")
+        ps.ps_kv4_evict(c, spare["cache"], self.w, spare["w"], spare["len"], keep, sink=sink,
+                        recent=recent, len=self.len, kpos=self.kpos, kpos_dst=spare["kpos"],
                         ws=self._workspace(ps.OP_KV4_EVICT, k=keep), stream=stream)
-        kpos = torch.zeros_like(d["kpos"]) if self.kpos is None else self.kpos
+        kpos = torch.zeros(c.B, c.Hkv, c.N, **i32) if self.kpos is None else self.kpos
+        # the one reference to the old buffers that a later eviction, this
+        # layer's or another's, may write through: whoever takes them empties it
         self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len)
-        self.cache, self.w, self.kpos, self.len = d["cache"], d["w"], d["kpos"], d["len"]
+        self.cache, self.w, self.kpos, self.len = (spare[k] for k in ("cache", "w", "kpos", "len"))
+        spare.clear()
         return self._spare

@@ -1,0 +1,136 @@
+"""Kv4Layer's own bookkeeping on the CPU: which buffers a layer owns, what its
+slots hold, how far it is filled.  The native calls are stood in for by the
+oracle on CPU tensors."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from drift_aware_kv_spherical_gb300 import kv4
+from drift_aware_kv_spherical_gb300 import polestar as ps
+
+B, N, HQ, HKV, DH = 2, 24, 4, 2, 64
+KMUL, VMUL = 0.25, 0.125
+
+
+class _Cache:
+    """A Kv4Cache over CPU tensors."""
+
+    def __init__(self, kcode, kscale, vcode, vscale, kmul=1.0, vmul=1.0):
+        self.buffers = (kcode, kscale, vcode, vscale)
+        self.B, self.Hkv, self.N, half = kcode.shape
+        self.dh, self.kmul, self.vmul, self.device = 2 * half, kmul, vmul, kcode.device
+
+    @classmethod
+    def empty(cls, B, Hkv, N, dh, kmul=1.0, vmul=1.0, device="cpu"):
+        mk = [torch.zeros(B, Hkv, N, dh // q, dtype=torch.uint8) for q in (2, 16, 2, 16)]
+        return cls(*mk, kmul=kmul, vmul=vmul)
+
+
+def _store(c, K, V, off=None, rows=None, cnt=None, stream=None):
+    R = K.shape[1]
+    for b in range(c.B):
+        n = R if cnt is None else min(int(cnt[b]), R)
+        for j in range(n):
+            r = j if rows is None else int(rows[b, j])
+            slot = r + (0 if off is None else int(off[b]))
+            if not (0 <= r < R and 0 <= slot < c.N):
+                continue
+            for X, S, code, scale in ((K, c.kmul, *c.buffers[:2]), (V, c.vmul, *c.buffers[2:])):
+                a, s = oracle.kv4_encode(X[b, r].float().numpy(), S)
+                code[b, :, slot], scale[b, :, slot] = torch.from_numpy(a), torch.from_numpy(s)
+
+
+def _evict(src, dst, w, w_dst, len_dst, keep, sink=0, recent=0, len=None, kpos=None,
+           kpos_dst=None, ws=None, stream=None):
+    if sink + recent > keep or keep > dst.N:
+        raise ps.PolestarError(ps.PS_ERR_ARG, "ps_kv4_evict")
+    assert not set(t.data_ptr() for t in src.buffers) & set(t.data_ptr() for t in dst.buffers)
+    for b in range(src.B):
+        n = int(len[b])
+        len_dst[b] = min(n, keep)
+        for h in range(src.Hkv):
+            at = torch.from_numpy(oracle.kv4_keep(w[b, h].numpy(), n, keep, sink, recent))
+            k = at.numel()
+            for x, y in zip(src.buffers, dst.buffers):
+                y[b, h, :k] = x[b, h, at]
+            w_dst[b, h, :k] = w[b, h, at]
+            kpos_dst[b, h, :k] = (at if kpos is None else kpos[b, h, at]).int()
+
+
+@pytest.fixture(autouse=True)
+def _native(monkeypatch):
+    monkeypatch.setattr(ps, "Kv4Cache", _Cache)
+    monkeypatch.setattr(ps, "ps_kv4_store", _store)
+    monkeypatch.setattr(ps, "ps_kv4_evict", _evict)
+    monkeypatch.setattr(ps, "ps_workspace_bytes", lambda op, **k: 0)
+
+
+def _layer():
+    return kv4.Kv4Layer(B, N, HQ, HKV, DH, KMUL, VMUL, device="cpu")
+
+
+def _rows(T, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(B, T, HKV, DH, generator=g).bfloat16(),
+            torch.randn(B, T, HKV, DH, generator=g).bfloat16())
+
+
+def _weights(layer, seed):
+    layer.w.copy_(torch.rand(layer.w.shape, generator=torch.Generator().manual_seed(seed)))
+
+
+def _snap(layer):
+    return [t.clone() for t in (*layer.cache.buffers, layer.w, layer.kpos, layer.len)]
+
+
+def _owned(layer):
+    ts = (*layer.cache.buffers, layer.w, layer.kpos, layer.len)
+    return {t.data_ptr() for t in ts}
+
+
+# ---- whose buffers they are
+@pytest.mark.parametrize("carry", [False, True])
+def test_layers_that_pass_one_spare_on_keep_their_own_rows(carry):
+    """Two rounds of evictions over three layers with one spare, given up between
+    the rounds or carried over: no layer's live buffers are another's, and every
+    layer ends as a layer that was evicted by itself."""
+    layers, alone = [_layer() for _ in range(3)], [_layer() for _ in range(3)]
+    for i, (a, b) in enumerate(zip(layers, alone)):
+        for x in (a, b):
+            x.append(*_rows(20, i))
+            _weights(x, i)
+    spare = None
+    for keep in (12, 7):
+        if not carry:
+            spare = None
+        for layer in layers:
+            others = [_snap(x) for x in layers if x is not layer and x.kpos is not None]
+            spare = layer.evict(keep, sink=1, recent=2, spare=spare)
+            after = [_snap(x) for x in layers if x is not layer and x.kpos is not None]
+            assert all(torch.equal(p, q) for x, y in zip(others, after) for p, q in zip(x, y))
+        for layer in alone:
+            layer.evict(keep, sink=1, recent=2)
+        live = [_owned(x) for x in layers]
+        assert all(not (live[i] & live[j]) for i in range(3) for j in range(i))
+        for a, b in zip(layers, alone):
+            assert a.len.tolist() == [keep] * B == b.len.tolist()
+            for x, y in zip(_snap(a)[:6], _snap(b)[:6]):
+                assert torch.equal(x[:, :, :keep], y[:, :, :keep])
+
+
+def test_a_spare_serves_one_eviction():
+    a, b = _layer(), _layer()
+    for x in (a, b):
+        x.append(*_rows(10, 1))
+        _weights(x, 1)
+    spare = a.evict(6)
+    b.evict(6, spare=spare)
+    with pytest.raises(ValueError):
+        a.evict(4, spare=spare)
+    own = a.evict(4)                 # makes buffers of its own again
+    with pytest.raises(ps.PolestarError):
+        a.evict(2, sink=3)           # a refused call changes nothing
+    assert own["cache"] is not a.cache and a.len.tolist() == [4, 4]
+    assert a.evict(2)["len"].tolist() == [4, 4]
+    assert not own                   # was a's own spare, and is its live cache now
