@@ -4,7 +4,8 @@ weight its slots have drawn.
 
 All arithmetic is in the ps_kv4_* calls (include/polestar.h); this class owns
 their buffers and passes them on.  Until the first eviction slot n holds position
-n; afterwards `kpos` says which, for every KV head.
+n; afterwards `kpos` says which, for every KV head.  The slots behind the kept
+ones are those of the positions that come next, and have drawn no weight.
 """
 
 import torch
@@ -21,6 +22,8 @@ class Kv4Layer:
         self.len = torch.zeros(B, dtype=torch.int32, device=device)
         self.w = torch.zeros(B, Hkv, N, dtype=torch.float32, device=device)
         self.kpos = None
+        self._shift = None      # [B]: position of a slot behind the kept ones, less the slot
+        self._slots = torch.arange(N, dtype=torch.int32, device=device)
         self._spare = None
         self._ws = {}
 
@@ -82,6 +85,13 @@ class Kv4Layer:
                     len=torch.zeros(c.B, **i32))
         elif not spare:
             raise ValueError("an eviction has taken this spare already")
+        # ps_kv4_evict leaves what lies behind the kept slots as it is, and the
+        # buffers served an older cache: the next positions, without weight
+        shift = (self.len - keep).clamp_(min=0)
+        if self._shift is not None:
+            shift += self._shift
+        spare["w"].zero_()
+        spare["kpos"].copy_((self._slots + shift[:, None])[:, None])
         ps.ps_kv4_evict(c, spare["cache"], self.w, spare["w"], spare["len"], keep, sink=sink,
                         recent=recent, len=self.len, kpos=self.kpos, kpos_dst=spare["kpos"],
                         ws=self._workspace(ps.OP_KV4_EVICT, k=keep), stream=stream)
@@ -90,5 +100,6 @@ class Kv4Layer:
         # layer's or another's, may write through: whoever takes them empties it
         self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len)
         self.cache, self.w, self.kpos, self.len = (spare[k] for k in ("cache", "w", "kpos", "len"))
+        self._shift = shift
         spare.clear()
         return self._spare

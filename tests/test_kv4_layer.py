@@ -134,3 +134,25 @@ def test_a_spare_serves_one_eviction():
     assert own["cache"] is not a.cache and a.len.tolist() == [4, 4]
     assert a.evict(2)["len"].tolist() == [4, 4]
     assert not own                   # was a's own spare, and is its live cache now
+
+
+# ---- what the slots hold
+def test_slots_behind_the_kept_ones_hold_nothing_of_an_older_cache():
+    """After every eviction they are the next positions' and have no weight."""
+    a = _layer()
+    a.append(*_rows(N, 2))
+    a.len.copy_(torch.tensor([N, N - 5]))
+    for keep in (15, 9, 4):
+        _weights(a, keep)
+        a.evict(keep, recent=1)
+        for b, total in enumerate((N, N - 5)):
+            assert torch.all(a.w[b, :, keep:] == 0)
+            want = torch.arange(total, total + N - keep, dtype=torch.int32).expand(HKV, -1)
+            assert torch.equal(a.kpos[b, :, keep:], want)
+            assert torch.all(a.kpos[b, :, keep - 1] == total - 1)   # the last one is kept
+    short = _layer()                 # fewer slots than are kept
+    short.append(*_rows(6, 3))
+    _weights(short, 3)
+    short.evict(10)
+    assert torch.equal(short.kpos, torch.arange(N, dtype=torch.int32).expand(B, HKV, N))
+    assert torch.all(short.w[:, :, 6:] == 0)
