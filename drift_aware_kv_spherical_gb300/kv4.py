@@ -41,9 +41,9 @@ class Kv4Layer:
         ps.ps_kv4_store(self.cache, K, V, off=off, rows=rows, cnt=cnt, stream=stream)
 
     def append(self, K, V):
-        """K and V of the next T tokens of every sequence, behind what is there."""
-        if self.kpos is not None:
-            raise ValueError("append positions are not tracked after an eviction")
+        """K and V of the next T tokens of every sequence, behind what is there:
+        slots len[b], len[b] + 1, ..., which hold the positions that come next
+        after an eviction too."""
         self.store(K, V, off=self.len)
         self.len += K.shape[1]
 

@@ -156,3 +156,40 @@ def test_slots_behind_the_kept_ones_hold_nothing_of_an_older_cache():
     short.evict(10)
     assert torch.equal(short.kpos, torch.arange(N, dtype=torch.int32).expand(B, HKV, N))
     assert torch.all(short.w[:, :, 6:] == 0)
+
+
+@pytest.mark.parametrize("cuts", [[(20, 8)], [(20, 8), (3, 9), (7, 5)]])
+def test_appending_goes_on_after_an_eviction(cuts):
+    """Append, evict, append, ...: every slot holds the row of the position that
+    kpos names, sequences of unequal length too, and new tokens compete for their
+    place in the next eviction by the weight they drew themselves."""
+    a = _layer()
+    K, V = _rows(48, 4)
+    code, scale = oracle.kv4_encode(K.float().numpy().transpose(0, 2, 1, 3), KMUL)
+    a.append(K[:, :2], V[:, :2])
+    a.len[1] = 0                     # the second sequence starts two tokens later
+    at, total = 2, np.array([2, 0])
+    for T, keep in cuts:
+        for _ in range(T):           # row `at` of sequence b is its position total[b]
+            a.append(K[:, at:at + 1], V[:, at:at + 1])
+            at += 1
+            total += 1
+        filled = a.len.clone()
+        _weights(a, keep)
+        for b in range(B):
+            a.w[b, :, int(filled[b]):] = 0
+        a.evict(keep, sink=1, recent=2)
+        assert a.len.tolist() == [min(int(n), keep) for n in filled]
+        for b in range(B):
+            n = int(a.len[b])
+            first = at - total[b]    # the row of its position 0
+            for h in range(HKV):
+                pos = a.kpos[b, h, :n].numpy()
+                assert np.all(np.diff(pos) > 0) and pos[-1] == total[b] - 1
+                assert np.array_equal(a.cache.buffers[0][b, h, :n], code[b, h, pos + first])
+                assert np.array_equal(a.cache.buffers[1][b, h, :n], scale[b, h, pos + first])
+    a.append(K[:, at:at + 4], V[:, at:at + 4])
+    for b in range(B):
+        n = int(a.len[b])
+        assert a.kpos[b, 0, n - 4:n].tolist() == list(range(total[b], total[b] + 4))
+        assert torch.all(a.w[b, :, n - 4:] == 0)
