@@ -8,9 +8,20 @@ n; afterwards `kpos` says which, for every KV head.  The slots behind the kept
 ones are those of the positions that come next, and have drawn no weight.
 """
 
+import contextlib
+
 import torch
 
 from . import polestar as ps
+
+
+def _on(stream, device):
+    """Torch's work on `stream` (a torch stream, a raw one, None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream, device)
+    return torch.cuda.stream(stream)
 
 
 class Kv4Layer:
@@ -36,15 +47,50 @@ class Kv4Layer:
         return self._ws[key]
 
     def store(self, K, V, off=None, rows=None, cnt=None, stream=None):
-        """Rows of K and V [B][R][Hkv][dh] into slots off[b] + r (see
-        ps.ps_kv4_store); `len` is the caller's to set."""
-        ps.ps_kv4_store(self.cache, K, V, off=off, rows=rows, cnt=cnt, stream=stream)
+        """Rows of K and V [B][R][Hkv][dh] as positions off[b] + r (see
+        ps.ps_kv4_store); `len` is the caller's to set.  Before the first eviction
+        a position is its slot.  After it every KV head takes the row into the slot
+        that holds the position, and skips a position that it has evicted."""
+        if self.kpos is None:
+            ps.ps_kv4_store(self.cache, K, V, off=off, rows=rows, cnt=cnt, stream=stream)
+            return
+        with _on(stream, self.cache.device):
+            self._store_kept(K, V, off, rows, cnt, stream)
+
+    def _store_kept(self, K, V, off, rows, cnt, stream):
+        c, (B, R) = self.cache, K.shape[:2]
+        if R == 0:
+            return
+        # listed[b][r]: row r is to be stored; R stands for no row
+        listed = torch.zeros(B, R + 1, dtype=torch.bool, device=c.device)
+        entry = torch.arange(R, dtype=torch.int32, device=c.device)
+        on = (entry < R).expand(B, R) if cnt is None else entry < cnt[:, None]
+        if rows is None:
+            listed[:, :R] = on
+        else:
+            on = on & (rows >= 0) & (rows < R)
+            listed.scatter_(1, torch.where(on, rows, R).long(), True)
+            listed[:, R] = False
+        row = self.kpos if off is None else self.kpos - off[:, None, None]
+        row = torch.where((row >= 0) & (row < R), row, R).long().view(B, -1)
+        hit = listed.gather(1, row)
+        # every head as a sequence of its own, its rows in the order of its slots
+        row = row.clamp_(max=R - 1).view(B, c.Hkv, c.N, 1).expand(-1, -1, -1, c.dh)
+        K, V = (X.transpose(1, 2).gather(2, row).view(B * c.Hkv, c.N, 1, c.dh) for X in (K, V))
+        heads = ps.Kv4Cache(*(t.view(B * c.Hkv, 1, c.N, -1) for t in c.buffers), c.kmul, c.vmul)
+        slots = torch.where(hit.view(-1, c.N), self._slots, -1)
+        ps.ps_kv4_store(heads, K, V, rows=slots, stream=stream)
+
+    def addresses(self):
+        """Where a captured store reads and writes: a graph of it holds while these
+        stay as they are."""
+        return tuple(t.data_ptr() for t in (*self.cache.buffers, self.kpos) if t is not None)
 
     def append(self, K, V):
         """K and V of the next T tokens of every sequence, behind what is there:
         slots len[b], len[b] + 1, ..., which hold the positions that come next
         after an eviction too."""
-        self.store(K, V, off=self.len)
+        ps.ps_kv4_store(self.cache, K, V, off=self.len)
         self.len += K.shape[1]
 
     def attend(self, Q, O, lse=None, *, scale=None, stream=None, **see):

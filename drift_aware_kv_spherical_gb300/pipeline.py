@@ -24,7 +24,8 @@ tokens commit only where the last layer's top-k position mask selects them
 
 With kv4=True each layer also keeps its cache in 4 bits (kv4.Kv4Layer): the
 rows a refresh rewrote are stored there behind it, and a block's attention
-reads that cache (`self.kv4[l].attend`).
+reads that cache (`self.kv4[l].attend`).  After an eviction (`self.kv4[l].evict`)
+a refresh stores the rows of the positions that each KV head still holds.
 
 scorer selects the drift signal: the proxy's fused KL (default), or one of
 the ablation signals (cosine dissimilarity, entropy) computed by
@@ -105,6 +106,7 @@ class Pipeline:
         self._flags = None
         self._gin = None
         self._graphs = {}
+        self._graph_kv4 = None
         self.undecided = torch.ones(B, P, dtype=torch.uint8, device=device)
         self.d_sum = torch.zeros(B, P, dtype=torch.float32, device=device)
         self.d_cnt = torch.zeros(B, P, dtype=torch.int32, device=device)
@@ -301,7 +303,7 @@ class Pipeline:
         captured on first use and replayed -- the same kernels in the same
         order as decode_step, without the host launching them one by one.
         The weights are captured by address and must not move between
-        steps."""
+        steps; an eviction from a 4-bit cache moves it, and drops the graphs."""
         main = stream if stream is not None else torch.cuda.current_stream(self.device)
         if self._gin is None:
             self._gin = dict(H=[h.clone() for h in Hs], Q=[q.clone() for q in Qs],
@@ -321,6 +323,10 @@ class Pipeline:
             if act & ps.SCHED_REINIT:
                 for dst, src in zip(g["u"], init_us):
                     dst.copy_(src, non_blocking=True)
+        kv4 = None if self.kv4 is None else [layer.addresses() for layer in self.kv4]
+        if kv4 != self._graph_kv4:
+            self._graphs = {}
+            self._graph_kv4 = kv4
         key = (act, self.t % 2)
         if key not in self._graphs:
             t0 = self.t

@@ -1,0 +1,109 @@
+"""Kv4Layer and the pipeline around an eviction, on the GPU: what a refresh, a
+captured step and further tokens do to a cut cache, and layers on streams of their
+own."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from drift_aware_kv_spherical_gb300 import polestar as ps
+from drift_aware_kv_spherical_gb300 import workloads as wl
+from drift_aware_kv_spherical_gb300.kv4 import Kv4Layer
+from drift_aware_kv_spherical_gb300.pipeline import Pipeline
+from tests._parity import np_
+
+pytestmark = pytest.mark.gpu
+
+W = wl.Workload("kv4_cut", 92, B=2, N=160, d=256, Hq=4, Hkv=2, dh=64, C=8, iters=3, k=2, P=16,
+                V=1024, dtype="bf16", planted=8, noise=1.0, drift_frac=0.1, drift_std=0.5,
+                blk_start=64, logit_std=2.0, wq_std=0.05)
+FIRST = ps.SCHED_REFRESH | ps.SCHED_FULL | ps.SCHED_REINIT
+
+
+@pytest.fixture(autouse=True)
+def _lib(lib):
+    yield lib
+    torch.cuda.synchronize()
+    ps.ps_check()
+
+
+def _holds_its_positions(layer, st, kmul, vmul):
+    """Every filled slot is the encoding of the bf16 cache's row at its position."""
+    n, kpos = layer.len.tolist(), np_(layer.kpos)
+    for i, (X, S) in enumerate(((st.Kc, kmul), (st.Vc, vmul))):
+        enc = oracle.kv4_encode(np_(X).transpose(0, 2, 1, 3), S)
+        for got, want in zip(layer.cache.buffers[2 * i:2 * i + 2], enc):
+            for b in range(W.B):
+                for h in range(W.Hkv):
+                    at = kpos[b, h, :n[b]]
+                    assert np.array_equal(np_(got)[b, h, :n[b]], want[b, h, at])
+
+
+def _cut(pipe, keep, seed):
+    layer = pipe.kv4[0]
+    layer.w.copy_(torch.rand(layer.w.shape, generator=torch.Generator().manual_seed(seed)))
+    layer.evict(keep, sink=2, recent=5)
+
+
+@pytest.mark.parametrize("graphs", [False, True])
+def test_refreshes_after_an_eviction(graphs):
+    """The kept slots follow the refreshed rows of their own positions, through
+    captured steps too, whose graphs from before an eviction are not replayed."""
+    L = wl.make_layer(W, 0, "cuda")
+    u, logits = wl.make_uniforms(W, 0, "cuda"), wl.make_logits(W, 0, "cuda")
+    pipe = Pipeline(W, layers=1, kv4=True, kmul=0.25, vmul=0.125)
+    H = L["H"]
+    for t in range(8):
+        H = H if t == 0 else wl.drift_rows(W, H, t)
+        Q = wl.make_queries(W, H, L["Wq"])
+        act = FIRST if t == 0 else ps.SCHED_REFRESH | (ps.SCHED_FULL if t == 5 else 0)
+        step = pipe.graph_step if graphs and t > 0 else pipe.decode_step
+        idle = None if pipe.kv4[0]._spare is None else \
+            [x.clone() for x in pipe.kv4[0]._spare["cache"].buffers]
+        step(act, [H], [Q], [L["Wk"]], [L["Wv"]], logits, [u])
+        if idle is not None:
+            now = pipe.kv4[0]._spare["cache"].buffers
+            assert all(torch.equal(x, y) for x, y in zip(idle, now)), t
+            _holds_its_positions(pipe.kv4[0], pipe.state[0], 0.25, 0.125)
+        if t in (2, 3, 6):
+            _cut(pipe, {2: 100, 3: 90, 6: 40}[t], t)
+
+
+def test_tokens_appended_to_a_cut_cache_are_attended():
+    """Append, evict, append: attention and weight over the cut cache with its
+    positions follow the oracle on the rows that are left."""
+    B, N, Hq, Hkv, dh = 2, 64, 4, 2, 64
+    g = torch.Generator().manual_seed(5)
+    K, V = (torch.randn(B, 80, Hkv, dh, generator=g).bfloat16().cuda() for _ in range(2))
+    kv = Kv4Layer(B, N, Hq, Hkv, dh, 0.25, 0.25)
+    kv.append(K[:, :50], V[:, :50])
+    Q = torch.randn(B, 3, Hq, dh, generator=g).bfloat16().cuda()
+    O, lse = torch.zeros_like(Q), torch.zeros(B, 3, Hq, device="cuda")
+    kv.attend(Q, O, lse)
+    kv.weigh(Q, lse)
+    kv.evict(30, sink=2, recent=4)
+    kv.append(K[:, 50:70], V[:, 50:70])
+    assert kv.len.tolist() == [50, 50]
+    kpos = np_(kv.kpos)[:, :, :50]
+    assert np.array_equal(kpos[:, :, 30:], np.broadcast_to(np.arange(50, 70), (B, Hkv, 20)))
+    full = [oracle.kv4_decode(*oracle.kv4_encode(np_(X).transpose(0, 2, 1, 3), 0.25), 0.25)
+            for X in (K, V)]
+    K64, V64 = (np.take_along_axis(X, kpos[..., None], 2) for X in full)
+    qpos = np.array([[69, 60, 55]] * B)
+    span = np.stack([np.zeros_like(qpos), qpos + 1], -1)
+    slope = np.array([0.5, 0.25, 0.125, 0.0625], np.float32)
+    see = dict(span=torch.from_numpy(span.astype(np.int32)).cuda(),
+               qpos=torch.from_numpy(qpos.astype(np.int32)).cuda(),
+               slope=torch.from_numpy(slope).cuda())
+    s = oracle.kv4_scores(Q.double().cpu().numpy(), K64, dh ** -0.5, span=span, kpos=kpos,
+                          qpos=qpos, slope=slope)
+    Oref, lref = oracle.kv4_attention(s, V64)
+    w0 = np_(kv.w)
+    kv.attend(Q, O, lse, **see)
+    kv.weigh(Q, lse, **see)
+    # bf16's half step, P's 11 bits; weights to 2^-14 (scores and lse in fp32)
+    assert np.all(np.abs(np_(O) - Oref) <= 2.0 ** -8 * np.abs(Oref) + 2.0 ** -10 * np.abs(V64).max())
+    assert np.allclose(np_(lse), lref, rtol=0, atol=1e-4)
+    drawn = np_(kv.w)[:, :, :50] - w0[:, :, :50]
+    assert np.all(w0[:, :, 30:] == 0) and np.all(np_(kv.w)[:, :, 50:] == 0)
+    assert np.allclose(drawn, oracle.kv4_weight(s, lref, Hkv), rtol=2.0 ** -14, atol=2.0 ** -20)

@@ -193,3 +193,54 @@ def test_appending_goes_on_after_an_eviction(cuts):
         n = int(a.len[b])
         assert a.kpos[b, 0, n - 4:n].tolist() == list(range(total[b], total[b] + 4))
         assert torch.all(a.w[b, :, n - 4:] == 0)
+
+
+@pytest.mark.parametrize("how", ["all", "cnt", "rows", "rows+cnt", "off"])
+def test_a_store_after_an_eviction_goes_to_the_slots_of_its_positions(how):
+    """Every head's slot takes the row of the position it holds; evicted positions,
+    unlisted rows and entries out of range leave everything as it was."""
+    a = _layer()
+    a.append(*_rows(20, 6))
+    _weights(a, 6)                   # other slots are kept for every head
+    a.evict(11, sink=1, recent=3)
+    before = [t.clone() for t in (*a.cache.buffers, a.kpos, a.w, a.len)]
+    R = 20
+    K, V = _rows(R, 7)
+    g = np.random.default_rng(8)
+    rows = np.full((B, R), -1)
+    rows[0, :9] = [3, 0, 19, 7, 12, -4, 20, 99, 5]
+    rows[1] = g.permutation(R)
+    cnt, off = np.array([8, 5]), np.array([2, -3])
+    opt = {}
+    if "rows" in how:
+        opt["rows"] = torch.from_numpy(rows.astype(np.int32))
+    if "cnt" in how:
+        opt["cnt"] = torch.from_numpy(cnt.astype(np.int32))
+    if how == "off":
+        opt["off"] = torch.from_numpy(off.astype(np.int32))
+    a.store(K, V, **opt)
+    enc = [oracle.kv4_encode(X.float().numpy().transpose(0, 2, 1, 3), S)
+           for X, S in ((K, KMUL), (V, VMUL))]
+    for b in range(B):
+        entries = range(R) if "rows" not in how else rows[b]
+        entries = list(entries)[:cnt[b]] if "cnt" in how else list(entries)
+        named = {int(r) + (int(off[b]) if how == "off" else 0): int(r)
+                 for r in entries if 0 <= r < R}
+        for h in range(HKV):
+            for n in range(N):
+                r = named.get(int(a.kpos[b, h, n]))
+                for i, x in enumerate(a.cache.buffers):
+                    want = before[i][b, h, n] if r is None else \
+                        torch.from_numpy(enc[i // 2][i % 2][b, h, r])
+                    assert torch.equal(x[b, h, n], want), (b, h, n, r)
+    assert all(torch.equal(x, y) for x, y in zip((a.kpos, a.w, a.len), before[4:]))
+
+
+def test_an_eviction_changes_what_a_captured_store_holds():
+    a = _layer()
+    a.append(*_rows(20, 9))
+    seen = {a.addresses()}
+    for keep in (12, 11):            # twice: the first buffers again, now with kpos
+        a.evict(keep)
+        assert a.addresses() not in seen
+        seen.add(a.addresses())
