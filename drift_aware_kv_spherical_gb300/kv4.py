@@ -38,12 +38,14 @@ class Kv4Layer:
         self._spare = None
         self._ws = {}
 
-    def _workspace(self, op, **sizes):
-        key = (op, *sorted(sizes.items()))
+    def _workspace(self, op, stream, **sizes):
+        """The scratch of a call on `stream`: its own, allocated there."""
+        key = (op, ps.raw_stream(stream, self.cache.device), *sorted(sizes.items()))
         if key not in self._ws:
             c = self.cache
-            self._ws[key] = ps.workspace(op, device=c.device, B=c.B, N=c.N, Hq=self.Hq, Hkv=c.Hkv,
-                                         dh=c.dh, **sizes)
+            with _on(stream, c.device):
+                self._ws[key] = ps.workspace(op, device=c.device, B=c.B, N=c.N, Hq=self.Hq,
+                                             Hkv=c.Hkv, dh=c.dh, **sizes)
         return self._ws[key]
 
     def store(self, K, V, off=None, rows=None, cnt=None, stream=None):
@@ -98,14 +100,14 @@ class Kv4Layer:
         qpos, slope, cap as in ps.ps_kv4_attn."""
         scale = self.cache.dh ** -0.5 if scale is None else scale
         ps.ps_kv4_attn(self.cache, Q, O, lse, scale=scale, len=self.len, kpos=self.kpos,
-                       ws=self._workspace(ps.OP_KV4_ATTN, P=Q.shape[1]), stream=stream, **see)
+                       ws=self._workspace(ps.OP_KV4_ATTN, stream, P=Q.shape[1]), stream=stream, **see)
 
     def weigh(self, Q, lse, *, scale=None, stream=None, **see):
         """Adds the weight that Q's rows put on every slot to `w`; lse as attend
         wrote it for the same arguments."""
         scale = self.cache.dh ** -0.5 if scale is None else scale
         ps.ps_kv4_weight(self.cache, Q, lse, self.w, self.w, scale=scale, len=self.len,
-                         kpos=self.kpos, ws=self._workspace(ps.OP_KV4_WEIGHT, P=Q.shape[1]),
+                         kpos=self.kpos, ws=self._workspace(ps.OP_KV4_WEIGHT, stream, P=Q.shape[1]),
                          stream=stream, **see)
 
     def evict(self, keep, sink=0, recent=0, spare=None, stream=None):
@@ -119,7 +121,12 @@ class Kv4Layer:
             for layer in layers:
                 spare = layer.evict(keep, spare=spare)
 
-        A spare serves one eviction, which empties it."""
+        A spare serves one eviction, which empties it.  Everything runs on
+        `stream`, behind what the spare's last owner enqueued on its own."""
+        with _on(stream, self.cache.device):
+            return self._evict(keep, sink, recent, spare, stream)
+
+    def _evict(self, keep, sink, recent, spare, stream):
         c = self.cache
         i32 = dict(dtype=torch.int32, device=c.device)
         if spare is None:
@@ -131,6 +138,9 @@ class Kv4Layer:
                     len=torch.zeros(c.B, **i32))
         elif not spare:
             raise ValueError("an eviction has taken this spare already")
+        here = torch.cuda.current_stream(c.device) if c.device.type == "cuda" else None
+        if spare.get("stream", here) != here and not torch.cuda.is_current_stream_capturing():
+            here.wait_stream(spare["stream"])   # (a capture begins behind everything)
         # ps_kv4_evict leaves what lies behind the kept slots as it is, and the
         # buffers served an older cache: the next positions, without weight
         shift = (self.len - keep).clamp_(min=0)
@@ -140,11 +150,15 @@ class Kv4Layer:
         spare["kpos"].copy_((self._slots + shift[:, None])[:, None])
         ps.ps_kv4_evict(c, spare["cache"], self.w, spare["w"], spare["len"], keep, sink=sink,
                         recent=recent, len=self.len, kpos=self.kpos, kpos_dst=spare["kpos"],
-                        ws=self._workspace(ps.OP_KV4_EVICT, k=keep), stream=stream)
+                        ws=self._workspace(ps.OP_KV4_EVICT, stream, k=keep), stream=stream)
         kpos = torch.zeros(c.B, c.Hkv, c.N, **i32) if self.kpos is None else self.kpos
         # the one reference to the old buffers that a later eviction, this
         # layer's or another's, may write through: whoever takes them empties it
-        self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len)
+        self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len, stream=here)
+        if here is not None:    # they may have been allocated on another stream, and may be freed
+            for t in (*c.buffers, self.w, kpos, self.len, self._shift):
+                if t is not None:
+                    t.record_stream(here)
         self.cache, self.w, self.kpos, self.len = (spare[k] for k in ("cache", "w", "kpos", "len"))
         self._shift = shift
         spare.clear()

@@ -432,6 +432,16 @@ def _kv4_stream(stream, c):
     return _stream(stream)
 
 
+def raw_stream(stream, device):
+    """`stream` (a torch stream, a raw one, None: the device's current one) as an
+    integer; 0 where the device is not a GPU."""
+    if stream is None and device.type != "cuda":
+        return 0
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
 def _plain(t, dtype, shape, null=False):
     """Pointer of a contiguous device tensor of this dtype and shape."""
     if t is None:

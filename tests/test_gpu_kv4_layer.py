@@ -107,3 +107,72 @@ def test_tokens_appended_to_a_cut_cache_are_attended():
     drawn = np_(kv.w)[:, :, :50] - w0[:, :, :50]
     assert np.all(w0[:, :, 30:] == 0) and np.all(np_(kv.w)[:, :, 50:] == 0)
     assert np.allclose(drawn, oracle.kv4_weight(s, lref, Hkv), rtol=2.0 ** -14, atol=2.0 ** -20)
+
+
+def _filled(B, N, Hq, Hkv, dh, T, seed):
+    g = torch.Generator().manual_seed(seed)
+    kv = Kv4Layer(B, N, Hq, Hkv, dh, 0.25, 0.25)
+    kv.append(*(torch.randn(B, T, Hkv, dh, generator=g).bfloat16().cuda() for _ in range(2)))
+    kv.w.copy_(torch.rand(B, Hkv, N, generator=g))
+    return kv
+
+
+def _state(kv):
+    return (*kv.cache.buffers, kv.w, kv.kpos, kv.len)
+
+
+def test_evictions_on_another_stream():
+    """With the current stream held up: everything an eviction does, the new
+    buffers' first values included, is on the stream that was given, and the next
+    owner of a spare waits for the last one."""
+    want = [_filled(2, 300, 4, 2, 64, 200, i) for i in range(2)]
+    got = [_filled(2, 300, 4, 2, 64, 200, i) for i in range(2)]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for keep in (120, 50):
+        for kv in want:
+            kv.evict(keep, sink=1, recent=3)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)           # about 0.1 s, on the current stream
+    got[0].evict(120, sink=1, recent=3, stream=s[0])
+    with torch.cuda.stream(s[0]):
+        torch.cuda._sleep(100_000_000)       # layer 0's old rows are not given up before this
+        spare = got[0].evict(50, sink=1, recent=3, stream=s[0].cuda_stream)
+    got[1].evict(120, sink=1, recent=3, spare=spare, stream=s[1])
+    got[1].evict(50, sink=1, recent=3, stream=s[1])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert a.len.tolist() == b.len.tolist() == [50, 50]
+        assert all(torch.equal(x[:, :, :50], y[:, :, :50])
+                   for x, y in zip(_state(a)[:6], _state(b)[:6]))
+        assert torch.equal(a.w, b.w) and torch.equal(a.kpos, b.kpos)
+
+
+def test_attention_on_two_streams_at_once(monkeypatch):
+    """A call's partial sums are its own: the same shape on two streams gives
+    what each gives alone."""
+    B, N, Hq, Hkv, dh = 1, 20000, 8, 2, 128
+    kv = _filled(B, N, Hq, Hkv, dh, N, 3)
+    g = torch.Generator().manual_seed(4)
+    Qs = [torch.randn(B, 1, Hq, dh, generator=g).bfloat16().cuda() for _ in range(2)]
+    want, outs = [], []
+    for Q in Qs:
+        O, lse = torch.zeros_like(Q), torch.zeros(B, 1, Hq, device="cuda")
+        kv.attend(Q, O, lse)
+        want.append((O, lse))
+    assert ps.ps_workspace_bytes(ps.OP_KV4_ATTN, B=B, N=N, Hq=Hq, Hkv=Hkv, dh=dh, P=1) > 0
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    used, call = {}, ps.ps_kv4_attn
+    monkeypatch.setattr(ps, "ps_kv4_attn", lambda *a, ws, stream, **k: (
+        used.setdefault(stream, ws.data_ptr()), call(*a, ws=ws, stream=stream, **k)))
+    for i in range(40):
+        for Q, s in zip(Qs, streams):
+            O, lse = torch.zeros_like(Q), torch.zeros(B, 1, Hq, device="cuda")
+            s.wait_stream(torch.cuda.current_stream())
+            kv.attend(Q, O, lse, stream=s)
+            outs.append((O, lse))
+    torch.cuda.synchronize()
+    for i, (O, lse) in enumerate(outs):
+        assert torch.equal(O, want[i % 2][0]) and torch.equal(lse, want[i % 2][1]), i
+    assert used[streams[0]] != used[streams[1]]
