@@ -9,6 +9,7 @@ ones are those of the positions that come next, and have drawn no weight.
 """
 
 import contextlib
+import functools
 
 import torch
 
@@ -22,6 +23,11 @@ def _on(stream, device):
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(stream, device)
     return torch.cuda.stream(stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _ws_bytes(op, **sizes):
+    return ps.ps_workspace_bytes(op, **sizes)
 
 
 class Kv4Layer:
@@ -39,13 +45,19 @@ class Kv4Layer:
         self._ws = {}
 
     def _workspace(self, op, stream, **sizes):
-        """The scratch of a call on `stream`: its own, allocated there."""
-        key = (op, ps.raw_stream(stream, self.cache.device), *sorted(sizes.items()))
+        """The scratch of a call on `stream`: its own, allocated there, at the next
+        power of two of bytes.  So calls of many lengths share a few buffers (at most
+        four times the largest call's bytes in all), and none that a captured graph
+        uses is ever given back."""
+        c = self.cache
+        n = _ws_bytes(op, B=c.B, N=c.N, Hq=self.Hq, Hkv=c.Hkv, dh=c.dh, **sizes)
+        if n == 0:
+            return None
+        key = (ps.raw_stream(stream, c.device), n.bit_length())
         if key not in self._ws:
-            c = self.cache
             with _on(stream, c.device):
-                self._ws[key] = ps.workspace(op, device=c.device, B=c.B, N=c.N, Hq=self.Hq,
-                                             Hkv=c.Hkv, dh=c.dh, **sizes)
+                self._ws[key] = torch.empty(1 << n.bit_length(), dtype=torch.uint8,
+                                            device=c.device)
         return self._ws[key]
 
     def store(self, K, V, off=None, rows=None, cnt=None, stream=None):

@@ -244,3 +244,24 @@ def test_an_eviction_changes_what_a_captured_store_holds():
         a.evict(keep)
         assert a.addresses() not in seen
         seen.add(a.addresses())
+
+
+# ---- how much it keeps
+def test_workspaces_of_many_lengths_share_a_few_buffers(monkeypatch):
+    """Prompts of every length up to 300 and evictions to many sizes keep no more
+    than four times the largest call's bytes (powers of two up to the next one);
+    every call has enough."""
+    need = lambda op, B, N, Hq, Hkv, dh, P=0, k=0: 1000 * (P + k)  # noqa: E731
+    kv4._ws_bytes.cache_clear()
+    monkeypatch.setattr(ps, "ps_workspace_bytes", need)
+    seen = []
+    for name in ("ps_kv4_attn", "ps_kv4_weight"):
+        monkeypatch.setattr(ps, name, lambda *a, ws, **k: seen.append(ws))
+    a = _layer()
+    for T in range(1, 301):
+        a.attend(torch.zeros(B, T, HQ, DH), None)
+        a.weigh(torch.zeros(B, T, HQ, DH), None)
+        assert all(ws.nbytes >= 1000 * T for ws in seen[-2:])
+    kept = {ws.data_ptr(): ws.nbytes for ws in seen}
+    assert sum(kept.values()) <= 4 * 300 * 1000
+    kv4._ws_bytes.cache_clear()
