@@ -39,6 +39,7 @@ class Kv4Layer:
         self.len = torch.zeros(B, dtype=torch.int32, device=device)
         self.w = torch.zeros(B, Hkv, N, dtype=torch.float32, device=device)
         self.kpos = None
+        self._note_len(0)
         self._shift = None      # [B]: position of a slot behind the kept ones, less the slot
         self._slots = torch.arange(N, dtype=torch.int32, device=device)
         self._spare = None
@@ -103,9 +104,39 @@ class Kv4Layer:
     def append(self, K, V):
         """K and V of the next T tokens of every sequence, behind what is there:
         slots len[b], len[b] + 1, ..., which hold the positions that come next
-        after an eviction too."""
+        after an eviction too.  Refused where some sequence has no room for them
+        (a captured call cannot know at its replays: past the capacity they store
+        nothing, and `len` must not be let grow that far)."""
+        T = K.shape[1]
+        if self._capturing():
+            self._len_seen = False      # from now on `len` changes at replays too
+        elif (top := self._filled()) + T > self.cache.N:
+            raise ValueError(f"no room for {T} more tokens: {top} of {self.cache.N} slots are filled")
         ps.ps_kv4_store(self.cache, K, V, off=self.len)
-        self.len += K.shape[1]
+        known = self._known()
+        self.len += T
+        if known:
+            self._note_len(self._top + T)
+
+    def _capturing(self):
+        return self.len.is_cuda and torch.cuda.is_current_stream_capturing()
+
+    # Slots of the fullest sequence (`_top`): known on the host from one append or
+    # eviction to the next, read back only after the caller has changed `len`.
+    def _note_len(self, top):
+        self._top, self._len_seen = top, (self.len, self.len._version)
+
+    def _known(self):
+        seen = self._len_seen
+        return bool(seen) and seen[0] is self.len and seen[1] == self.len._version
+
+    def _filled(self):
+        if not self._known():
+            top = max(self.len.tolist(), default=0)
+            if self._len_seen is False:
+                return top
+            self._note_len(top)
+        return self._top
 
     def attend(self, Q, O, lse=None, *, scale=None, stream=None, **see):
         """Attention of Q [B][T][Hq][dh] over the cache into O; `see`: span,
@@ -164,6 +195,9 @@ class Kv4Layer:
                         recent=recent, len=self.len, kpos=self.kpos, kpos_dst=spare["kpos"],
                         ws=self._workspace(ps.OP_KV4_EVICT, stream, k=keep), stream=stream)
         kpos = torch.zeros(c.B, c.Hkv, c.N, **i32) if self.kpos is None else self.kpos
+        if self._capturing():
+            self._len_seen = False
+        known = self._known()
         # the one reference to the old buffers that a later eviction, this
         # layer's or another's, may write through: whoever takes them empties it
         self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len, stream=here)
@@ -173,5 +207,7 @@ class Kv4Layer:
                     t.record_stream(here)
         self.cache, self.w, self.kpos, self.len = (spare[k] for k in ("cache", "w", "kpos", "len"))
         self._shift = shift
+        if known:
+            self._note_len(min(self._top, keep))
         spare.clear()
         return self._spare

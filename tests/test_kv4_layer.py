@@ -265,3 +265,48 @@ def test_workspaces_of_many_lengths_share_a_few_buffers(monkeypatch):
     kept = {ws.data_ptr(): ws.nbytes for ws in seen}
     assert sum(kept.values()) <= 4 * 300 * 1000
     kv4._ws_bytes.cache_clear()
+
+
+# ---- how far it is filled
+def test_appending_past_the_capacity_is_refused():
+    """A call that some sequence has no room for raises and changes nothing, however
+    `len` came to be what it is; one that fits exactly does not."""
+    def full(layer, T, why):
+        before = [t.clone() for t in (*layer.cache.buffers, layer.len)]
+        with pytest.raises(ValueError, match="no room"):
+            layer.append(*_rows(T, 1))
+        after = (*layer.cache.buffers, layer.len)
+        assert all(torch.equal(x, y) for x, y in zip(before, after)), why
+
+    a = _layer()
+    full(a, N + 1, "empty")
+    a.append(*_rows(N - 1, 2))
+    full(a, 2, "one slot left")
+    a.append(*_rows(1, 3))
+    full(a, 1, "filled by appends")
+    _weights(a, 1)
+    a.evict(10)
+    a.append(*_rows(N - 10, 4))
+    full(a, 1, "filled again after an eviction")
+    a.len[0] = 3                      # the other sequence is full still
+    full(a, 1, "changed in place")
+    a.len = torch.tensor([3, N - 2], dtype=torch.int32)
+    full(a, 3, "replaced")
+    a.append(*_rows(2, 5))
+    assert a.len.tolist() == [5, N]
+    a.evict(4)                        # of a len that was set by the caller
+    assert a.len.tolist() == [4, 4]
+    full(a, N - 3, "known from the eviction")
+    a.append(*_rows(N - 4, 6))
+    b = _layer()
+    b.len.fill_(N)
+    full(b, 1, "filled by the caller")
+
+
+def test_appending_reads_nothing_back(monkeypatch):
+    """A loop of appends and evictions never waits for the device to learn `len`."""
+    a = _layer()
+    monkeypatch.setattr(torch.Tensor, "tolist", None)
+    for _ in range(3):
+        a.append(*_rows(12, 1))
+        a.evict(12)
