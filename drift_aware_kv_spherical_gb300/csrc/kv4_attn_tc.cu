@@ -123,7 +123,7 @@ __device__ __forceinline__ void tc_slots(const Kv4AttnArgs& a, TcWork& w) {
     const int t0 = row_token(a, m0), t1 = row_token(a, min(m0 + 2 * kTile, a.M) - 1);
     int lo = INT32_MAX, hi = INT32_MIN;
     for (int t = t0 + (threadIdx.x & 31); t <= t1; t += 32) {
-      const int2 x = __ldg(reinterpret_cast<const int2*>(a.span) + (long)w.b * a.T + t);
+      const int2 x = row_span(a, (long)w.b * a.T + t);
       if (x.x < x.y) {
         lo = min(lo, x.x);
         hi = max(hi, x.y);

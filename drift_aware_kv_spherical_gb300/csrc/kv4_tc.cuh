@@ -24,6 +24,11 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The positions that token `tok` sees.  Two loads: `span` may start at any i32.
+__device__ __forceinline__ int2 row_span(const Kv4AttnArgs& a, long tok) {
+  return make_int2(__ldg(a.span + 2 * tok), __ldg(a.span + 2 * tok + 1));
+}
+
 // Codes and scales of one slot's row (K or V).
 template <int DH>
 struct RawRow {

@@ -297,7 +297,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
         span[k] = make_int2(0, INT32_MAX);
         const int m = r * kTile + lane + 32 * k, t = row_token(a, m);
         if (r < end && m < a.M && a.span != nullptr)
-          span[k] = __ldg(reinterpret_cast<const int2*>(a.span) + (long)b * a.T + t);
+          span[k] = row_span(a, (long)b * a.T + t);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
