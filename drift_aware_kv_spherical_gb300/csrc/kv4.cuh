@@ -85,6 +85,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// The smaller one, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -96,6 +102,18 @@ constexpr float kTanh0 = -0.33333286f, kTanh1 = 0.13323874f, kTanh2 = -0.0511326
 __device__ __forceinline__ float tanh_small(float y) {
   const float z = y * y;
   return fmaf(y, z * fmaf(z, fmaf(z, kTanh2, kTanh1), kTanh0), y);
+}
+// 1 - 2 / (e^2y + 1) of y2 = 2 log2(e) y: absolute error 2.5e-7, of a score that
+// times the cap.  Up to kCapAbs that is 1/30 of what P's 11 bits of bf16 queries
+// leave; under a larger cap it would be more than a small score itself.
+constexpr float kCapAbs = 64.f, kTwoLog2e = 2.f * kLog2e;
+__device__ __forceinline__ float tanh_abs(float y2) {
+  return fmaf(-2.f, rcp_approx(exp2_approx(y2) + 1.f), 1.f);
+}
+// Any y to 2^-20 of its tanh.
+__device__ __forceinline__ float tanh_any(float y) {
+  const float low = tanh_small(y), t = tanh_abs(y * kTwoLog2e);
+  return fabsf(y) <= kTanhTop ? low : t;
 }
 
 // D += A B, m16n8k16, f16 operands, fp32 accumulators.

@@ -308,18 +308,25 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-// Four scores capped to fp32's precision, for a whole warp.
-__device__ __forceinline__ void cap4(const Kv4AttnArgs& a, float* x) {
-  float y[4];
+// tanh of four scores / cap, for a whole warp: to fp32's precision, or (not PRECISE,
+// where P is rounded to 11 bits) to 2^-20, up to kCapAbs to 2.5e-7 of 1.
+template <bool PRECISE>
+__device__ __forceinline__ void cap4(const Kv4AttnArgs& a, float* y) {
+  if (!PRECISE && a.cap <= kCapAbs) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) y[c] = x[c] * a.inv_cap;
+    for (int c = 0; c < 4; ++c) y[c] = tanh_abs(y[c] * kTwoLog2e);
+    return;
+  }
   const float top = max3(fmaxf(fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
   if (__all_sync(0xffffffffu, top <= kTanhTop)) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = a.cap * tanh_small(y[c]);
+    for (int c = 0; c < 4; ++c) y[c] = tanh_small(y[c]);
+  } else if (PRECISE) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = tanhf(y[c]);
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = a.cap * tanhf(y[c]);
+    for (int c = 0; c < 4; ++c) y[c] = tanh_any(y[c]);
   }
 }
 
@@ -385,8 +392,8 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
 
   // O of rows 8 nb + 2 t + (c & 1), elements [g dh/8, (g+1) dh/8): element
   // 2 i + c / 2 in o[nb][i][c].  Scores are in log2 units: a raw product times
-  // fa (of 2 score / cap where scores are capped); `base` is subtracted, the
-  // maximum so far less kPShift.
+  // fa (of score / cap where scores are capped); `base` is subtracted, the maximum
+  // so far less kPShift.
   float o[NB][MT][4], fa[NB][2], base[NB][2], lrow[NB][2];
   const float cap2 = a.cap * kLog2e;
   const bool capped = a.cap > 0.f;
@@ -398,8 +405,8 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       for (int c = 0; c < 4; ++c) o[nb][i][c] = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      fa[nb][u] =
-          par[nb * 8 + 2 * t + u].f * (F32 ? 1.f : capped ? 2.f * kLog2e * a.inv_cap : kLog2e);
+      fa[nb][u] = fminf(
+          par[nb * 8 + 2 * t + u].f * (capped ? a.inv_cap : F32 ? 1.f : kLog2e), FLT_MAX);
       base[nb][u] = kNoMax;
       lrow[nb][u] = 0.f;
     }
@@ -449,18 +456,13 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       for (int nb = 0; nb < NB; ++nb) {
         // the four scores less sub
         auto scores = [&](const float* sub, float* x) {
-          if (F32) {
+          if (F32 || capped) {
             float y[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) y[c] = s[nb][c] * fa[nb][c & 1];
-            if (capped) cap4(a, y);
+            if (capped) cap4<F32>(a, y);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[c] = fmaf(y[c], kLog2e, -sub[c & 1]);
-          } else if (capped) {  // tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              x[c] = fmaf(-2.f * cap2, rcp_approx(exp2_approx(s[nb][c] * fa[nb][c & 1]) + 1.f),
-                          cap2 - sub[c & 1]);
+            for (int c = 0; c < 4; ++c) x[c] = fmaf(y[c], capped ? cap2 : kLog2e, -sub[c & 1]);
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) x[c] = fmaf(s[nb][c], fa[nb][c & 1], -sub[c & 1]);
@@ -758,10 +760,10 @@ __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)
     const float f0 = rp[0].f, l0 = -rp[0].lse, f1 = rp[1].f, l1 = -rp[1].lse;
     if (GEN && a.cap > 0.f) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = s[c] * (c & 1 ? f1 : f0);
-      cap4(a, x);
+      for (int c = 0; c < 4; ++c) x[c] = s[c] * (c & 1 ? f1 : f0) * a.inv_cap;
+      cap4<true>(a, x);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] += c & 1 ? l1 : l0;
+      for (int c = 0; c < 4; ++c) x[c] = fmaf(x[c], a.cap, c & 1 ? l1 : l0);
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] = fmaf(s[c], c & 1 ? f1 : f0, c & 1 ? l1 : l0);

@@ -248,7 +248,7 @@ __device__ __forceinline__ float stage_q(float scale, uint8_t* qs, int r) {
 // item: what is not read in every step would push the scores out of registers.
 struct TcRow {
   float f;                // score factor of a raw product
-  float slope2;           // distance bias in log2 units
+  float slope2;           // distance bias, in units of the cap or log2 units
   int lo, hi, qpos, len;  // positions seen; the row's own; the sequence's slots
 };
 template <class T>
@@ -272,7 +272,7 @@ __device__ __forceinline__ TcRow tc_row(const Kv4AttnArgs& a, bool in, int b, in
   row.len = min(max(a.len != nullptr ? __ldg(a.len + b) : a.Ncache, 0), a.Ncache);
   if (in) {
     const long tok = (long)b * a.T + t;
-    if (a.slope != nullptr) row.slope2 = a.slope[h] * kLog2e;
+    if (a.slope != nullptr) row.slope2 = a.slope[h] * (a.cap > 0.f ? a.inv_cap : kLog2e);
     row.hi = INT32_MAX;
     if (a.span != nullptr) {
       row.lo = a.span[2 * tok];
@@ -315,28 +315,36 @@ __device__ __forceinline__ float abs_max(const float* s) {
     t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
   return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
 }
-// Whether the series below does for scores up to `top` (log2 units).
-__device__ __forceinline__ bool cap_small(const Kv4AttnArgs& a, float top) {
-  return top * (a.inv_cap * kLn2) <= kTanhTop;
+// Score / cap of a raw product, from the row's score factor.
+__device__ __forceinline__ float cap_factor(const Kv4AttnArgs& a, float f) {
+  return fminf(f * a.inv_cap, FLT_MAX);
 }
-// tanh y = 1 - 2 / (e^2y + 1): absolute error about 1e-7.  x: raw product.
-__device__ __forceinline__ float cap_score(const Kv4AttnArgs& a, float x, float f) {
-  const float e = exp2_approx(x * (2.f * f * a.inv_cap * kLog2e));
-  return a.cap * kLog2e * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
-}
-// s[0..C): raw products, f their factor -> log2-unit scores.
+// s[0..C): raw products, f their factor -> tanh(score / cap), none above `top` (NaN
+// stays).  `small`: the series does for all of the warp's.  Caps past kCapAbs pay for
+// both formulas where it does not: 2048 rows x 32 heads on 4096 slots under a cap of
+// 30 with scores past it 275 us, 461 with both.
 template <int C>
-__device__ __forceinline__ void cap_scores(const Kv4AttnArgs& a, float* s, float f, bool small) {
+__device__ __forceinline__ void cap_tanh(const Kv4AttnArgs& a, float* s, float f, bool small,
+                                         float top) {
   if (small) {
-    cap_series<C>(s, f * kLog2e, a.inv_cap * kLn2);
+    tanh_series<C>(s, f);
+  } else if (a.cap <= kCapAbs) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = tanh_abs(s[c] * (f * kTwoLog2e));
   } else {
 #pragma unroll
-    for (int c = 0; c < C; ++c) s[c] = cap_score(a, s[c], f);
+    for (int c = 0; c < C; ++c) s[c] = min_nan(tanh_any(s[c] * f), top);
   }
 }
+// The same of one product, by the same formula.
+__device__ __forceinline__ float cap_tanh1(const Kv4AttnArgs& a, float x, float f, bool small) {
+  const float y = x * f, low = tanh_small(y), t = tanh_abs(y * kTwoLog2e);
+  return small || (a.cap > kCapAbs && fabsf(y) <= kTanhTop) ? low : t;
+}
 
-// s[0..C): raw products of C slots from n0 on -> log2-unit scores (GEN), and
-// -inf where the row does not see the slot.  pos: explicit positions, or null.
+// s[0..C): raw products of C slots from n0 on -> scores (GEN: in units of the cap if
+// there is one, else log2 units), and -inf where the row does not see the slot.
+// pos: explicit positions, or null.
 template <bool GEN, int C>
 __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, volatile int* rowp,
                                           int n0, TcSeen seen, const int* pos) {
@@ -345,7 +353,8 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, volati
     const float f2 = row.f * kLog2e;
     const uint64_t ff = f2_pack(f2, f2);
     if (a.cap > 0.f) {
-      cap_scores<C>(a, s, row.f, __all_sync(0xffffffffu, cap_small(a, abs_max<C>(s) * f2)));
+      const float fy = cap_factor(a, row.f);
+      cap_tanh<C>(a, s, fy, __all_sync(0xffffffffu, abs_max<C>(s) * fy <= kTanhTop), 1.f);
     } else {
 #pragma unroll
       for (int c = 0; c < C; c += 2)
@@ -395,7 +404,7 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
   // second pass (32 at a time then: their arithmetic needs registers too).
   constexpr bool LATE = FAST && GEN == kCap;
   constexpr int C = GEN && !LATE ? 32 : 64;
-  const float rf = LATE ? __int_as_float(row[0]) : 0.f;
+  const float fy = LATE ? cap_factor(a, __int_as_float(row[0])) : 0.f;
   float top = 0.f;
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains: one would wait on itself
 #pragma unroll 1
@@ -418,8 +427,8 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
   }
   if ((GEN || !FAST) && !LATE) tc::tmem_wait_st();
   const float m_raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-  const float m_tile = LATE ? cap_score(a, m_raw, rf) : m_raw * f2;
-  const bool small = LATE && __all_sync(0xffffffffu, cap_small(a, top * rf * kLog2e));
+  const bool small = LATE && __all_sync(0xffffffffu, top * fy <= kTanhTop);
+  const float m_tile = (LATE ? cap_tanh1(a, m_raw, fy, small) : m_raw) * f2;
   const bool grow = m_tile > m_used + kGrow;
   if (__any_sync(0xffffffffu, grow)) {
     const float m_new = grow ? m_tile : m_used;
@@ -453,7 +462,8 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
       tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
       tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
       tc::tmem_wait_ld();
-      if constexpr (LATE) cap_scores<64>(a, s, rf, small);
+      // (the two formulas meet within 2^-20 only: none may pass P's range)
+      if constexpr (LATE) cap_tanh<64>(a, s, fy, small, (m_used + kGrow) * (a.inv_cap * kLn2));
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         float x0, x1;
@@ -573,7 +583,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
           if (lane == 0) tc::mbar_arrive(q_full + g);
         }
         sm_put(rowp, row);
-        f2 = GEN ? 1.f : row.f * kLog2e;
+        f2 = !GEN ? row.f * kLog2e : a.cap > 0.f ? a.cap * kLog2e : 1.f;  // to log2 units
       }
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; act && j < nt; ++j, ++it) {

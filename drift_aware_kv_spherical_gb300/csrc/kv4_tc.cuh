@@ -68,18 +68,16 @@ __device__ __forceinline__ void fetch_q(const void* any, const __nv_bfloat16* sr
   }
 }
 
-// The same for C of them, two at a time: s[c] -> u tanh(y) / y, u = f s[c], y = k u.
+// tanh_small of C products, two at a time: s[c] -> tanh(f s[c]).
 template <int C>
-__device__ __forceinline__ void cap_series(float* s, float f, float k) {
-  const float k2 = k * k;
-  const float c0 = k2 * kTanh0, c1 = k2 * k2 * kTanh1, c2 = k2 * k2 * k2 * kTanh2;
-  const uint64_t ff = f2_pack(f, f), cc0 = f2_pack(c0, c0), cc1 = f2_pack(c1, c1),
-                 cc2 = f2_pack(c2, c2);
+__device__ __forceinline__ void tanh_series(float* s, float f) {
+  const uint64_t ff = f2_pack(f, f), c0 = f2_pack(kTanh0, kTanh0), c1 = f2_pack(kTanh1, kTanh1),
+                 c2 = f2_pack(kTanh2, kTanh2);
 #pragma unroll
   for (int c = 0; c < C; c += 2) {
-    const uint64_t u = f2_mul(f2_pack(s[c], s[c + 1]), ff), z = f2_mul(u, u);
-    const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, cc2, cc1), cc0));
-    f2_unpack(f2_fma(u, q, u), s[c], s[c + 1]);
+    const uint64_t y = f2_mul(f2_pack(s[c], s[c + 1]), ff), z = f2_mul(y, y);
+    const uint64_t q = f2_mul(z, f2_fma(z, f2_fma(z, c2, c1), c0));
+    f2_unpack(f2_fma(y, q, y), s[c], s[c + 1]);
   }
 }
 

@@ -40,7 +40,7 @@ constexpr int kMaxSplit = 8;  // CTAs of a portable cluster
 // What a step's rows bring, by column.
 struct StepRows {
   float nlse[kTile];     // -lse; -inf past the last row
-  float slope[kTile];    // distance bias
+  float slope[kTile];    // distance bias, in units of the cap if there is one
   int qpos[kTile];       // the row's position; as float from the block's first slot
                          // where slots are positions
   int lo[kTile];         // positions seen: lo + [0, num)
@@ -87,24 +87,27 @@ __device__ __forceinline__ void put_row_bf16(uint8_t* op, int r, const RawRow<DH
 template <bool GEN, bool MASKED>
 __device__ __forceinline__ float weigh32(const Kv4AttnArgs& a, float* s, const StepRows& rows,
                                          int c0, int pos, float dpos) {
-  const uint64_t f = f2_pack(a.scale, a.scale);
+  float f = a.scale;  // takes s to natural units
   if constexpr (GEN) {
     if (a.cap > 0.f) {
+      const float fy = fminf(fmaxf(a.scale * a.inv_cap, -FLT_MAX), FLT_MAX);
       float top = 0.f;
 #pragma unroll
       for (int c = 0; c < 32; c += 2) top = max3(top, fabsf(s[c]), fabsf(s[c + 1]));
-      if (__all_sync(0xffffffffu, top * fabsf(a.scale) * a.inv_cap <= kTanhTop)) {
-        cap_series<32>(s, a.scale, a.inv_cap);
+      if (__all_sync(0xffffffffu, top * fabsf(fy) <= kTanhTop)) {
+        tanh_series<32>(s, fy);
       } else {
-        const float k = a.scale * a.inv_cap;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = a.cap * tanhf(s[c] * k);
+        for (int c = 0; c < 32; ++c) s[c] = tanhf(s[c] * fy);
       }
-    } else {
+      f = a.cap;
+    } else if (a.slope != nullptr) {
+      const uint64_t ff = f2_pack(f, f);
+      f = 1.f;
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), f), s[c], s[c + 1]);
+      for (int c = 0; c < 32; c += 2) f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), ff), s[c], s[c + 1]);
     }
-    if (a.slope != nullptr) {
+    if (a.slope != nullptr) {  // in units of the cap, as s is
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         const float d = a.kpos != nullptr ? (float)(rows.qpos[c0 + c] - pos)
@@ -113,8 +116,8 @@ __device__ __forceinline__ float weigh32(const Kv4AttnArgs& a, float* s, const S
       }
     }
   }
-  // in natural units up to here: score and lse nearly cancel
-  const uint64_t e = f2_pack(kLog2e, kLog2e), one = f2_pack(1.f, 1.f);
+  // natural units up to the exponential: score and lse nearly cancel
+  const uint64_t e = f2_pack(kLog2e, kLog2e), ff = f2_pack(f, f);
   uint64_t sum[2] = {0, 0};
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
@@ -123,8 +126,7 @@ __device__ __forceinline__ float weigh32(const Kv4AttnArgs& a, float* s, const S
     for (int h = 0; h < 2; ++h) {
       const int k = c + 2 * h;
       float x0, x1;
-      f2_unpack(f2_mul(f2_fma(f2_pack(s[k], s[k + 1]), GEN ? one : f, h == 0 ? nl.x : nl.y), e),
-                x0, x1);
+      f2_unpack(f2_mul(f2_fma(f2_pack(s[k], s[k + 1]), ff, h == 0 ? nl.x : nl.y), e), x0, x1);
       if constexpr (MASKED) {
         if ((uint32_t)(pos - rows.lo[c0 + k]) >= rows.num[c0 + k]) x0 = -INFINITY;
         if ((uint32_t)(pos - rows.lo[c0 + k + 1]) >= rows.num[c0 + k + 1]) x1 = -INFINITY;
@@ -368,7 +370,7 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
         rows.lo[c] = seen.x;
         rows.num[c] = seen.x < seen.y ? (uint32_t)seen.y - (uint32_t)seen.x : 0u;
         if constexpr (GEN) {
-          rows.slope[c] = slope[k];
+          rows.slope[c] = a.cap > 0.f ? slope[k] * a.inv_cap : slope[k];
           rows.qpos[c] = by_pos ? qpos[k] : __float_as_int((float)(qpos[k] - n0));
         }
       }

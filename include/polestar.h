@@ -541,6 +541,8 @@ typedef struct {
  * O = 0 and lse = -inf.  Sums and statistics in fp32; the products' operands
  * are f16: the cache's values and bf16 queries exact, fp32 queries and their
  * weights in two f16 terms, the weights of bf16 queries rounded to 11 bits.
+ * The cap's tanh to 2^-20 of the score; of bf16 queries under a cap of up to 64
+ * to 2.5e-7 of the cap, where that is more (ps_kv4_weight: fp32's precision).
  * Deterministic.  Workspace: ps_workspace_bytes(PS_OP_KV4_ATTN, B, N = Ncache,
  * Hq, Hkv, dh, P = T). */
 ps_status ps_kv4_attn(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,

@@ -61,3 +61,66 @@ def test_arrays_that_start_at_any_element(T, with_pos):
     ps.ps_kv4_weight(c, Q, lse, w0, w, scale=0.125, **opt)
     ps.ps_kv4_weight(c, Q, lse2, _at_element_1(w0), w2, scale=0.125, **odd)
     assert torch.equal(w, w2)
+
+
+CAPS = [1e-30, 1e-3, 0.5, 50.0, 64.0, 65.0, 1e4, 1e6, 1e9, 1e20, 3e38]
+
+
+@pytest.mark.parametrize("T", [1, 12, 40, 150])
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("bias", [False, True])
+def test_caps_of_any_size(T, cap, bias):
+    """Scores within a dozen under caps from far below to far above them, rows near
+    a cap of 1e4 among them: every row's lse is as good as its own scores, its
+    weights sum to 1, and attention and weight agree.
+
+    A row's scores: products as _tol; score / cap, its tanh and the product with
+    the cap to 2^-20 of the score, or up to a cap of 64 to 2^-21.5 of that, which is
+    less where the score is past a third of it."""
+    B, Hq, Hkv, dh, N = 1, 4, 2, 64, 333
+    scale = dh ** -0.5
+    c, K, V = _cache(B, Hkv, N, dh, 17)
+    Q, _ = _query(B, T, Hq, dh, BF16, T, 1.5)
+    if T > 1:
+        Q[0, 1] *= 2000.0            # products up to some 1e4 beside rows of a dozen
+    Qn = Q.double().cpu().numpy()
+    opt = dict(cap=float(cap))
+    qpos = slope = None
+    if bias:
+        qpos, slope = np.full((B, T), N // 2), np.full(Hq, 2.0 ** -6, np.float32)
+        opt.update(qpos=_i32(qpos), slope=torch.from_numpy(slope).cuda())
+    s = oracle.kv4_scores(Qn, K, scale, cap=float(np.float32(cap)), qpos=qpos, slope=slope)
+    Oref, lref = oracle.kv4_attention(s, V)
+    O, lse = _attn(c, Q, scale=scale, **opt)
+    Kg = np.repeat(np.abs(K), Hq // Hkv, 1)
+    sabs = scale * np.einsum("bthd,bhnd->bthn", np.abs(Qn), Kg).max(-1)
+    top = np.minimum(sabs, cap)
+    capped = 2.0 ** -20 * top + (2.0 ** -21.5 * cap if cap <= 64 else 0.0)
+    # the cap's slope is at most 1: products' errors do not grow, and nothing passes it
+    ds = np.minimum(2.0 ** -22 * sabs * (dh / 16 + 2), 2 * top) + capped + 2.0 ** -21 * (top + 1)
+    if bias:
+        ds = ds + 2.0 ** -21 * (N / 2 * 2.0 ** -6 + top)
+    lim = 2 * ds + 2.0 ** -20 * (1 + np.abs(lref))
+    err = np.abs(np_(lse).astype(np.float64) - lref)
+    assert np.all(err <= lim), (err / lim).max()
+    # P to 2^-11, then bf16's half step
+    do = (np.expm1(2 * ds) + 2.0 ** -11 + 2.0 ** -19)[..., None] * np.abs(V).max()
+    assert np.all(np.abs(np_(O).astype(np.float64) - Oref) <= do + 2.0 ** -8 * np.abs(Oref))
+    # the weight from the attention's own lse: every row's sums to 1
+    row = np.expm1(3 * ds + lim + 2.0 ** -21 * np.abs(lref)) + 2.0 ** -18
+    w = np_(_weight(c, Q, lse, scale=scale, **opt)).astype(np.float64)
+    per = row.reshape(B, T, Hkv, Hq // Hkv).sum((1, 3))
+    assert np.all(np.abs(w.sum(-1) - T * Hq // Hkv) <= per), (w.sum(-1), per)
+
+
+@pytest.mark.parametrize("T", [1, 150])
+@pytest.mark.parametrize("cap", [0.0, 30.0, 1e6])
+def test_a_nan_query_stays_nan_under_a_cap(T, cap):
+    c, _, _ = _cache(1, 1, 256, 128, 5)
+    Q, _ = _query(1, T, 2, 128, BF16, 5, 4000.0 if cap == 1e6 else 30.0)
+    want, lw = _attn(c, Q, scale=1.0, cap=cap)
+    Q[0, 0, 1, 3] = float("nan")
+    O, lse = _attn(c, Q, scale=1.0, cap=cap)
+    assert torch.isnan(O[0, 0, 1]).all() and torch.isnan(lse[0, 0, 1])
+    assert torch.equal(O[0, 0, 0], want[0, 0, 0]) and torch.equal(O[0, 1:], want[0, 1:])
+    assert torch.isfinite(want.float()).all() and torch.isfinite(lw).all()
