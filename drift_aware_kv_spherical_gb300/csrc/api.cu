@@ -536,7 +536,7 @@ ps_status kv4_rows(ps_handle h, const ps_kv4_cache* c, const void* K, const void
   PS_REQUIRE((long)R * c->Hkv <= (1 << 30));
   PS_PTR(K); PS_PTR(V);
   Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)b_ld, (long)ld, off, rows, cnt,
-                c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul, 0};
+                c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul, {}};
   return launch_status(kv4_rows_run(a, load, static_cast<cudaStream_t>(stream)));
 }
 
@@ -560,7 +560,7 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
   a->Q = q->Q; a->dtype = q->dtype;
   a->B = c->B; a->T = q->T; a->Hq = q->Hq; a->Hkv = c->Hkv;
   a->G = q->Hq / c->Hkv; a->M = q->T * a->G;
-  a->g_recip = ((1ull << 40) + a->G - 1) / a->G;
+  a->by_g = row_quotient(a->G);
   a->Ncache = c->Ncache; a->dh = c->dh;
   a->q_bld = (long)q->q_bld; a->q_ld = (long)q->q_ld;
   a->len = q->len; a->span = q->span; a->kpos = q->kpos; a->qpos = q->qpos; a->slope = q->slope;

@@ -158,10 +158,9 @@ __device__ __forceinline__ float row_lse(float mx, float l) {
   return l == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx - kPShift) + log2f(l)) * kLn2;
 }
 
-// Row m of a KV head as (token, query head of the group): m = t G + j.  The
-// quotient by a 2^40 reciprocal, exact while m G < 2^40.
+// Row m of a KV head as (token, query head of the group): m = t G + j.
 __device__ __forceinline__ int row_token(const Kv4AttnArgs& a, int m) {
-  return (int)(((uint64_t)(uint32_t)m * a.g_recip) >> 40);
+  return (int)a.by_g.of((uint32_t)m);
 }
 
 // Four elements of a finished row: O = acc / l.

@@ -105,7 +105,7 @@ __device__ __forceinline__ bool block_at(const Kv4RowsArgs& a, BlockAt* o) {
   const int lane = threadIdx.x & 31;
   const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int b = blockIdx.y;
-  const uint32_t group = (uint32_t)(((uint64_t)warp * a.hkv_recip) >> 40);
+  const uint32_t group = a.by_hkv.of(warp);
   const int h = (int)(warp - group * a.Hkv);
   const int j = (int)group * kRows + lane / kBlocks;
   const int cnt = a.cnt != nullptr ? min(a.cnt[b], a.R) : a.R;
@@ -164,7 +164,7 @@ cudaError_t launch_rows(const Kv4RowsArgs& a, bool load, cudaStream_t s) {
 }  // namespace
 
 cudaError_t kv4_rows_run(Kv4RowsArgs a, bool load, cudaStream_t s) {
-  a.hkv_recip = ((1ull << 40) + a.Hkv - 1) / a.Hkv;
+  a.by_hkv = quotient(a.Hkv);
 #define PS_KV4_CASE(DH)                                              \
   if (a.dh == DH)                                                    \
     return a.dtype == PS_F32 ? launch_rows<float, DH>(a, load, s)    \

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "quotient.h"
 
 namespace ps {
 
@@ -107,14 +108,14 @@ struct Kv4RowsArgs {  // store: K, V -> cache; load: cache -> K, V
   const int32_t* off; const int32_t* rows; const int32_t* cnt;
   uint8_t* kcode; uint8_t* kscale; uint8_t* vcode; uint8_t* vscale;
   float kmul, vmul;
-  uint64_t hkv_recip;  // ceil(2^40 / Hkv), set by kv4_rows_run
+  Quotient by_hkv;  // set by kv4_rows_run
 };
 cudaError_t kv4_rows_run(Kv4RowsArgs a, bool load, cudaStream_t s);
 
 struct Kv4AttnArgs {
   const uint8_t* kcode; const uint8_t* kscale; const uint8_t* vcode; const uint8_t* vscale;
   const void* Q; int dtype; int B, T, Hq, Hkv, G, M, Ncache, dh; long q_bld, q_ld;
-  uint64_t g_recip;     // ceil(2^40 / G)
+  RowQuotient by_g;
   const int32_t* len; const int32_t* span; const int32_t* kpos; const int32_t* qpos;
   const float* slope;
   float scale;          // of a raw product: the caller's scale times kmul

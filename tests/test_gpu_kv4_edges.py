@@ -124,3 +124,48 @@ def test_a_nan_query_stays_nan_under_a_cap(T, cap):
     assert torch.isnan(O[0, 0, 1]).all() and torch.isnan(lse[0, 0, 1])
     assert torch.equal(O[0, 0, 0], want[0, 0, 0]) and torch.equal(O[0, 1:], want[0, 1:])
     assert torch.isfinite(want.float()).all() and torch.isfinite(lw).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_rows_than_2_to_the_24(dtype):
+    """The first and the last tokens of a call with more than 2^24 rows a KV head get
+    what a call of their own gets, output, lse and weight."""
+    T, tail, N, dh = (1 << 24) + 300, 400, 16, 64
+    c, _, _ = _cache(1, 1, N, dh, 21)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    Q = torch.randn(1, T, 1, dh, generator=g, device="cuda", dtype=dtype)
+    O, lse = _attn(c, Q, scale=0.125)
+    Ot, lt = _attn(c, Q[:, -tail:].contiguous(), scale=0.125)
+    assert torch.equal(O[:, -tail:], Ot) and torch.equal(lse[:, -tail:], lt)
+    Oh, lh = _attn(c, Q[:, :tail].contiguous(), scale=0.125)
+    assert torch.equal(O[:, :tail], Oh) and torch.equal(lse[:, :tail], lh)
+    if dtype == BF16:   # every row's weights sum to 1, each to 2^-18, added with compensation
+        w = _weight(c, Q, lse, scale=0.125)
+        assert abs(float(w.double().sum()) - T) <= T * 2.0 ** -18
+    # a span that the last rows alone have: what they weigh is theirs
+    span = torch.zeros(1, T, 2, dtype=torch.int32, device="cuda")
+    span[:, -tail:, 1] = N
+    wt = _weight(c, Q[:, -tail:].contiguous(), lt, scale=0.125)
+    ws = _weight(c, Q, lse, scale=0.125, span=span)
+    assert torch.allclose(ws, wt, rtol=2.0 ** -18, atol=0)
+
+
+@pytest.mark.parametrize("dh", [128, 256])
+def test_lists_of_more_entries_than_2_to_the_24(dh):
+    """Entries at both ends of a list of more than 2^24 warps' entries; all others
+    name no row."""
+    R, n = (1 << 24) * (512 // dh) + 40, 30
+    X = torch.randn(n, dh, device="cuda").to(BF16)
+    rows = torch.full((1, R), -1, dtype=torch.int32, device="cuda")
+    rows[0, :n // 2] = torch.arange(n // 2)
+    rows[0, -(n - n // 2):] = torch.arange(n // 2, n)
+    c, want = ps.Kv4Cache.empty(1, 1, n, dh), ps.Kv4Cache.empty(1, 1, n, dh)
+    ps.ps_kv4_store(want, X.view(1, n, 1, dh), -X.view(1, n, 1, dh))
+    lib = ps.Library.load()
+    Y = -X
+    st = lib.cdll.ps_kv4_store(lib.handle(0), c._c, X.data_ptr(), Y.data_ptr(), ps.PS_BF16, R, 0,
+                               dh, None, rows.data_ptr(), None,
+                               torch.cuda.current_stream().cuda_stream)
+    assert st == ps.PS_OK
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(c.buffers, want.buffers))
