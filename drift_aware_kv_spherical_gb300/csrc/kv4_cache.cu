@@ -61,8 +61,9 @@ __device__ __forceinline__ void dequant_block(uint2 c, uint32_t sc, float mul, f
 
 // The codes of x[0..15] / den.  fl(x / den) by Markstein's theorem: with y =
 // RN(1 / den), q = RN(x y) and the exact remainder r = x - q den, RN(q + r y) is
-// the correctly rounded quotient while nothing over- or underflows.  Three
-// instructions, no branch: bf16 rows hit E2M1's ties exactly so often (x and den
+// the correctly rounded quotient while nothing over- or underflows.  The remainder
+// is taken as q den - x, which is +0 and not -0 where it vanishes, and subtracted:
+// so a quotient of -0 stays -0.  Three instructions, no branch: bf16 rows hit E2M1's ties exactly so often (x and den
 // have few bits) that a fast path which detects them took its slow one in every
 // warp.
 __device__ __forceinline__ uint2 codes16(const float* x, float den, float y) {
@@ -70,7 +71,7 @@ __device__ __forceinline__ uint2 codes16(const float* x, float den, float y) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const float q0 = __fmul_rn(x[e], y);
-    q[e] = __fmaf_rn(__fmaf_rn(-q0, den, x[e]), y, q0);
+    q[e] = __fmaf_rn(-__fmaf_rn(q0, den, -x[e]), y, q0);
   }
   return make_uint2(e2m1x8(q), e2m1x8(q + 8));
 }
@@ -83,8 +84,10 @@ __device__ __forceinline__ uint32_t encode_block(const float* x, float S, float 
   const uint32_t sc = e4m3_code(__fdiv_rn(m, six_s));
   const float den = __fmul_rn(e4m3_value(sc), S);
   *codes = make_uint2(0u, 0u);
-  if (den >= 0x1p-90f && den <= 0x1p90f && m < INFINITY) {
-    *codes = codes16(x, den, __frcp_rn(den));
+  const float y = __frcp_rn(den);
+  // (a block scale that saturates leaves quotients far past 6, infinite ones too)
+  if (den >= 0x1p-90f && den <= 0x1p90f && m * y < 0x1p90f) {
+    *codes = codes16(x, den, y);
   } else if (den > 0.f) {  // out of the theorem's range
     float q[16];
 #pragma unroll

@@ -169,3 +169,35 @@ def test_lists_of_more_entries_than_2_to_the_24(dh):
     assert st == ps.PS_OK
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(c.buffers, want.buffers))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mul", [1.0, 0.7, 2.0 ** -60, 1e-37, 2.0 ** -126])
+def test_store_keeps_signs(dtype, mul):
+    """Zeros of both signs in live blocks, values whose code is a zero, quotients far
+    past 6 and past fp32 (a block scale that saturates under a small tensor scale),
+    NaN of both signs: bits as the oracle's divisions give them."""
+    R, dh = 64, 64
+    rng = np.random.default_rng(7)
+    X = (rng.standard_normal((1, R, 1, dh)) * np.float64(mul) * 100).astype(np.float32)
+    X[0, 0, 0, ::3], X[0, 0, 0, 1::3] = -0.0, 0.0
+    X[0, 1, 0, :] = -0.0                                  # a block of nothing else: scale 0
+    X[0, 2, 0, ::2] *= 1e-4                               # small ones, to zeros of their sign
+    X[0, 3, 0, ::2] = -0.0
+    for r, big in ((4, 1e30), (5, 3e38), (6, 1e38)):      # saturated scales
+        X[0, r, 0, :] = np.where(rng.random(dh) < 0.5, -1, 1) * big
+        X[0, r, 0, ::5] = -0.0
+        X[0, r, 0, 1::5] = -np.float32(mul)
+    X[0, 7, 0, ::4], X[0, 7, 0, 1::4] = np.float32("nan"), -np.float32("nan")
+    X[0, 8, 0, ::4], X[0, 8, 0, 1::4] = -np.inf, np.inf
+    X[0, 9, 0, :] = np.where(rng.random(dh) < 0.5, -1, 1) * np.float32(1e-45)
+    X[0, 9, 0, 0] = np.float32(mul) * 448 * 6
+    K = torch.from_numpy(X).to(dtype)
+    c = ps.Kv4Cache.empty(1, 1, R, dh, mul, mul)
+    ps.ps_kv4_store(c, K.cuda(), -K.cuda())
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        for x, at in ((K, 0), (-K, 2)):
+            code, scale = oracle.kv4_encode(x.float().numpy().transpose(0, 2, 1, 3), mul)
+            assert np.array_equal(np_(c.buffers[at + 1]), scale)
+            bad = np.argwhere(np_(c.buffers[at]) != code)
+            assert bad.size == 0, (bad[:8], dtype, mul)
