@@ -478,7 +478,8 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
-              if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)
+              if (n + sg + 8 * (c >> 1) >= len ||
+                  (a.span != nullptr && (pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)))
                 x[c] = -INFINITY;
             }
           }
@@ -776,7 +777,8 @@ __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)
     if (masked) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (n_sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp[c & 1].lo || pos[c >> 1] >= rp[c & 1].hi)
+        if (n_sg + 8 * (c >> 1) >= len ||
+            (a.span != nullptr && (pos[c >> 1] < rp[c & 1].lo || pos[c >> 1] >= rp[c & 1].hi)))
           x[c] = -INFINITY;
     }
 #pragma unroll

@@ -371,7 +371,7 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, float* s, volati
           s[c] = fmaf(-row.slope2, fabsf((float)(row.qpos - pos[c])), s[c]);
       }
     }
-    if (pos != nullptr) {
+    if (pos != nullptr && a.span != nullptr) {  // (without a span any position is seen)
 #pragma unroll
       for (int c = 0; c < C; ++c)
         if (n0 + c >= row.len || pos[c] < row.lo || pos[c] >= row.hi) s[c] = -INFINITY;

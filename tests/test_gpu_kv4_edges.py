@@ -201,3 +201,42 @@ def test_store_keeps_signs(dtype, mul):
             assert np.array_equal(np_(c.buffers[at + 1]), scale)
             bad = np.argwhere(np_(c.buffers[at]) != code)
             assert bad.size == 0, (bad[:8], dtype, mul)
+
+
+def _against_oracle(c, K, V, Q, dtype, scale, dist=0.0, **opt):
+    """Attention, and the weight from the oracle's lse, against the oracle; `dist`:
+    the largest distance bias."""
+    Qn = Q.double().cpu().numpy()
+    s = oracle.kv4_scores(Qn, K, scale, opt.get("len"), opt.get("span"), opt.get("kpos"),
+                          opt.get("qpos"), opt.get("slope"))
+    Oref, lref = oracle.kv4_attention(s, V)
+    dev = {k: torch.from_numpy(v).cuda() if k == "slope" else _i32(v) for k, v in opt.items()}
+    O, lse = _attn(c, Q, scale=scale, **dev)
+    ds, do = _tol(Qn, K, V, scale, 0, dtype)
+    ds, do = ds + 2.0 ** -22 * dist, do + np.expm1(2.0 ** -21 * dist) * np.abs(V).max()
+    _check_attn(O, lse, Oref, lref, ds, do, dtype)
+    lse32 = torch.from_numpy(lref).float().cuda()
+    w = np_(_weight(c, Q, lse32, scale=scale, **dev)).astype(np.float64)
+    ref = oracle.kv4_weight(s, lse32.double().cpu().numpy(), c.Hkv)
+    big = np.abs(lref[np.isfinite(lref)]).max(initial=0)
+    lim = ref * (np.expm1(2 * ds + 2.0 ** -21 * big) + 2.0 ** -18) + 1e-30
+    assert np.all(np.abs(w - ref) <= lim), np.max(np.abs(w - ref) / lim)
+
+
+@pytest.mark.parametrize("T", [1, 12, 40, 150])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bias", [False, True])
+def test_any_position_is_seen_without_a_span(T, dtype, bias):
+    """Positions below 0 and at the end of their type, as an offset or a mark may
+    leave them: without a span a row sees every filled slot."""
+    B, Hq, Hkv, dh, N = 2, 4, 2, 64, 203
+    rng = np.random.default_rng(T)
+    c, K, V = _cache(B, Hkv, N, dh, T)
+    Q, _ = _query(B, T, Hq, dh, dtype, T)
+    opt = dict(len=np.array([N, 150]))
+    if bias:
+        opt.update(kpos=rng.integers(-300, 300, (B, Hkv, N)), qpos=rng.integers(-9, 9, (B, T)),
+                   slope=np.array([0.25, 0.125, 0.0625, 0.03125], np.float32))
+    else:
+        opt["kpos"] = rng.choice([-(1 << 31), -1, 0, 7, (1 << 31) - 1], (B, Hkv, N))
+    _against_oracle(c, K, V, Q, dtype, 0.125, 310 * 0.25 if bias else 0.0, **opt)
