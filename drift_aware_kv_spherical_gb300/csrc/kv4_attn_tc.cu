@@ -293,11 +293,11 @@ struct TcRange {
 };
 __device__ __forceinline__ TcRange tc_range(const TcRow& row) {
   const bool live = row.lo < row.hi;
-  const int hi = min(row.hi, row.len);
+  const int lo = max(row.lo, 0), hi = max(min(row.hi, row.len), 0);  // of slots: 64 less is one too
   TcRange r;
-  r.any_lo = __reduce_min_sync(0xffffffffu, live ? row.lo : INT32_MAX);
+  r.any_lo = __reduce_min_sync(0xffffffffu, live ? lo : INT32_MAX);
   r.any_hi = __reduce_max_sync(0xffffffffu, live ? hi : INT32_MIN);
-  r.all_lo = __reduce_max_sync(0xffffffffu, live ? row.lo : INT32_MIN);
+  r.all_lo = __reduce_max_sync(0xffffffffu, live ? lo : INT32_MIN);
   r.all_hi = __reduce_min_sync(0xffffffffu, live ? hi : INT32_MAX) - 64;  // of the first of 64
   return r;
 }

@@ -128,8 +128,8 @@ __device__ __forceinline__ float weigh32(const Kv4AttnArgs& a, float* s, const S
       float x0, x1;
       f2_unpack(f2_mul(f2_fma(f2_pack(s[k], s[k + 1]), ff, h == 0 ? nl.x : nl.y), e), x0, x1);
       if constexpr (MASKED) {
-        if ((uint32_t)(pos - rows.lo[c0 + k]) >= rows.num[c0 + k]) x0 = -INFINITY;
-        if ((uint32_t)(pos - rows.lo[c0 + k + 1]) >= rows.num[c0 + k + 1]) x1 = -INFINITY;
+        if ((uint32_t)pos - (uint32_t)rows.lo[c0 + k] >= rows.num[c0 + k]) x0 = -INFINITY;
+        if ((uint32_t)pos - (uint32_t)rows.lo[c0 + k + 1] >= rows.num[c0 + k + 1]) x1 = -INFINITY;
       }
       sum[h] = f2_add(sum[h], f2_pack(exp2_approx(x0), exp2_approx(x1)));
     }

@@ -240,3 +240,32 @@ def test_any_position_is_seen_without_a_span(T, dtype, bias):
     else:
         opt["kpos"] = rng.choice([-(1 << 31), -1, 0, 7, (1 << 31) - 1], (B, Hkv, N))
     _against_oracle(c, K, V, Q, dtype, 0.125, 310 * 0.25 if bias else 0.0, **opt)
+
+
+LOWEST, HIGHEST = -(1 << 31), (1 << 31) - 1
+
+
+@pytest.mark.parametrize("T", [1, 12, 40, 150, 290])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", ["open", "mixed", "below"])
+@pytest.mark.parametrize("with_pos", [False, True])
+def test_spans_that_are_open_at_their_ends(T, dtype, kind, with_pos):
+    """Bounds at the ends of their type: no lower bound, no upper one, neither, spans
+    that end before the first slot, in one tile with ordinary ones."""
+    B, Hq, Hkv, dh, N = 2, 2, 1, 64, 330
+    rng = np.random.default_rng(T)
+    c, K, V = _cache(B, Hkv, N, dh, T)
+    Q, _ = _query(B, T, Hq, dh, dtype, T)
+    span = np.empty((B, T, 2), np.int64)
+    if kind == "open":
+        span[..., 0], span[..., 1] = LOWEST, HIGHEST
+    elif kind == "mixed":
+        span[..., 0] = rng.choice([LOWEST, LOWEST + 1, -3, 0, 100], (B, T))
+        span[..., 1] = rng.choice([HIGHEST, 64, 200, N, LOWEST + 5], (B, T))
+    else:
+        span[..., 0], span[..., 1] = LOWEST, rng.choice([LOWEST + 5, -64, -1, 0], (B, T))
+        span[:, ::3] = [50, 250]
+    opt = dict(len=np.array([N, 300]), span=span)
+    if with_pos:
+        opt["kpos"] = rng.integers(-100, 400, (B, Hkv, N))
+    _against_oracle(c, K, V, Q, dtype, 0.125, **opt)
