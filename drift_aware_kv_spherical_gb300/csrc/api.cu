@@ -100,6 +100,13 @@ constexpr int kMaxD = 8192;
 constexpr int kMaxDh = 256;
 
 bool kv4_dh_ok(int dh) { return dh == 64 || dh == 128 || dh == 256; }
+// Query rows of a call, without products that leave their type.
+bool kv4_rows_ok(int B, int T, int Hq) {
+  constexpr long most = INT32_MAX / 64;
+  return T <= most && Hq <= most && (long)T * Hq <= most && (long)T * Hq * B <= most;
+}
+// Slots a head: a few tiles more than these still are an int.
+constexpr int kMaxSlots = INT32_MAX - (1 << 16);
 
 }  // namespace
 
@@ -224,7 +231,9 @@ size_t ps_workspace_bytes(int op, int B, int N, int d, int C, int Hq, int Hkv,
     case PS_OP_COMMIT: return (P > 0 && V > 0) ? commit_ws(B, P, V) : 0;
     case PS_OP_KV4_ATTN:
     case PS_OP_KV4_WEIGHT:
-      if (N <= 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || P <= 0 || !kv4_dh_ok(dh)) return 0;
+      if (N <= 0 || N > kMaxSlots || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || P <= 0 ||
+          !kv4_dh_ok(dh) || !kv4_rows_ok(B, P, Hq))
+        return 0;
       return op == PS_OP_KV4_ATTN ? kv4_attn_ws(B, N, Hq, Hkv, dh, P)
                                   : kv4_weight_ws(B, N, Hq, Hkv, dh, P);
     case PS_OP_KV4_EVICT: return (Hkv > 0 && k > 0) ? kv4_evict_ws(B, Hkv, k) : 0;
@@ -511,7 +520,8 @@ namespace {
 
 // The shape, pointers and tensor scales of a cache.
 ps_status check_kv4(const ps_kv4_cache* c) {
-  PS_REQUIRE(c != nullptr && c->B >= 0 && c->Hkv >= 1 && c->Hkv <= 512 && c->Ncache >= 1 && kv4_dh_ok(c->dh));
+  PS_REQUIRE(c != nullptr && c->B >= 0 && c->Hkv >= 1 && c->Hkv <= 512 && c->Ncache >= 1 &&
+             c->Ncache <= kMaxSlots && kv4_dh_ok(c->dh));
   PS_REQUIRE(c->B <= 65535 && (long)c->B * c->Hkv <= 65535);
   PS_REQUIRE(std::isnormal(c->kmul) && c->kmul > 0.f && std::isnormal(c->vmul) && c->vmul > 0.f);
   if (c->B > 0) {
@@ -552,7 +562,7 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
   PS_REQUIRE((q->slope == nullptr) || (q->qpos != nullptr));
   *none = c->B == 0 || q->T == 0;
   if (*none) return PS_OK;
-  PS_REQUIRE((long)c->B * q->T * q->Hq <= INT32_MAX / 64 && q->Hq / c->Hkv <= 4096);
+  PS_REQUIRE(kv4_rows_ok(c->B, q->T, q->Hq) && q->Hq / c->Hkv <= 4096);
   PS_REQUIRE(ld_ok(q->q_ld, (long)q->Hq * c->dh, q->dtype) && ld_ok(q->q_bld, 0, q->dtype));
   PS_PTR(q->Q);
   *a = Kv4AttnArgs{};

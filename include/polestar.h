@@ -477,8 +477,8 @@ int ps_schedule_step(const ps_schedule_params* p, ps_schedule_state* s,
  * hold any bytes; calls never let it reach a result.
  *
  * Every call needs B >= 0 (0: no-op), 1 <= Hkv <= 512, B * Hkv <= 65535,
- * Ncache >= 1 and 16-byte aligned codes, scales, K, V, Q and O; the other
- * arrays may start at any element.
+ * 1 <= Ncache < 2^31 - 2^16 and 16-byte aligned codes, scales, K, V, Q and O;
+ * the other arrays may start at any element.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint8_t* kcode;

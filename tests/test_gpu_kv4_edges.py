@@ -269,3 +269,30 @@ def test_spans_that_are_open_at_their_ends(T, dtype, kind, with_pos):
     if with_pos:
         opt["kpos"] = rng.integers(-100, 400, (B, Hkv, N))
     _against_oracle(c, K, V, Q, dtype, 0.125, **opt)
+
+
+def test_sizes_that_leave_their_type_are_refused():
+    """Counts whose products leave an int, and slots up to the largest one: an
+    error, and nothing launched."""
+    lib = ps.Library.load()
+    c, _, _ = _cache(1, 1, 30, 64, 3)
+    Q, _ = _query(1, 3, 1, 64, BF16, 3)
+    O, lse = torch.full_like(Q, 7), torch.full((1, 3, 1), 7.0, device="cuda")
+    w = torch.full((1, 1, 30), 7.0, device="cuda")
+    ptr = [t.data_ptr() for t in c.buffers]
+
+    def calls(B, N, T, Hq):
+        cc = ps.Kv4Cache._pack.pack(*ptr, B, 1, N, 64, 1.0, 1.0)
+        q = ps._Q_PACK.pack(Q.data_ptr(), 0, 0, 0, 0, 0, 64 * Hq, 64 * Hq, ps.PS_BF16, T, Hq,
+                            1.0, 0.0)
+        return (lib.cdll.ps_kv4_attn(lib.handle(0), cc, q, O.data_ptr(), lse.data_ptr(), None, 0,
+                                     None),
+                lib.cdll.ps_kv4_weight(lib.handle(0), cc, q, lse.data_ptr(), None, w.data_ptr(),
+                                       None, 0, None))
+
+    most = (1 << 31) - 1
+    for sizes in ((1, most, 3, 1), (1, 30, most, 1), (1, 30, 1 << 30, 4), (1, 30, most, 4096),
+                  (1, 30, most, most)):
+        assert calls(*sizes) == (ps.PS_ERR_ARG, ps.PS_ERR_ARG), sizes
+    torch.cuda.synchronize()
+    assert bool((O == 7).all()) and bool((w == 7).all())
