@@ -544,6 +544,7 @@ ps_status kv4_rows(ps_handle h, const ps_kv4_cache* c, const void* K, const void
   if (c->B == 0 || R == 0) return PS_OK;
   PS_REQUIRE(ld_ok(ld, (long)c->Hkv * c->dh, dtype) && ld_ok(b_ld, 0, dtype));
   PS_REQUIRE((long)R * c->Hkv <= (1 << 30));
+  PS_REQUIRE(!load || c->B == 1 || b_ld > 0);  // sequences read back over one another
   PS_PTR(K); PS_PTR(V);
   Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)b_ld, (long)ld, off, rows, cnt,
                 c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul, {}};

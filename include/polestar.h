@@ -508,7 +508,8 @@ ps_status ps_kv4_store(ps_handle h, const ps_kv4_cache* c, const void* K,
                        const int32_t* cnt, void* stream);
 
 /* The reverse, with the same list: element = fl(code * s * S) rounded to
- * dtype (bf16: RNE) into K and V; rows not listed are untouched. */
+ * dtype (bf16: RNE) into K and V, whose rows must not overlap (b_ld > 0 for
+ * B > 1); rows not listed are untouched. */
 ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V,
                       int dtype, int R, int64_t b_ld, int64_t ld,
                       const int32_t* off, const int32_t* rows,

@@ -296,3 +296,16 @@ def test_sizes_that_leave_their_type_are_refused():
         assert calls(*sizes) == (ps.PS_ERR_ARG, ps.PS_ERR_ARG), sizes
     torch.cuda.synchronize()
     assert bool((O == 7).all()) and bool((w == 7).all())
+
+
+def test_reading_back_into_rows_shared_by_sequences_is_refused():
+    c, _, _ = _cache(2, 1, 30, 64, 4)
+    one = [torch.full((1, 30, 1, 64), 7.0, device="cuda") for _ in range(2)]
+    shared = [x.expand(2, -1, -1, -1) for x in one]
+    with pytest.raises(ps.PolestarError) as e:
+        ps.ps_kv4_load(c, *shared)
+    assert e.value.status == ps.PS_ERR_ARG and all(bool((x == 7).all()) for x in one)
+    ps.ps_kv4_store(c, *shared)      # as inputs they may
+    out = [torch.zeros(2, 30, 1, 64, device="cuda") for _ in range(2)]
+    ps.ps_kv4_load(c, *out)
+    assert all(torch.equal(x[0], x[1]) for x in out)
