@@ -576,9 +576,9 @@ ps_status kv4_query(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q, K
   a->q_bld = (long)q->q_bld; a->q_ld = (long)q->q_ld;
   a->len = q->len; a->span = q->span; a->kpos = q->kpos; a->qpos = q->qpos; a->slope = q->slope;
   a->scale = q->scale * c->kmul; a->vmul = c->vmul;
-  // within [1e-18, 1e18], past which a cap leaves nothing of fp32 scores, or all
-  // of those below 1e14: score / cap stays in range
-  a->cap = q->cap > 0.f ? std::fmin(std::fmax(q->cap, 1e-18f), 1e18f) : 0.f;
+  // within [1e-18, 1e30], past which a cap leaves nothing of fp32 scores, or all
+  // of those below 1e26: score / cap stays in range
+  a->cap = q->cap > 0.f ? std::fmin(std::fmax(q->cap, 1e-18f), 1e30f) : 0.f;
   a->inv_cap = q->cap > 0.f ? 1.f / a->cap : 0.f;
   a->num_sms = h->num_sms; a->status = h->status;
   return PS_OK;

@@ -44,7 +44,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kGrow = 4.f;      // log2 growth of a maximum before O is rescaled
 constexpr int kMaxCluster = 8;    // CTAs of a portable cluster
-constexpr float kNoMax = -1e30f;  // a maximum that every score outgrows
+constexpr float kNoMax = -FLT_MAX;  // a maximum that every score outgrows
 // Rows [m0, m0 + rows) of (b, hkv) into shared memory as B fragments
 // [row / 8][part][ks / 2][lane] (uint4: two steps' pairs), with their constants;
 // rows past M are zero and see nothing.  DH / 8 lanes a row, every load of a
@@ -487,7 +487,8 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
         float x[4];
         scores(base[nb], x);
         // The running maximum follows only when some row has outgrown it by
-        // 2^kGrow; until then P carries a factor up to that.
+        // 2^kGrow; until then P carries a factor up to that.  Scores from 2^24 on
+        // lie further apart than these shifts: rounded so that P stays in f16.
         if (__any_sync(0xffffffffu,
                        fmaxf(fmaxf(x[0], x[2]), fmaxf(x[1], x[3])) > kPShift + kGrow)) {
           const float zero[2] = {0.f, 0.f};
@@ -497,8 +498,8 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
             float mx = fmaxf(x[u], x[2 + u]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) - kPShift;
-            if (mx > base[nb][u] + kGrow) {
+            mx = __fsub_ru(fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)), kPShift);
+            if (mx > __fadd_rd(base[nb][u], kGrow)) {
               const float corr = exp2_approx(base[nb][u] - mx);
               base[nb][u] = mx;
               lrow[nb][u] *= corr;

@@ -43,6 +43,9 @@ constexpr int kRing = 4;            // items known and not yet taken by every wa
 constexpr int kTile = 128;          // slots a step; rows of a row tile
 constexpr float kGrow = 8.f;        // log2 growth of a maximum before O is rescaled
 constexpr float kTcShift = 4.f;     // log2 of the factor that P carries: P <= 2^12 in f16
+// A maximum from which on scores are rounded before it is subtracted from them: it
+// is rounded itself, and by 2^-24 of it P would leave f16.
+constexpr float kHuge = 0x1p22f;
 
 template <int DH>
 struct TcSmem {
@@ -399,7 +402,8 @@ template <int DH, int GEN, bool FAST>
 __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int* row, float f2,
                                              int n0, TcSeen seen0, TcSeen seen1, const int* ps,
                                              uint32_t s_col, uint32_t o_col, bool has_o,
-                                             uint64_t* p_full, float& m_used, float& l) {
+                                             uint64_t* p_full, float& m_used, float& l,
+                                             bool& huge) {
   // The maximum; scores that are more than raw products go back to TMEM for the
   // second pass (32 at a time then: their arithmetic needs registers too).
   constexpr bool LATE = FAST && GEN == kCap;
@@ -428,8 +432,8 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
   if ((GEN || !FAST) && !LATE) tc::tmem_wait_st();
   const float m_raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
   const bool small = LATE && __all_sync(0xffffffffu, top * fy <= kTanhTop);
-  const float m_tile = (LATE ? cap_tanh1(a, m_raw, fy, small) : m_raw) * f2;
-  const bool grow = m_tile > m_used + kGrow;
+  const float m_unit = LATE ? cap_tanh1(a, m_raw, fy, small) : m_raw, m_tile = m_unit * f2;
+  const bool grow = m_tile > __fadd_rd(m_used, kGrow);
   if (__any_sync(0xffffffffu, grow)) {
     const float m_new = grow ? m_tile : m_used;
     const float corr = grow ? exp2_approx(m_used - m_new) : 1.f;
@@ -446,10 +450,25 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
     }
     l *= corr;
     m_used = m_new;
+    huge = __any_sync(0xffffffffu, fabsf(m_used) >= kHuge && fabsf(m_used) < INFINITY);
   }
   // P over the scores: the first half lies on scores already read
-  const float base = m_used == -INFINITY ? 0.f : m_used - kTcShift;
-  const uint64_t ff = f2_pack(f2, f2), nb = f2_pack(-base, -base);
+  const float base = m_used == -INFINITY ? 0.f : __fsub_ru(m_used, kTcShift);
+  float fx = f2;
+  if (!LATE && huge) {
+    fx = 1.f;
+#pragma unroll 1
+    for (int k = 0; k < 128; k += 32) {
+      uint32_t s[32];
+      tc::tmem_ld32_nowait(s_col + k, s);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * f2);
+      tc::tmem_st32(s_col + k, s);
+    }
+    tc::tmem_wait_st();
+  }
+  const uint64_t ff = f2_pack(fx, fx), nb = f2_pack(-base, -base);
   uint64_t sum[2] = {0, 0};
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
@@ -462,8 +481,8 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
       tc::tmem_ld32_nowait(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
       tc::tmem_ld32_nowait(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
       tc::tmem_wait_ld();
-      // (the two formulas meet within 2^-20 only: none may pass P's range)
-      if constexpr (LATE) cap_tanh<64>(a, s, fy, small, (m_used + kGrow) * (a.inv_cap * kLn2));
+      // (the two formulas meet within 2^-20 only: none may pass the maximum)
+      if constexpr (LATE) cap_tanh<64>(a, s, fy, small, m_unit);
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         float x0, x1;
@@ -586,6 +605,7 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
         f2 = !GEN ? row.f * kLog2e : a.cap > 0.f ? a.cap * kLog2e : 1.f;  // to log2 units
       }
       float m_used = -INFINITY, l = 0.f;
+      bool huge = false;
       for (int j = 0; act && j < nt; ++j, ++it) {
         const int n0 = n_lo + j * kTile;
         ok = __all_sync(0xffffffffu, tc::mbar_wait(s_full + g, it & 1, a.status, abort_flag));
@@ -595,13 +615,13 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
         const TcSeen seen1 = by_pos ? kSome : tc_seen(range, n0 + 64);
         if (seen0 == kAll && seen1 == kAll)
           softmax_step<DH, GEN, true>(a, rowp, f2, n0, kAll, kAll, nullptr, s_col, o_col, j > 0,
-                                      p_full + 2 * g, m_used, l);
+                                      p_full + 2 * g, m_used, l, huge);
         else
           // a step's positions: written before its K, and not again until the
           // V of the third step after it has been asked for
           softmax_step<DH, GEN, false>(a, rowp, f2, n0, seen0, seen1,
                                        by_pos ? pos_ring + ((all + j) & 3) * kTile : nullptr,
-                                       s_col, o_col, j > 0, p_full + 2 * g, m_used, l);
+                                       s_col, o_col, j > 0, p_full + 2 * g, m_used, l, huge);
       }
       all += nt;
       const TcWork w = sm_get<TcWork>(keep);
@@ -921,7 +941,9 @@ cudaError_t launch_tc(const Kv4AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t kv4_attn_tc_launch(const Kv4AttnArgs& a, cudaStream_t s) {
-  const int gen = a.slope != nullptr || a.kpos != nullptr ? kAny : a.cap > 0.f ? kCap : kPlain;
+  // (kCap takes caps that keep scores below kHuge)
+  const int gen = a.slope != nullptr || a.kpos != nullptr || a.cap > kHuge / 4 ? kAny
+                  : a.cap > 0.f ? kCap : kPlain;
 #define PS_KV4_TC(DH, GEN) \
   if (a.dh == DH && gen == GEN) return launch_tc<DH, GEN>(a, s);
   PS_KV4_TC(64, kPlain)

@@ -309,3 +309,39 @@ def test_reading_back_into_rows_shared_by_sequences_is_refused():
     out = [torch.zeros(2, 30, 1, 64, device="cuda") for _ in range(2)]
     ps.ps_kv4_load(c, *out)
     assert all(torch.equal(x[0], x[1]) for x in out)
+
+
+@pytest.mark.parametrize("T", [1, 20, 40, 150])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("how", ["", "bias", "cap", "negative"])
+def test_scores_of_any_magnitude(T, dtype, how):
+    """Finite queries give finite rows however large the scores, up to where fp32
+    scores lie 2^70 apart: each row a mean of the values it sees, the value itself
+    where one score is clear of the others by more than the products' rounding."""
+    B, H, N, dh, scale = 1, 2, 700, 64, 0.125
+    c, K, V = _cache(B, H, N, dh, 31)
+    for mag in (1e5, 1e6, 1e7, 1e8, 1e9, 1e12, 1e30):
+        Q, _ = _query(B, T, H, dh, dtype, 31)
+        Q = Q * mag
+        opt = {}
+        if how == "bias":
+            opt = dict(qpos=_i32(np.full((B, T), N // 2)), slope=torch.full((H,), 2.0 ** -7,
+                                                                          device="cuda"))
+        elif how == "cap":
+            opt = dict(cap=mag)
+        O, lse = _attn(c, Q, scale=-scale if how == "negative" else scale, **opt)
+        Qn = Q.double().cpu().numpy()
+        s = oracle.kv4_scores(Qn, K, -scale if how == "negative" else scale,
+                              cap=float(np.float32(mag)) if how == "cap" else 0.0)
+        sabs = scale * np.einsum("bthd,bhnd->bthn", np.abs(Qn), np.abs(K)).max(-1)
+        top = np.sort(s, -1)[..., -2:]
+        assert torch.isfinite(O.float()).all() and torch.isfinite(lse).all(), mag
+        # a score to 2^-19 of the sum of its terms' sizes, twice; 60: e^-60 and a bias
+        clear = top[..., 1] - top[..., 0] > 2.0 ** -17 * sabs + 60
+        On = np_(O).astype(np.float64)
+        assert np.abs(On).max() <= np.abs(V).max() * (1 + 2.0 ** -7)
+        at = s.argmax(-1)                                    # [B][T][H]
+        want = np.stack([[V[b, np.arange(H), at[b, t]] for t in range(T)] for b in range(B)])
+        assert np.all(np.abs(On - want)[clear] <= 2.0 ** -8 * np.abs(want)[clear] + 1e-6), mag
+        err = np.abs(np_(lse).astype(np.float64) - top[..., 1])
+        assert np.all(err <= 2.0 ** -18 * sabs + 8 + N * 2.0 ** -8), (mag, err.max())
