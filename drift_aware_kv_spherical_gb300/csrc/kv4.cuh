@@ -133,7 +133,7 @@ struct alignas(16) RowPar {
   float lse;     // k_kv4_weight; +inf past the last row
   float slope;   // distance bias
   int qpos;
-  int lo, hi;    // visible positions
+  int lo, last;  // visible positions, both ends included; lo > last: none
 };
 
 __device__ __forceinline__ int kv4_len(const Kv4AttnArgs& a, int b) {

@@ -57,7 +57,7 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
   for (int r = threadIdx.x / LN; r < rows; r += step) {
     const int m = m0 + r;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    RowPar p{0.f, INFINITY, 0.f, 0, 0, 0};
+    RowPar p{0.f, INFINITY, 0.f, 0, INT32_MAX, INT32_MIN};
     if (m < a.M) {
       const int t = row_token(a, m), h = hkv * a.G + (m - t * a.G);
       const long tok = (long)b * a.T + t;
@@ -69,8 +69,12 @@ __device__ __forceinline__ void stage_rows(const Kv4AttnArgs& a, int b, int hkv,
         load16(static_cast<const __nv_bfloat16*>(a.Q) + at, x);
       }
       p.slope = a.slope != nullptr ? a.slope[h] : 0.f;
-      p.lo = a.span != nullptr ? a.span[2 * tok] : 0;
-      p.hi = a.span != nullptr ? a.span[2 * tok + 1] : INT32_MAX;
+      const int lo = a.span != nullptr ? a.span[2 * tok] : INT32_MIN;
+      const int hi = a.span != nullptr ? a.span[2 * tok + 1] : INT32_MAX;
+      if (a.span == nullptr || lo < hi) {
+        p.lo = lo;
+        p.last = a.span != nullptr ? hi - 1 : INT32_MAX;
+      }
       p.qpos = a.qpos != nullptr ? a.qpos[tok] : 0;
       p.lse = a.lse_in != nullptr ? a.lse_in[tok * a.Hq + h] : -INFINITY;
     }
@@ -361,8 +365,9 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   if (kpos != nullptr) {
     if (a.span != nullptr) all_hi = -1;
   } else if (a.span != nullptr) {  // slots are positions: skip what no row sees
-    const int lo = lane < rows ? par[lane].lo : 0, hi = lane < rows ? par[lane].hi : 0;
-    const bool in = lo < hi, row = lane < rows;
+    const bool row = lane < rows;
+    const int lo = row ? par[lane].lo : 0, hi = row ? par[lane].last + 1 : 0;
+    const bool in = lo < hi;
     n_lo = max(0, __reduce_min_sync(0xffffffffu, in ? lo : INT32_MAX));
     n_hi = min(len, __reduce_max_sync(0xffffffffu, in ? hi : INT32_MIN));
     all_lo = __reduce_max_sync(0xffffffffu, row ? lo : INT32_MIN);
@@ -478,8 +483,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const RowPar& rp = par[nb * 8 + 2 * t + (c & 1)];
-              if (n + sg + 8 * (c >> 1) >= len ||
-                  (a.span != nullptr && (pos[c >> 1] < rp.lo || pos[c >> 1] >= rp.hi)))
+              if (n + sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp.lo || pos[c >> 1] > rp.last)
                 x[c] = -INFINITY;
             }
           }
@@ -729,7 +733,7 @@ struct SeenRange {
 __device__ __forceinline__ SeenRange seen_range(const RowPar* par, int rows, int len) {
   int lo = INT32_MAX, hi = INT32_MIN, lo_all = INT32_MIN, hi_all = INT32_MAX;
   for (int r = threadIdx.x & 31; r < rows; r += 32) {
-    const int x = par[r].lo, y = par[r].hi;
+    const int x = par[r].lo, y = par[r].last + 1;
     if (x < y) {
       lo = min(lo, x);
       hi = max(hi, y);
@@ -778,8 +782,7 @@ __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)
     if (masked) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (n_sg + 8 * (c >> 1) >= len ||
-            (a.span != nullptr && (pos[c >> 1] < rp[c & 1].lo || pos[c >> 1] >= rp[c & 1].hi)))
+        if (n_sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp[c & 1].lo || pos[c >> 1] > rp[c & 1].last)
           x[c] = -INFINITY;
     }
 #pragma unroll
