@@ -312,29 +312,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-// tanh of four scores / cap, for a whole warp: to fp32's precision, or (not PRECISE,
-// where P is rounded to 11 bits) to 2^-20, up to kCapAbs to 2.5e-7 of 1.
-template <bool PRECISE>
-__device__ __forceinline__ void cap4(const Kv4AttnArgs& a, float* y) {
-  if (!PRECISE && a.cap <= kCapAbs) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = tanh_abs(y[c] * kTwoLog2e);
-    return;
-  }
+// tanh of four scores / cap to fp32's precision, for a whole warp.
+__device__ __forceinline__ void tanh4(float* y) {
   const float top = max3(fmaxf(fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
   if (__all_sync(0xffffffffu, top <= kTanhTop)) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) y[c] = tanh_small(y[c]);
-  } else if (PRECISE) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = tanhf(y[c]);
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = tanh_any(y[c]);
+    for (int c = 0; c < 4; ++c) y[c] = tanhf(y[c]);
   }
 }
 
-// GEN: a distance bias or explicit positions.
+// GEN: a distance bias, explicit positions or, of bf16 queries, a cap past kCapAbs
+// (its formula in every instance made 8 tokens on 64 K slots under a cap 53.5 us for
+// 51.9).
 template <int DH, int NB, bool F32, bool GEN>
 __global__ void __launch_bounds__(kThreads, DH <= 128 && NB == 1 && !F32 ? 5 : 1)
 k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
@@ -397,8 +389,8 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
 
   // O of rows 8 nb + 2 t + (c & 1), elements [g dh/8, (g+1) dh/8): element
   // 2 i + c / 2 in o[nb][i][c].  Scores are in log2 units: a raw product times
-  // fa (of score / cap where scores are capped); `base` is subtracted, the maximum
-  // so far less kPShift.
+  // fa (of score / cap where scores are capped, for bf16 queries 2 log2(e) times
+  // that); `base` is subtracted, the maximum so far less kPShift.
   float o[NB][MT][4], fa[NB][2], base[NB][2], lrow[NB][2];
   const float cap2 = a.cap * kLog2e;
   const bool capped = a.cap > 0.f;
@@ -410,8 +402,9 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       for (int c = 0; c < 4; ++c) o[nb][i][c] = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      fa[nb][u] = fminf(
-          par[nb * 8 + 2 * t + u].f * (capped ? a.inv_cap : F32 ? 1.f : kLog2e), FLT_MAX);
+      const float f = par[nb * 8 + 2 * t + u].f;
+      fa[nb][u] = capped ? fminf(f * (F32 ? a.inv_cap : a.inv_cap * kTwoLog2e), FLT_MAX)
+                         : f * (F32 ? 1.f : kLog2e);
       base[nb][u] = kNoMax;
       lrow[nb][u] = 0.f;
     }
@@ -461,13 +454,23 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
       for (int nb = 0; nb < NB; ++nb) {
         // the four scores less sub
         auto scores = [&](const float* sub, float* x) {
-          if (F32 || capped) {
+          if (F32) {
             float y[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) y[c] = s[nb][c] * fa[nb][c & 1];
-            if (capped) cap4<F32>(a, y);
+            if (capped) tanh4(y);
 #pragma unroll
             for (int c = 0; c < 4; ++c) x[c] = fmaf(y[c], capped ? cap2 : kLog2e, -sub[c & 1]);
+          } else if (GEN && a.cap > kCapAbs) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              x[c] = fmaf(tanh_any(s[nb][c] * fa[nb][c & 1] * (1.f / kTwoLog2e)), cap2,
+                          -sub[c & 1]);
+          } else if (capped) {  // tanh_abs, times the cap in its last step
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              x[c] = fmaf(-2.f * cap2, rcp_approx(exp2_approx(s[nb][c] * fa[nb][c & 1]) + 1.f),
+                          cap2 - sub[c & 1]);
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) x[c] = fmaf(s[nb][c], fa[nb][c & 1], -sub[c & 1]);
@@ -767,7 +770,7 @@ __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)
     if (GEN && a.cap > 0.f) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] = s[c] * (c & 1 ? f1 : f0) * a.inv_cap;
-      cap4<true>(a, x);
+      tanh4(x);
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] = fmaf(x[c], a.cap, c & 1 ? l1 : l0);
     } else {
@@ -1054,7 +1057,7 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
     if (e != cudaSuccess || a.nsplit == 1) return e;
     return a.dh == 64 ? launch_combine<64, false>(a, s) : launch_combine<128, false>(a, s);
   }
-  const bool gen = a.slope != nullptr || a.kpos != nullptr;
+  const bool gen = a.slope != nullptr || a.kpos != nullptr || a.cap > kCapAbs;
 #define PS_KV4_CASE(DH, NB)                                           \
   if (a.dh == DH && p.nb == NB) {                                     \
     if (f32) return launch_attn<DH, NB, true, true>(a, s);            \
