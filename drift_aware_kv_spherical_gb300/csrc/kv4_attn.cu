@@ -324,12 +324,15 @@ __device__ __forceinline__ void tanh4(float* y) {
   }
 }
 
-// GEN: a distance bias, explicit positions or, of bf16 queries, a cap past kCapAbs
-// (its formula in every instance made 8 tokens on 64 K slots under a cap 53.5 us for
-// 51.9).
-template <int DH, int NB, bool F32, bool GEN>
+// What an instance takes: no bias nor explicit positions; those too; and, of bf16
+// queries, caps past kCapAbs (whose formula in every instance made 8 tokens on 64 K
+// slots under a cap 53.5 us for 51.9, with positions on 16 K slots 28.7 for 26.7).
+enum RowKind { kPlainRows, kAnyRows, kLargeCap };
+
+template <int DH, int NB, bool F32, RowKind KIND>
 __global__ void __launch_bounds__(kThreads, DH <= 128 && NB == 1 && !F32 ? 5 : 1)
 k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
+  constexpr bool GEN = KIND != kPlainRows;
   constexpr int KS = DH / 16, MT = DH / 16, P = F32 ? 2 : 1;  // QK steps; O tiles of 16 elements
   constexpr int kRows = 8 * NB;
   pdl_prologue();
@@ -461,7 +464,7 @@ k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
             if (capped) tanh4(y);
 #pragma unroll
             for (int c = 0; c < 4; ++c) x[c] = fmaf(y[c], capped ? cap2 : kLog2e, -sub[c & 1]);
-          } else if (GEN && a.cap > kCapAbs) {
+          } else if (KIND == kLargeCap) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               x[c] = fmaf(tanh_any(s[nb][c] * fa[nb][c & 1] * (1.f / kTwoLog2e)), cap2,
@@ -910,13 +913,13 @@ cudaError_t launch_combine(const Kv4AttnArgs& a, cudaStream_t s) {
              : launch_pdl(k_kv4_combine<DH, F32, 128>, grid, dim3(128), 0, s, a);
 }
 
-template <int DH, int NB, bool F32, bool GEN>
+template <int DH, int NB, bool F32, RowKind KIND>
 cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t q_bytes =
       (size_t)NB * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, true>::kBytes;
   constexpr size_t o_bytes = (size_t)(kWarps + 1) * 8 * NB * DH * 4;
   constexpr size_t smem = q_bytes > o_bytes ? q_bytes : o_bytes;
-  auto kern = k_kv4_attn<DH, NB, F32, GEN>;
+  auto kern = k_kv4_attn<DH, NB, F32, KIND>;
   static bool attr_set = false;
   if (!attr_set && smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1057,12 +1060,13 @@ cudaError_t kv4_attn_run(Kv4AttnArgs a, cudaStream_t s) {
     if (e != cudaSuccess || a.nsplit == 1) return e;
     return a.dh == 64 ? launch_combine<64, false>(a, s) : launch_combine<128, false>(a, s);
   }
-  const bool gen = a.slope != nullptr || a.kpos != nullptr || a.cap > kCapAbs;
+  const bool gen = a.slope != nullptr || a.kpos != nullptr;
 #define PS_KV4_CASE(DH, NB)                                           \
   if (a.dh == DH && p.nb == NB) {                                     \
-    if (f32) return launch_attn<DH, NB, true, true>(a, s);            \
-    return gen ? launch_attn<DH, NB, false, true>(a, s)               \
-               : launch_attn<DH, NB, false, false>(a, s);             \
+    if (f32) return launch_attn<DH, NB, true, kAnyRows>(a, s);        \
+    if (a.cap > kCapAbs) return launch_attn<DH, NB, false, kLargeCap>(a, s); \
+    return gen ? launch_attn<DH, NB, false, kAnyRows>(a, s)           \
+               : launch_attn<DH, NB, false, kPlainRows>(a, s);        \
   }
   PS_KV4_CASE(64, 1)
   PS_KV4_CASE(64, 2)
