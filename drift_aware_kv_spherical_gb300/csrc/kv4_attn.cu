@@ -758,8 +758,8 @@ __device__ __forceinline__ SeenRange seen_range(const RowPar* par, int rows, int
 // acc[j] += sum over nbs blocks of 8 rows of exp(score - lse), slots n + sg + 8 j.
 template <int DH, bool F32, bool GEN>
 __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)[4],
-                                      const uint4* qp, const RowPar* rp, int nbs, int n_sg, int len, const int* pos,
-                                      bool masked, float* acc) {
+                                      const uint4* qp, const RowPar* rp, int nbs, int n_sg,
+                                      int len, const int* pos, bool masked, float* acc) {
   constexpr int KS = DH / 16, P = F32 ? 2 : 1;
 #pragma unroll 1
   for (; nbs > 0; --nbs, qp += P * (KS / 2) * 32, rp += 8) {
@@ -788,7 +788,8 @@ __device__ __forceinline__ void weigh(const Kv4AttnArgs& a, const uint32_t (*kf)
     if (masked) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (n_sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp[c & 1].lo || pos[c >> 1] > rp[c & 1].last)
+        if (n_sg + 8 * (c >> 1) >= len || pos[c >> 1] < rp[c & 1].lo ||
+            pos[c >> 1] > rp[c & 1].last)
           x[c] = -INFINITY;
     }
 #pragma unroll

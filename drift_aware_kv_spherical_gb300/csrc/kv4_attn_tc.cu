@@ -29,8 +29,9 @@
 // and P back, of which two row tiles hide only half.  4096 rows x 32 heads x 2 on
 // 4096 slots 419 us, 1.31 PFLOP/s, 68 % of a large library product's rate; the
 // tensor cores are busy half the time, the exponentials' unit a quarter.  Caps and
-// biases lengthen the chain: 2048 rows x 32 heads on 4096 slots 123 us plain, 198
-// capped, 254 with a bias too.
+// biases lengthen the chain: 2048 rows x 32 heads on 4096 slots 122 us plain, 191
+// capped, 241 with a bias too.  Explicit positions are masked slot by slot: causal
+// 100 us, 563 with them.
 // Every mbarrier wait is bounded (tc::mbar_wait); after a timeout the CTA waits
 // for the MMAs it issued, frees TMEM and returns with the status word set.
 #include "kv4_tc.cuh"
@@ -325,7 +326,7 @@ __device__ __forceinline__ float cap_factor(const Kv4AttnArgs& a, float f) {
 // s[0..C): raw products, f their factor -> tanh(score / cap), none above `top` (NaN
 // stays).  `small`: the series does for all of the warp's.  Caps past kCapAbs pay for
 // both formulas where it does not: 2048 rows x 32 heads on 4096 slots under a cap of
-// 30 with scores past it 275 us, 461 with both.
+// 30 with scores past it 248 us, 461 with both.
 template <int C>
 __device__ __forceinline__ void cap_tanh(const Kv4AttnArgs& a, float* s, float f, bool small,
                                          float top) {
@@ -424,7 +425,8 @@ __device__ __forceinline__ void softmax_step(const Kv4AttnArgs& a, volatile int*
     if ((GEN || !FAST) && !LATE) {
       tc_scores<GEN != 0, C>(a, s, row, n0 + k, seen, ps != nullptr ? ps + k : nullptr);
 #pragma unroll
-      for (int q = 0; q < C; q += 32) tc::tmem_st32(s_col + k + q, reinterpret_cast<uint32_t*>(s) + q);
+      for (int q = 0; q < C; q += 32)
+        tc::tmem_st32(s_col + k + q, reinterpret_cast<uint32_t*>(s) + q);
     }
 #pragma unroll
     for (int c = 0; c < C; c += 2) m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);

@@ -11,7 +11,7 @@
 //
 // What bounds them: memory, and for the store instructions close behind (issue
 // 58 % busy): eight 4096-row windows of 32 heads of 128 (688 MB each way) stored
-// in 131 us, 5.3 TB/s, and read back in 122, 5.7 TB/s, 84 % of a copy's rate; a
+// in 130 us, 5.3 TB/s, and read back in 118, 5.8 TB/s, 86 % of a copy's rate; a
 // refresh's list of a few hundred rows 5 us each, the launch.
 #include "kv4.cuh"
 
@@ -40,7 +40,8 @@ __device__ __forceinline__ void put_block(__nv_bfloat16* p, const float* x) {
 __device__ __forceinline__ void put_block(float* p, const float* x) {
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    reinterpret_cast<float4*>(p)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+    reinterpret_cast<float4*>(p)[q] =
+        make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
 }
 
 // value = fl(fl(code * scale) * mul) of one block (the first product is exact)
@@ -63,9 +64,9 @@ __device__ __forceinline__ void dequant_block(uint2 c, uint32_t sc, float mul, f
 // RN(1 / den), q = RN(x y) and the exact remainder r = x - q den, RN(q + r y) is
 // the correctly rounded quotient while nothing over- or underflows.  The remainder
 // is taken as q den - x, which is +0 and not -0 where it vanishes, and subtracted:
-// so a quotient of -0 stays -0.  Three instructions, no branch: bf16 rows hit E2M1's ties exactly so often (x and den
-// have few bits) that a fast path which detects them took its slow one in every
-// warp.
+// so a quotient of -0 stays -0.  Three instructions, no branch: bf16 rows hit E2M1's
+// ties exactly so often (x and den have few bits) that a fast path which detects
+// them took its slow one in every warp.
 __device__ __forceinline__ uint2 codes16(const float* x, float den, float y) {
   float q[16];
 #pragma unroll
@@ -77,7 +78,8 @@ __device__ __forceinline__ uint2 codes16(const float* x, float den, float y) {
 }
 
 // One block with the tensor scale S: its codes and scale.
-__device__ __forceinline__ uint32_t encode_block(const float* x, float S, float six_s, uint2* codes) {
+__device__ __forceinline__ uint32_t encode_block(const float* x, float S, float six_s,
+                                                 uint2* codes) {
   float m = 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));

@@ -245,7 +245,8 @@ k_kv4_select(const __grid_constant__ Kv4EvictArgs a, int32_t* __restrict__ idx) 
 
 // A thread takes one 16-byte piece of the codes of kRowsEach kept rows, all
 // loads before the first store, so that enough bytes are in flight at scattered
-// addresses (one row a thread 197 us where two take 189, four 190); a row's first K and first V thread move its scales too.
+// addresses (one row a thread 197 us where two take 189, four 190); a row's first
+// K and first V thread move its scales too.
 constexpr int kRowsEach = 2;
 
 template <int DH>

@@ -105,7 +105,8 @@ __device__ __forceinline__ float weigh32(const Kv4AttnArgs& a, float* s, const S
       const uint64_t ff = f2_pack(f, f);
       f = 1.f;
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), ff), s[c], s[c + 1]);
+      for (int c = 0; c < 32; c += 2)
+        f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), ff), s[c], s[c + 1]);
     }
     if (a.slope != nullptr) {  // in units of the cap, as s is
 #pragma unroll

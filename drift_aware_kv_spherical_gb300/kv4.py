@@ -111,7 +111,8 @@ class Kv4Layer:
         if self._capturing():
             self._len_seen = False      # from now on `len` changes at replays too
         elif (top := self._filled()) + T > self.cache.N:
-            raise ValueError(f"no room for {T} more tokens: {top} of {self.cache.N} slots are filled")
+            raise ValueError(f"no room for {T} more tokens: {top} of {self.cache.N} slots "
+                             "are filled")
         ps.ps_kv4_store(self.cache, K, V, off=self.len)
         known = self._known()
         self.len += T
@@ -143,7 +144,8 @@ class Kv4Layer:
         qpos, slope, cap as in ps.ps_kv4_attn."""
         scale = self.cache.dh ** -0.5 if scale is None else scale
         ps.ps_kv4_attn(self.cache, Q, O, lse, scale=scale, len=self.len, kpos=self.kpos,
-                       ws=self._workspace(ps.OP_KV4_ATTN, stream, P=Q.shape[1]), stream=stream, **see)
+                       ws=self._workspace(ps.OP_KV4_ATTN, stream, P=Q.shape[1]),
+                       stream=stream, **see)
 
     def weigh(self, Q, lse, *, scale=None, stream=None, **see):
         """Adds the weight that Q's rows put on every slot to `w`; lse as attend

@@ -22,10 +22,12 @@ the commit runs every step on the last drift computed, and suffix-block
 tokens commit only where the last layer's top-k position mask selects them
 [Polestar §2.B, suffix block commitment].
 
-With kv4=True each layer also keeps its cache in 4 bits (kv4.Kv4Layer): the
-rows a refresh rewrote are stored there behind it, and a block's attention
-reads that cache (`self.kv4[l].attend`).  After an eviction (`self.kv4[l].evict`)
-a refresh stores the rows of the positions that each KV head still holds.
+With kv4=True each layer also keeps its cache in 4 bits (kv4.Kv4Layer), beside
+the bf16 one that the refresh writes (28 % more cache memory, for one that
+attention reads in 28 % of the bytes): the rows a refresh rewrote are stored
+there, and a block's attention reads it (`self.kv4[l].attend`).  After an
+eviction (`self.kv4[l].evict`) a refresh stores the rows of the positions that
+each KV head still holds.
 
 scorer selects the drift signal: the proxy's fused KL (default), or one of
 the ablation signals (cosine dissimilarity, entropy) computed by

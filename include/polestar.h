@@ -518,7 +518,8 @@ ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V,
 /* Queries of T tokens a sequence and what they see of the cache.
  *   s   = scale * <q, k>                       k as the cache holds it
  *   s   = cap * tanh(s / cap)                  if cap > 0
- *   s  -= slope[h] * |qpos[b][t] - pos|        if slope (and qpos) given
+ *   s  -= slope[h] * |qpos[b][t] - pos|        if slope (and qpos) given; at
+ *                                              most 2^31 - 1 apart
  * Slot n of head g holds position kpos[b][g][n] (kpos NULL: n).  Row (b, t)
  * sees slot n iff n < len[b] (len NULL: Ncache) and span[b][t][0] <= pos <
  * span[b][t][1] (span NULL: all): causal is [0, qpos + 1), a prefix mask
@@ -553,7 +554,8 @@ ps_status ps_kv4_attn(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,
 /* w_out[b][g][n] = w_in[b][g][n] + the sum over the T tokens and the query
  * heads of group g of exp(s - lse), lse [B][T][Hq] as ps_kv4_attn wrote it for
  * the same query; slots that no row sees get w_in (w_in NULL: 0).  w_in may be
- * w_out.  [B][Hkv][Ncache] f32.  Deterministic.  Workspace: PS_OP_KV4_WEIGHT,
+ * w_out.  [B][Hkv][Ncache] f32.  A term is as good as the difference of an fp32 s
+ * and an fp32 lse: to some 2^-22 of their size.  Deterministic.  Workspace: PS_OP_KV4_WEIGHT,
  * same sizes. */
 ps_status ps_kv4_weight(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,
                         const float* lse, const float* w_in, float* w_out,

@@ -102,7 +102,8 @@ def test_tokens_appended_to_a_cut_cache_are_attended():
     kv.attend(Q, O, lse, **see)
     kv.weigh(Q, lse, **see)
     # bf16's half step, P's 11 bits; weights to 2^-14 (scores and lse in fp32)
-    assert np.all(np.abs(np_(O) - Oref) <= 2.0 ** -8 * np.abs(Oref) + 2.0 ** -10 * np.abs(V64).max())
+    assert np.all(np.abs(np_(O) - Oref) <=
+                  2.0 ** -8 * np.abs(Oref) + 2.0 ** -10 * np.abs(V64).max())
     assert np.allclose(np_(lse), lref, rtol=0, atol=1e-4)
     drawn = np_(kv.w)[:, :, :50] - w0[:, :, :50]
     assert np.all(w0[:, :, 30:] == 0) and np.all(np_(kv.w)[:, :, 50:] == 0)
