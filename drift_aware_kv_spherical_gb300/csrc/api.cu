@@ -536,7 +536,7 @@ bool ld_ok(int64_t ld, long least, int dtype) {
 
 ps_status kv4_rows(ps_handle h, const ps_kv4_cache* c, const void* K, const void* V, int dtype,
                    int R, int64_t b_ld, int64_t ld, const int32_t* off, const int32_t* rows,
-                   const int32_t* cnt, bool load, void* stream) {
+                   const int32_t* cnt, const int32_t* kpos, bool load, void* stream) {
   TraceScope trace_scope(h);
   PS_REQUIRE(h != nullptr && dtype_ok(dtype) && R >= 0);
   ps_status st = check_kv4(c);
@@ -546,8 +546,8 @@ ps_status kv4_rows(ps_handle h, const ps_kv4_cache* c, const void* K, const void
   PS_REQUIRE((long)R * c->Hkv <= (1 << 30));
   PS_REQUIRE(!load || c->B == 1 || b_ld > 0);  // sequences read back over one another
   PS_PTR(K); PS_PTR(V);
-  Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)b_ld, (long)ld, off, rows, cnt,
-                c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul, {}};
+  Kv4RowsArgs a{K, V, dtype, c->B, R, c->Hkv, c->Ncache, c->dh, (long)b_ld, (long)ld, off, rows,
+                cnt, kpos, c->kcode, c->kscale, c->vcode, c->vscale, c->kmul, c->vmul, {}};
   return launch_status(kv4_rows_run(a, load, static_cast<cudaStream_t>(stream)));
 }
 
@@ -590,13 +590,20 @@ extern "C" ps_status ps_kv4_store(ps_handle h, const ps_kv4_cache* c, const void
                                   const void* V, int dtype, int R, int64_t b_ld, int64_t ld,
                                   const int32_t* off, const int32_t* rows, const int32_t* cnt,
                                   void* stream) {
-  return kv4_rows(h, c, K, V, dtype, R, b_ld, ld, off, rows, cnt, false, stream);
+  return kv4_rows(h, c, K, V, dtype, R, b_ld, ld, off, rows, cnt, nullptr, false, stream);
+}
+
+extern "C" ps_status ps_kv4_store_pos(ps_handle h, const ps_kv4_cache* c, const void* K,
+                                      const void* V, int dtype, int R, int64_t b_ld, int64_t ld,
+                                      const int32_t* off, const int32_t* rows, const int32_t* cnt,
+                                      const int32_t* kpos, void* stream) {
+  return kv4_rows(h, c, K, V, dtype, R, b_ld, ld, off, rows, cnt, kpos, false, stream);
 }
 
 extern "C" ps_status ps_kv4_load(ps_handle h, const ps_kv4_cache* c, void* K, void* V, int dtype,
                                  int R, int64_t b_ld, int64_t ld, const int32_t* off,
                                  const int32_t* rows, const int32_t* cnt, void* stream) {
-  return kv4_rows(h, c, K, V, dtype, R, b_ld, ld, off, rows, cnt, true, stream);
+  return kv4_rows(h, c, K, V, dtype, R, b_ld, ld, off, rows, cnt, nullptr, true, stream);
 }
 
 extern "C" ps_status ps_kv4_attn(ps_handle h, const ps_kv4_cache* c, const ps_kv4_query* q,
@@ -628,11 +635,14 @@ extern "C" ps_status ps_kv4_weight(ps_handle h, const ps_kv4_cache* c, const ps_
   return launch_status(kv4_weight_run(a, static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" ps_status ps_kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps_kv4_cache* dst,
-                                  const float* w, const int32_t* len, const int32_t* kpos,
-                                  int keep, int sink, int recent, float* w_dst,
-                                  int32_t* kpos_dst, int32_t* len_dst, void* ws,
-                                  size_t ws_bytes, void* stream) {
+namespace {
+
+// `on`: ps_kv4_evict_on's part too.
+ps_status kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps_kv4_cache* dst, const float* w,
+                    const int32_t* len, const int32_t* kpos, int keep, int sink, int recent,
+                    float* w_dst, int32_t* kpos_dst, int32_t* len_dst, bool on,
+                    const int32_t* shift, int32_t* shift_dst, void* ws, size_t ws_bytes,
+                    void* stream) {
   TraceScope trace_scope(h);
   PS_REQUIRE(h != nullptr);
   ps_status st = check_kv4(src);
@@ -645,6 +655,7 @@ extern "C" ps_status ps_kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps
   if (src->B == 0) return PS_OK;
   PS_NN(w); PS_NN(w_dst); PS_NN(len_dst);
   PS_REQUIRE(w != w_dst && (kpos == nullptr || kpos != kpos_dst) && len != len_dst);
+  PS_REQUIRE(!on || (kpos_dst != nullptr && shift_dst != nullptr && shift != shift_dst));
   PS_REQUIRE(src->kcode != dst->kcode && src->vcode != dst->vcode &&
              src->kscale != dst->kscale && src->vscale != dst->vscale);
   st = check_ws(kv4_evict_ws(src->B, src->Hkv, keep), ws, ws_bytes);
@@ -652,6 +663,28 @@ extern "C" ps_status ps_kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps
   Kv4EvictArgs a{src->kcode, src->kscale, src->vcode, src->vscale,
                  dst->kcode, dst->kscale, dst->vcode, dst->vscale,
                  src->B, src->Hkv, src->Ncache, dst->Ncache, src->dh, keep, sink, recent,
-                 w, len, kpos, w_dst, kpos_dst, len_dst, ws};
+                 w, len, kpos, w_dst, kpos_dst, len_dst, on ? shift : nullptr,
+                 on ? shift_dst : nullptr, ws};
   return launch_status(kv4_evict_run(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" ps_status ps_kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps_kv4_cache* dst,
+                                  const float* w, const int32_t* len, const int32_t* kpos,
+                                  int keep, int sink, int recent, float* w_dst,
+                                  int32_t* kpos_dst, int32_t* len_dst, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  return kv4_evict(h, src, dst, w, len, kpos, keep, sink, recent, w_dst, kpos_dst, len_dst, false,
+                   nullptr, nullptr, ws, ws_bytes, stream);
+}
+
+extern "C" ps_status ps_kv4_evict_on(ps_handle h, const ps_kv4_cache* src,
+                                     const ps_kv4_cache* dst, const float* w, const int32_t* len,
+                                     const int32_t* kpos, int keep, int sink, int recent,
+                                     float* w_dst, int32_t* kpos_dst, int32_t* len_dst,
+                                     const int32_t* shift, int32_t* shift_dst, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  return kv4_evict(h, src, dst, w, len, kpos, keep, sink, recent, w_dst, kpos_dst, len_dst, true,
+                   shift, shift_dst, ws, ws_bytes, stream);
 }

@@ -150,6 +150,14 @@ k_kv4_select(const __grid_constant__ Kv4EvictArgs a, int32_t* __restrict__ idx) 
   }
   // Kept: protected slots, keys above `at`, and the first `need` equal to it.
   const int kept_n = all ? n : a.keep;
+  if (a.shift_dst != nullptr) {  // the slots behind them: the positions that come next
+    const int shift = (a.shift != nullptr ? a.shift[b] : 0) + n - kept_n;
+    if (bh % a.Hkv == 0 && tid == 0) a.shift_dst[b] = shift;
+    for (int j = kept_n + tid; j < a.Ndst; j += kST) {
+      a.w_dst[(long)bh * a.Ndst + j] = 0.f;
+      a.kpos_dst[(long)bh * a.Ndst + j] = j + shift;
+    }
+  }
   int32_t* out = idx + (long)bh * a.keep;
   float* w_dst = a.w_dst + (long)bh * a.Ndst;
   int32_t* kpos_dst = a.kpos_dst != nullptr ? a.kpos_dst + (long)bh * a.Ndst : nullptr;

@@ -106,6 +106,7 @@ cudaError_t refresh_run(const RefreshArgs& a, cudaStream_t s);
 struct Kv4RowsArgs {  // store: K, V -> cache; load: cache -> K, V
   const void* K; const void* V; int dtype; int B, R, Hkv, Ncache, dh; long b_ld, ld;
   const int32_t* off; const int32_t* rows; const int32_t* cnt;
+  const int32_t* kpos;  // store: positions of the slots, or null
   uint8_t* kcode; uint8_t* kscale; uint8_t* vcode; uint8_t* vscale;
   float kmul, vmul;
   Quotient by_hkv;  // set by kv4_rows_run
@@ -139,7 +140,9 @@ struct Kv4EvictArgs {
   uint8_t* kcode_dst; uint8_t* kscale_dst; uint8_t* vcode_dst; uint8_t* vscale_dst;
   int B, Hkv, Ncache, Ndst, dh, keep, sink, recent;
   const float* w; const int32_t* len; const int32_t* kpos;
-  float* w_dst; int32_t* kpos_dst; int32_t* len_dst; void* ws;
+  float* w_dst; int32_t* kpos_dst; int32_t* len_dst;
+  const int32_t* shift; int32_t* shift_dst;  // shift_dst: fill what lies behind, too
+  void* ws;
 };
 size_t kv4_evict_ws(int B, int Hkv, int keep);
 cudaError_t kv4_evict_run(const Kv4EvictArgs& a, cudaStream_t s);

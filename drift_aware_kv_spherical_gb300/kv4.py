@@ -41,7 +41,6 @@ class Kv4Layer:
         self.kpos = None
         self._note_len(0)
         self._shift = None      # [B]: position of a slot behind the kept ones, less the slot
-        self._slots = torch.arange(N, dtype=torch.int32, device=device)
         self._spare = None
         self._ws = {}
 
@@ -66,35 +65,8 @@ class Kv4Layer:
         ps.ps_kv4_store); `len` is the caller's to set.  Before the first eviction
         a position is its slot.  After it every KV head takes the row into the slot
         that holds the position, and skips a position that it has evicted."""
-        if self.kpos is None:
-            ps.ps_kv4_store(self.cache, K, V, off=off, rows=rows, cnt=cnt, stream=stream)
-            return
-        with _on(stream, self.cache.device):
-            self._store_kept(K, V, off, rows, cnt, stream)
-
-    def _store_kept(self, K, V, off, rows, cnt, stream):
-        c, (B, R) = self.cache, K.shape[:2]
-        if R == 0:
-            return
-        # listed[b][r]: row r is to be stored; R stands for no row
-        listed = torch.zeros(B, R + 1, dtype=torch.bool, device=c.device)
-        entry = torch.arange(R, dtype=torch.int32, device=c.device)
-        on = (entry < R).expand(B, R) if cnt is None else entry < cnt[:, None]
-        if rows is None:
-            listed[:, :R] = on
-        else:
-            on = on & (rows >= 0) & (rows < R)
-            listed.scatter_(1, torch.where(on, rows, R).long(), True)
-            listed[:, R] = False
-        row = self.kpos if off is None else self.kpos - off[:, None, None]
-        row = torch.where((row >= 0) & (row < R), row, R).long().view(B, -1)
-        hit = listed.gather(1, row)
-        # every head as a sequence of its own, its rows in the order of its slots
-        row = row.clamp_(max=R - 1).view(B, c.Hkv, c.N, 1).expand(-1, -1, -1, c.dh)
-        K, V = (X.transpose(1, 2).gather(2, row).view(B * c.Hkv, c.N, 1, c.dh) for X in (K, V))
-        heads = ps.Kv4Cache(*(t.view(B * c.Hkv, 1, c.N, -1) for t in c.buffers), c.kmul, c.vmul)
-        slots = torch.where(hit.view(-1, c.N), self._slots, -1)
-        ps.ps_kv4_store(heads, K, V, rows=slots, stream=stream)
+        ps.ps_kv4_store(self.cache, K, V, off=off, rows=rows, cnt=cnt, kpos=self.kpos,
+                        stream=stream)
 
     def addresses(self):
         """Where a captured store reads and writes: a graph of it holds while these
@@ -179,36 +151,31 @@ class Kv4Layer:
             if not spare:
                 spare = dict(
                     cache=ps.Kv4Cache.empty(c.B, c.Hkv, c.N, c.dh, c.kmul, c.vmul, c.device),
-                    w=torch.zeros_like(self.w), kpos=torch.zeros(c.B, c.Hkv, c.N, **i32),
-                    len=torch.zeros(c.B, **i32))
+                    w=torch.empty_like(self.w), kpos=torch.empty(c.B, c.Hkv, c.N, **i32),
+                    len=torch.empty(c.B, **i32), shift=torch.empty(c.B, **i32))
         elif not spare:
             raise ValueError("an eviction has taken this spare already")
         here = torch.cuda.current_stream(c.device) if c.device.type == "cuda" else None
         if spare.get("stream", here) != here and not torch.cuda.is_current_stream_capturing():
             here.wait_stream(spare["stream"])   # (a capture begins behind everything)
-        # ps_kv4_evict leaves what lies behind the kept slots as it is, and the
-        # buffers served an older cache: the next positions, without weight
-        shift = (self.len - keep).clamp_(min=0)
-        if self._shift is not None:
-            shift += self._shift
-        spare["w"].zero_()
-        spare["kpos"].copy_((self._slots + shift[:, None])[:, None])
         ps.ps_kv4_evict(c, spare["cache"], self.w, spare["w"], spare["len"], keep, sink=sink,
                         recent=recent, len=self.len, kpos=self.kpos, kpos_dst=spare["kpos"],
+                        shift=self._shift, shift_dst=spare["shift"],
                         ws=self._workspace(ps.OP_KV4_EVICT, stream, k=keep), stream=stream)
-        kpos = torch.zeros(c.B, c.Hkv, c.N, **i32) if self.kpos is None else self.kpos
+        kpos, shift = self.kpos, self._shift
+        if kpos is None:
+            kpos, shift = torch.empty(c.B, c.Hkv, c.N, **i32), torch.empty(c.B, **i32)
         if self._capturing():
             self._len_seen = False
         known = self._known()
         # the one reference to the old buffers that a later eviction, this
         # layer's or another's, may write through: whoever takes them empties it
-        self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len, stream=here)
+        self._spare = dict(cache=c, w=self.w, kpos=kpos, len=self.len, shift=shift, stream=here)
         if here is not None:    # they may have been allocated on another stream, and may be freed
-            for t in (*c.buffers, self.w, kpos, self.len, self._shift):
-                if t is not None:
-                    t.record_stream(here)
-        self.cache, self.w, self.kpos, self.len = (spare[k] for k in ("cache", "w", "kpos", "len"))
-        self._shift = shift
+            for t in (*c.buffers, self.w, kpos, self.len, shift):
+                t.record_stream(here)
+        self.cache, self.w, self.kpos, self.len, self._shift = (
+            spare[k] for k in ("cache", "w", "kpos", "len", "shift"))
         if known:
             self._note_len(min(self._top, keep))
         spare.clear()

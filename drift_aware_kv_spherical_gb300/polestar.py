@@ -26,7 +26,7 @@ EXPORTED = ["ps_create", "ps_destroy", "ps_check", "ps_status_string", "ps_last_
             "ps_store_record_bytes", "ps_host_alloc", "ps_host_free",
             "ps_nvfp4_pack_clusters", "ps_nvfp4_fetch_dequant", "ps_schedule_step", "ps_drift_score",
             "ps_block_progress", "ps_kv4_store", "ps_kv4_load", "ps_kv4_attn",
-            "ps_kv4_weight", "ps_kv4_evict"]
+            "ps_kv4_weight", "ps_kv4_evict", "ps_kv4_store_pos", "ps_kv4_evict_on"]
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
@@ -97,10 +97,12 @@ _SIGS = {
     "ps_commit": (_i, [_p, _p, _i, _i, _i, _i, _p, _p, _p, _i, _p, _p, _p, _p, _i,
                        CommitParams, _p, _p, _p, _p, _sz, _p]),
     "ps_kv4_store": (_i, [_p, _p, _p, _p, _i, _i, _i64, _i64, _p, _p, _p, _p]),
+    "ps_kv4_store_pos": (_i, [_p, _p, _p, _p, _i, _i, _i64, _i64, _p, _p, _p, _p, _p]),
     "ps_kv4_load": (_i, [_p, _p, _p, _p, _i, _i, _i64, _i64, _p, _p, _p, _p]),
     "ps_kv4_attn": (_i, [_p, _p, _p, _p, _p, _p, _sz, _p]),
     "ps_kv4_weight": (_i, [_p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "ps_kv4_evict": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
+    "ps_kv4_evict_on": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 
 
@@ -471,7 +473,7 @@ def _rows_ld(t, B, H, dh):
     return R, sb if B > 1 else 0, sr if R > 1 else H * dh
 
 
-def _kv4_rows(name, c, K, V, off, rows, cnt, stream):
+def _kv4_rows(name, c, K, V, off, rows, cnt, stream, *kpos):
     R, bld, ld = _rows_ld(K, c.B, c.Hkv, c.dh)
     if (V.dtype != K.dtype or V.shape != K.shape or not V.is_cuda or
             (V.stride() != K.stride() and _rows_ld(V, c.B, c.Hkv, c.dh) != (R, bld, ld))):
@@ -480,14 +482,19 @@ def _kv4_rows(name, c, K, V, off, rows, cnt, stream):
     st = getattr(lib.cdll, name)(
         lib.handle(c.index), c._c, K.data_ptr(), V.data_ptr(), _dtype(K), R, bld, ld,
         _plain(off, torch.int32, (c.B,), True), _plain(rows, torch.int32, (c.B, R), True),
-        _plain(cnt, torch.int32, (c.B,), True), _kv4_stream(stream, c))
+        _plain(cnt, torch.int32, (c.B,), True), *kpos, _kv4_stream(stream, c))
     _check(st, name)
 
 
-def ps_kv4_store(c, K, V, off=None, rows=None, cnt=None, stream=None):
+def ps_kv4_store(c, K, V, off=None, rows=None, cnt=None, stream=None, kpos=None):
     """Rows of K and V [B][R][Hkv][dh] (all, or the listed ones) into slots
-    off[b] + r of the cache."""
-    _kv4_rows("ps_kv4_store", c, K, V, off, rows, cnt, stream)
+    off[b] + r of the cache, or with kpos [B][Hkv][Ncache], the slots' ascending
+    positions, into the slot of every head that holds position off[b] + r."""
+    if kpos is None:
+        _kv4_rows("ps_kv4_store", c, K, V, off, rows, cnt, stream)
+    else:
+        _kv4_rows("ps_kv4_store_pos", c, K, V, off, rows, cnt, stream,
+                  _plain(kpos, torch.int32, (c.B, c.Hkv, c.N)))
 
 
 def ps_kv4_load(c, K, V, off=None, rows=None, cnt=None, stream=None):
@@ -539,19 +546,25 @@ def ps_kv4_weight(c, Q, lse, w_in, w_out, *, scale, len=None, span=None, kpos=No
 
 
 def ps_kv4_evict(src, dst, w, w_dst, len_dst, keep, sink=0, recent=0, len=None, kpos=None,
-                 kpos_dst=None, ws=None, stream=None):
+                 kpos_dst=None, ws=None, stream=None, shift=None, shift_dst=None):
     """Keeps `keep` slots of every (sequence, KV head) of src -- the first
     `sink`, the last `recent` and the heaviest of the others by w -- in the
-    first slots of dst."""
+    first slots of dst.  With shift_dst [B] the slots behind them get no weight
+    and the positions that come next (ps_kv4_evict_on)."""
     lib = _lib()
     f32, i32 = torch.float32, torch.int32
     a, b = (src.B, src.Hkv, src.N), (src.B, src.Hkv, dst.N)
     wsp, wn = _ws(ws)
-    st = lib.cdll.ps_kv4_evict(
-        lib.handle(src.index), src._c, dst._c, _plain(w, f32, a),
-        _plain(len, i32, (src.B,), True), _plain(kpos, i32, a, True), int(keep), int(sink),
-        int(recent), _plain(w_dst, f32, b), _plain(kpos_dst, i32, b, True),
-        _plain(len_dst, i32, (src.B,)), wsp, wn, _kv4_stream(stream, src))
+    args = (lib.handle(src.index), src._c, dst._c, _plain(w, f32, a),
+            _plain(len, i32, (src.B,), True), _plain(kpos, i32, a, True), int(keep), int(sink),
+            int(recent), _plain(w_dst, f32, b), _plain(kpos_dst, i32, b, True),
+            _plain(len_dst, i32, (src.B,)))
+    if shift_dst is None:
+        st = lib.cdll.ps_kv4_evict(*args, wsp, wn, _kv4_stream(stream, src))
+    else:
+        st = lib.cdll.ps_kv4_evict_on(*args, _plain(shift, i32, (src.B,), True),
+                                      _plain(shift_dst, i32, (src.B,)), wsp, wn,
+                                      _kv4_stream(stream, src))
     _check(st, "ps_kv4_evict")
 
 

@@ -507,6 +507,15 @@ ps_status ps_kv4_store(ps_handle h, const ps_kv4_cache* c, const void* K,
                        int64_t ld, const int32_t* off, const int32_t* rows,
                        const int32_t* cnt, void* stream);
 
+/* The same into a cache whose slots hold the positions kpos [B][Hkv][Ncache]
+ * (ascending in every head; NULL: the slots themselves), as an eviction leaves it:
+ * row r goes, in every KV head, to the slot that holds position off[b] + r, and is
+ * skipped where none does. */
+ps_status ps_kv4_store_pos(ps_handle h, const ps_kv4_cache* c, const void* K,
+                           const void* V, int dtype, int R, int64_t b_ld,
+                           int64_t ld, const int32_t* off, const int32_t* rows,
+                           const int32_t* cnt, const int32_t* kpos, void* stream);
+
 /* The reverse, with the same list: element = fl(code * s * S) rounded to
  * dtype (bf16: RNE) into K and V, whose rows must not overlap (b_ld > 0 for
  * B > 1); rows not listed are untouched. */
@@ -576,6 +585,17 @@ ps_status ps_kv4_evict(ps_handle h, const ps_kv4_cache* src, const ps_kv4_cache*
                        int keep, int sink, int recent, float* w_dst,
                        int32_t* kpos_dst, int32_t* len_dst, void* ws,
                        size_t ws_bytes, void* stream);
+
+/* The same, and leaves dst ready to go on: the slots behind the kept ones, up to
+ * dst->Ncache, get weight 0 and the positions that come next.  A slot n behind the
+ * filled ones stands for position n + shift[b] (shift [B], NULL: 0), in dst for
+ * n + shift_dst[b], shift_dst[b] = shift[b] + len[b] - len_dst[b].  kpos_dst and
+ * shift_dst are needed, shift_dst is not shift. */
+ps_status ps_kv4_evict_on(ps_handle h, const ps_kv4_cache* src, const ps_kv4_cache* dst,
+                          const float* w, const int32_t* len, const int32_t* kpos,
+                          int keep, int sink, int recent, float* w_dst,
+                          int32_t* kpos_dst, int32_t* len_dst, const int32_t* shift,
+                          int32_t* shift_dst, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

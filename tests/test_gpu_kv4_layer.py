@@ -10,7 +10,7 @@ from drift_aware_kv_spherical_gb300 import polestar as ps
 from drift_aware_kv_spherical_gb300 import workloads as wl
 from drift_aware_kv_spherical_gb300.kv4 import Kv4Layer
 from drift_aware_kv_spherical_gb300.pipeline import Pipeline
-from tests._parity import np_
+from tests._parity import Guarded, np_
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,101 @@ def test_attention_on_two_streams_at_once(monkeypatch):
     for i, (O, lse) in enumerate(outs):
         assert torch.equal(O, want[i % 2][0]) and torch.equal(lse, want[i % 2][1]), i
     assert used[streams[0]] != used[streams[1]]
+
+
+@pytest.mark.parametrize("B,R,Hkv,dh,N,dtype", [
+    (2, 60, 3, 64, 50, torch.bfloat16), (1, 9, 2, 256, 1, torch.float32),
+    (3, 200, 1, 128, 130, torch.float32), (1, 1, 5, 128, 700, torch.bfloat16)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_store_by_positions(B, R, Hkv, dh, N, dtype, listed):
+    """Rows to the slots that hold their positions, which differ from head to head;
+    everything else untouched: bits as the oracle's."""
+    rng = np.random.default_rng(R + N)
+    K, V = (torch.from_numpy(rng.standard_normal((B, R, Hkv, dh)).astype(np.float32)).to(dtype)
+            for _ in range(2))
+    span = max(N, R) + 40
+    kpos = np.sort(np.stack([[rng.choice(span, N, False) for _ in range(Hkv)]
+                             for _ in range(B)]), -1) - 20
+    off = rng.integers(-10, 10, B)
+    rows = rng.integers(-2, R + 2, (B, R))
+    cnt = rng.integers(0, R + 1, B)
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()  # noqa: E731
+    bufs = [Guarded((B, Hkv, N, dh // q), torch.uint8, fill=0x3C) for q in (2, 16, 2, 16)]
+    c = ps.Kv4Cache(*(g.t for g in bufs), kmul=0.7, vmul=0.3)
+    opt = dict(rows=i32(rows), cnt=i32(cnt)) if listed else {}
+    ps.ps_kv4_store(c, K.cuda(), V.cuda(), off=i32(off), kpos=i32(kpos), **opt)
+    enc = [oracle.kv4_encode(X.float().numpy().transpose(0, 2, 1, 3), S)
+           for X, S in ((K, 0.7), (V, 0.3))]
+    for b in range(B):
+        entries = rows[b, :cnt[b]] if listed else np.arange(R)
+        named = {int(r) + int(off[b]): int(r) for r in entries if 0 <= r < R}
+        for h in range(Hkv):
+            for n in range(N):
+                r = named.get(int(kpos[b, h, n]))
+                for i, g in enumerate(bufs):
+                    want = 0x3C if r is None else enc[i // 2][i % 2][b, h, r]
+                    assert np.all(np_(g.t[b, h, n]) == want), (b, h, n, r)
+    assert all(g.intact() for g in bufs)
+
+
+@pytest.mark.parametrize("B,Hkv,dh,N,M,keep", [
+    (2, 3, 64, 100, 100, 40), (1, 2, 128, 3000, 2000, 700), (3, 1, 64, 9000, 9100, 8000),
+    (1, 1, 256, 5, 5, 5)])
+@pytest.mark.parametrize("again", [False, True])
+def test_an_eviction_that_goes_on(B, Hkv, dh, N, M, keep, again):
+    """ps_kv4_evict_on: what ps_kv4_evict gives, and behind it the positions that come
+    next, without weight; from slots and from positions that were shifted before."""
+    rng = np.random.default_rng(N)
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()  # noqa: E731
+    src = ps.Kv4Cache(*(torch.from_numpy(rng.integers(0, 256, (B, Hkv, N, dh // q), dtype=np.uint8))
+                        .cuda() for q in (2, 16, 2, 16)))
+    w = torch.rand(B, Hkv, N, device="cuda")
+    length = rng.integers(0, N + 1, B)
+    length[0] = N
+    shift = rng.integers(1, 1000, B) if again else np.zeros(B, int)
+    kpos = np.arange(N) + shift[:, None, None] + np.zeros((B, Hkv, 1), int)
+    opt = dict(len=i32(length), kpos=i32(kpos) if again else None,
+               ws=ps.workspace(ps.OP_KV4_EVICT, B=B, N=N, Hkv=Hkv, k=keep))
+    sink = min(2, keep)
+    got, want = [], []
+    for out in (got, want):
+        d = ps.Kv4Cache(*(torch.full((B, Hkv, M, dh // q), 0x3C, dtype=torch.uint8, device="cuda")
+                          for q in (2, 16, 2, 16)))
+        wd = Guarded((B, Hkv, M), torch.float32, fill=5)
+        kd = Guarded((B, Hkv, M), torch.int32, fill=-9)
+        ld, sd = Guarded((B,), torch.int32, fill=-9), Guarded((B,), torch.int32, fill=-9)
+        on = dict(shift=i32(shift) if again else None, shift_dst=sd.t) if out is got else {}
+        ps.ps_kv4_evict(src, d, w, wd.t, ld.t, keep, sink=sink, kpos_dst=kd.t, **opt, **on)
+        assert all(g.intact() for g in (wd, kd, ld, sd))
+        out.extend([*d.buffers, wd.t, kd.t, ld.t, sd.t])
+    kept = np.minimum(length, keep)
+    assert got[6].tolist() == list(kept) == want[6].tolist()
+    assert got[7].tolist() == list(shift + length - kept) and want[7].tolist() == [-9] * B
+    for b in range(B):
+        k = int(kept[b])
+        for x, y in zip(got[:6], want[:6]):
+            assert torch.equal(x[b, :, :k], y[b, :, :k])
+        assert all(bool((x[b, :, k:] == 0x3C).all()) for x in got[:4])
+        assert bool((got[4][b, :, k:] == 0).all())
+        after = torch.arange(k, M, dtype=torch.int32) + int(shift[b] + length[b] - k)
+        assert torch.equal(got[5][b, :, k:].cpu(), after.expand(Hkv, -1))
+        assert bool((want[5][b, :, k:] == -9).all()) and bool((want[4][b, :, k:] == 5).all())
+
+
+def test_what_an_eviction_that_goes_on_needs():
+    c, d = ps.Kv4Cache.empty(1, 1, 30, 64), ps.Kv4Cache.empty(1, 1, 30, 64)
+    w, wd = torch.zeros(1, 1, 30, device="cuda"), torch.zeros(1, 1, 30, device="cuda")
+    ld, sd = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    kd = torch.zeros(1, 1, 30, dtype=torch.int32, device="cuda")
+    ws = ps.workspace(ps.OP_KV4_EVICT, B=1, N=30, Hkv=1, k=5)
+    for bad in (dict(shift_dst=sd), dict(shift=sd, shift_dst=sd, kpos_dst=kd)):
+        with pytest.raises(ps.PolestarError) as e:
+            ps.ps_kv4_evict(c, d, w, wd, ld, 5, ws=ws, **bad)
+        assert e.value.status == ps.PS_ERR_ARG
+    for bad in (dict(shift_dst=sd.long(), kpos_dst=kd),
+                dict(shift_dst=sd, kpos_dst=kd, shift=wd[0])):
+        with pytest.raises(ValueError):
+            ps.ps_kv4_evict(c, d, w, wd, ld, 5, ws=ws, **bad)
+    K = torch.zeros(1, 4, 1, 64, device="cuda")
+    with pytest.raises(ValueError):
+        ps.ps_kv4_store(c, K, K, kpos=kd[:, :, :20])

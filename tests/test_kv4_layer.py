@@ -27,28 +27,34 @@ class _Cache:
         return cls(*mk, kmul=kmul, vmul=vmul)
 
 
-def _store(c, K, V, off=None, rows=None, cnt=None, stream=None):
+def _store(c, K, V, off=None, rows=None, cnt=None, stream=None, kpos=None):
     R = K.shape[1]
     for b in range(c.B):
         n = R if cnt is None else min(int(cnt[b]), R)
         for j in range(n):
             r = j if rows is None else int(rows[b, j])
-            slot = r + (0 if off is None else int(off[b]))
-            if not (0 <= r < R and 0 <= slot < c.N):
+            at = r + (0 if off is None else int(off[b]))
+            if not 0 <= r < R:
                 continue
             for X, S, code, scale in ((K, c.kmul, *c.buffers[:2]), (V, c.vmul, *c.buffers[2:])):
                 a, s = oracle.kv4_encode(X[b, r].float().numpy(), S)
-                code[b, :, slot], scale[b, :, slot] = torch.from_numpy(a), torch.from_numpy(s)
+                for h in range(c.Hkv):
+                    held = torch.arange(c.N) if kpos is None else kpos[b, h]
+                    for n in (held == at).nonzero().flatten():
+                        code[b, h, n] = torch.from_numpy(a[h])
+                        scale[b, h, n] = torch.from_numpy(s[h])
 
 
 def _evict(src, dst, w, w_dst, len_dst, keep, sink=0, recent=0, len=None, kpos=None,
-           kpos_dst=None, ws=None, stream=None):
+           kpos_dst=None, ws=None, stream=None, shift=None, shift_dst=None):
     if sink + recent > keep or keep > dst.N:
         raise ps.PolestarError(ps.PS_ERR_ARG, "ps_kv4_evict")
     assert not set(t.data_ptr() for t in src.buffers) & set(t.data_ptr() for t in dst.buffers)
     for b in range(src.B):
         n = int(len[b])
         len_dst[b] = min(n, keep)
+        if shift_dst is not None:
+            shift_dst[b] = (0 if shift is None else int(shift[b])) + n - min(n, keep)
         for h in range(src.Hkv):
             at = torch.from_numpy(oracle.kv4_keep(w[b, h].numpy(), n, keep, sink, recent))
             k = at.numel()
@@ -56,6 +62,9 @@ def _evict(src, dst, w, w_dst, len_dst, keep, sink=0, recent=0, len=None, kpos=N
                 y[b, h, :k] = x[b, h, at]
             w_dst[b, h, :k] = w[b, h, at]
             kpos_dst[b, h, :k] = (at if kpos is None else kpos[b, h, at]).int()
+            if shift_dst is not None:
+                w_dst[b, h, k:] = 0
+                kpos_dst[b, h, k:] = torch.arange(k, dst.N) + int(shift_dst[b])
 
 
 @pytest.fixture(autouse=True)
