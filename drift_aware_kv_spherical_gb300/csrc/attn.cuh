@@ -166,11 +166,13 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 
 // One row again, for a whole warp, over the slots that it sees only.  The tiles'
 // products multiply what a row does not see by zero, which leaves a NaN if that is
-// infinite or NaN: a row that did not come out finite is computed like this.
+// infinite or NaN, and fp32's low terms turn a seen infinity's score into one (0 times
+// infinity): a row that did not come out finite is computed like this, its lse too.
 template <typename T>
 __device__ __noinline__ void attn_redo(const AttnArgs& a, const AttnSeq s, int t, int h) {
   constexpr int E = 8;  // elements a lane: dh <= 256
   const int lane = threadIdx.x & 31;
+  __syncwarp();  // (what other lanes stored of the row comes first)
   const int2 see = attn_seen(a, s, t);
   const T* q = static_cast<const T*>(a.Q) + (long)(s.q0 + t) * a.q_ld + (long)h * a.dh;
   const long at = (long)(h / a.G) * a.dh;
@@ -205,6 +207,7 @@ __device__ __noinline__ void attn_redo(const AttnArgs& a, const AttnSeq s, int t
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if (lane + 32 * e < a.dh) Store<T>::put(to + lane + 32 * e, o[e] * inv);
+  if (lane == 0 && a.lse != nullptr) a.lse[(long)(s.q0 + t) * a.Hq + h] = attn_lse(m, l);
 }
 
 // Four finished elements of a row from its sums; false where one is infinite or NaN.
