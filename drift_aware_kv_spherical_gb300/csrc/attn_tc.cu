@@ -41,6 +41,10 @@ namespace {
 constexpr int kTcThreads = 384;
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
 constexpr int kItems = 4;           // items known and not yet taken by every warp
+// Items of a softmax warp with rows to be computed again.  The first is the last one that
+// its CTA asks for: kItems more may be known by then, and one claimed.
+constexpr int kAgain = 8;
+static_assert(kAgain >= kItems + 2, "the items that still come");
 constexpr int kTile = 128;          // slots a step
 static_assert(kTcRows == 128, "a thread a row");
 constexpr float kGrow = 8.f;        // log2 growth of a maximum before O is rescaled
@@ -59,6 +63,15 @@ struct TcItem {
   }
 };
 
+struct TcAgain {
+  uint32_t rows;  // of the warp
+  int r0, h0;     // first row of Q of the row tile, first head of the group
+};
+struct TcAgains {
+  int num;
+  TcAgain item[kAgain];
+};
+
 template <int DH>
 struct TcSmem {
   static constexpr uint32_t kOp = (DH / 64) * 16384u;      // 128 rows of DH bf16
@@ -66,7 +79,8 @@ struct TcSmem {
   static constexpr uint32_t kKv = 2 * kOp;                 // Q at 0
   static constexpr uint32_t kBar = kKv + kRing * kOp;
   static constexpr uint32_t kWork = kBar + 512;            // TcItem [kItems], then a claim
-  static constexpr size_t kBytes = 1024 + kWork + kItems * sizeof(TcItem) + 16;
+  static constexpr uint32_t kRedo = kWork + kItems * sizeof(TcItem) + 16;  // TcAgains [8]
+  static constexpr size_t kBytes = 1024 + kRedo + 8 * sizeof(TcAgains);
 };
 static_assert(sizeof(TcItem) % 16 == 0, "the claim behind the items is 16-byte aligned");
 static_assert(TcSmem<128>::kBytes <= 227 * 1024, "a CTA's shared memory");
@@ -349,6 +363,7 @@ k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMa
   uint64_t* c_done = c_ask + 1;   // the 39th of 64
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* stop = abort_flag + 1;  // no more items: rows are to be computed again
   TcItem* ring = reinterpret_cast<TcItem*>(smem + SM::kWork);
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -374,8 +389,10 @@ k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMa
     tc::mbar_init(c_ask, 1);
     tc::mbar_init(c_done, 1);
     *abort_flag = 0;
+    *stop = 0;
     tc::fence_mbar_init();
   }
+  if (tid < 8) reinterpret_cast<TcAgains*>(smem + SM::kRedo)[tid].num = 0;
   if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
   tc::fence_before_sync();
   __syncthreads();
@@ -511,12 +528,13 @@ k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMa
       if (!part) {
         const __nv_bfloat162 z = __hadd2(zero[0], zero[1]);
         const bool fine = __low2float(z) == 0.f && __high2float(z) == 0.f;
-        uint32_t bad = __ballot_sync(0xffffffffu, in && !fine);
-        while (bad != 0) {
-          const int k = __ffs(bad) - 1;
-          bad &= bad - 1;
-          attn_redo<__nv_bfloat16>(a, seq, __shfl_sync(0xffffffffu, t, k),
-                                   __shfl_sync(0xffffffffu, h, k));
+        const uint32_t bad = __ballot_sync(0xffffffffu, in && !fine);
+        if (bad != 0) {
+          if (lane == 0) {
+            TcAgains* const x = reinterpret_cast<TcAgains*>(smem + SM::kRedo) + warp;
+            x->item[x->num++] = TcAgain{bad, seq.q0 + t - tt, h - hh};
+            *stop = 1;
+          }
         }
       }
     }
@@ -741,6 +759,10 @@ k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMa
           if (!__all_sync(0xffffffffu, ok)) break;
           ++k;
         }
+        if (__any_sync(0xffffffffu, *stop != 0)) {
+          item = -1;
+          continue;
+        }
         if (lane == 0) {
           tc::fence_proxy_async_smem();  // the last claim has been read
           claim_ask(claim, c_done);
@@ -765,6 +787,19 @@ k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMa
   if (warp == 8) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
+  } else if (warp < 8 && *stop != 0 && *abort_flag == 0) {
+    // Rows that are computed again, when no other warp waits any more: 32 over 100 thousand
+    // slots take longer than a wait may.  (The items that are left run in CTAs of their own.)
+    const TcAgains* const again = reinterpret_cast<const TcAgains*>(smem + SM::kRedo) + warp;
+    for (int i = 0; i < again->num; ++i) {
+      const TcAgain x = again->item[i];
+      const AttnSeq seq =
+          attn_seq(a, attn_find(a.S, x.r0, [&](int s) { return (long)attn_q_off(a, s); }));
+      for (uint32_t rows = x.rows; rows != 0; rows &= rows - 1) {
+        const int m = (warp & 3) * 32 + __ffs(rows) - 1, t = (int)a.by_g.of((uint32_t)m);
+        attn_redo<__nv_bfloat16>(a, seq, x.r0 - seq.q0 + t, x.h0 + m - t * a.G);
+      }
+    }
   }
 }
 
