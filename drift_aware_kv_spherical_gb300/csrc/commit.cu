@@ -130,6 +130,7 @@ k_commit_rule(int P, int nchunk, const float* __restrict__ pm,
   int tok = 0;
   if (DRAWN) {
     if (valid) c = (double)conf[row];
+    if (c != c) c = -INFINITY;
   } else if (valid) {
     float M = -INFINITY;
     for (int q = 0; q < nchunk; ++q) M = fmaxf(M, pm[row * nchunk + q]);
@@ -171,7 +172,7 @@ k_commit_rule(int P, int nchunk, const float* __restrict__ pm,
   const int any_und = __syncthreads_or(cur_und);
   if (p.ensure_progress && any_und && !any_commit) {
     // largest confidence among undecided current tokens, ties to lower j
-    double bc = cur_und ? c : -1.0;
+    double bc = cur_und ? c : -INFINITY;
     int bj = cur_und ? j : INT_MAX;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {

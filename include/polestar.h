@@ -763,7 +763,8 @@ ps_status ps_sample(ps_handle h, const ps_sample_rows* s, int32_t* token, float*
                     int32_t* n, void* stream);
 
 /* ps_commit's rule with the tokens' confidences given (conf [B][P] f32, e.g. the prob
- * of ps_sample): everything as there, no logits, no workspace. */
+ * of ps_sample; any numbers, a NaN counts as -inf): everything as there, no logits, no
+ * workspace. */
 ps_status ps_commit_drawn(ps_handle h, const float* conf, int B, int P,
                           const uint8_t* role, uint8_t* undecided, const float* D_blk,
                           int d_ld, float* d_sum, int32_t* d_cnt, float* d_prev,
