@@ -4,7 +4,9 @@
 // angle is kept as a fraction of a turn in 64-bit fixed point: position * turns
 // modulo 2^64 is exact at any position, where a product in fp32 is off by a tenth
 // of a radian at a million.  Its nearest quarter turn is split off as an integer and
-// the rest, at most an eighth of a turn, is a float good to 2^-28 of a turn.
+// the rest, at most an eighth of a turn, is a float good to 2^-28 of a turn, 2^-25.3
+// radians.  (Added on by the derivatives, what that leaves took the worst mean error of an
+// angle from 2.4e-8 to 1.5e-8 only: cosine and sine are rounded themselves.)
 //
 // A CTA takes a token of a sequence: its threads work out the cosine and sine of
 // every pair once into shared memory, then move all heads of Q, K and V, each

@@ -665,7 +665,7 @@ typedef struct {
 } ps_rope_rows;
 
 /* One to three parts (a layer's Q, K and V) in one launch.  B * T < 2^31,
- * H <= 4096.  The angle is position * turns to 2^-26 radians at any position of 32
+ * H <= 4096.  The angle is position * turns to 2^-25 radians at any position of 32
  * bits (ps_rope_turns works in fp64: some 2^-50 of a frequency).  Bit-exact from
  * call to call. */
 ps_status ps_rope(ps_handle h, const ps_rope_rows* r, const ps_rope_part* parts,
