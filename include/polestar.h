@@ -650,8 +650,9 @@ typedef struct {
  * (j where rows is NULL; entries outside [0, T) are skipped) names row r of
  * sequence b: its position is pos[b*T + r] (pos NULL: off[b] + r), its slot
  * dst[b*T + r] (dst NULL: off[b] + r; off NULL: r).  Other rows are untouched.
- * An entry that is there twice, or a slot named twice, holds either row; with
- * Y == X the entries of a list must differ. */
+ * An entry that is there twice writes the same twice, but with Y == X, where the
+ * entries of a list must differ.  Of a slot that two rows name every element is one of
+ * the two rows', not all of them the same one's, and another call's may be others. */
 typedef struct {
   const uint64_t* turns;  /* [rot/2], device memory                           */
   const int32_t* pos;     /* [B][T] or NULL; negative positions turn back     */
@@ -667,7 +668,7 @@ typedef struct {
 /* One to three parts (a layer's Q, K and V) in one launch.  B * T < 2^31,
  * H <= 4096.  The angle is position * turns to 2^-25 radians at any position of 32
  * bits (ps_rope_turns works in fp64: some 2^-50 of a frequency).  Bit-exact from
- * call to call. */
+ * call to call, slots named twice apart. */
 ps_status ps_rope(ps_handle h, const ps_rope_rows* r, const ps_rope_part* parts,
                   int nparts, void* stream);
 
