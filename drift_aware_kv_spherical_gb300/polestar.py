@@ -712,7 +712,9 @@ def ps_attn(Q, K, V, O, lse=None, *, q_off, k_off, k_len=None, span=None, causal
     """Attention of Q [Tq][Hq][dh] over K, V [Tk][Hkv][dh] (a cache [B][N][Hkv][dh] as
     B * N rows) into O [Tq][Hq][dh] and lse [Tq][Hq]: sequence s has the rows q_off[s] up to
     q_off[s + 1] of Q and k_off[s] up to k_off[s] + k_len[s] (k_len None: k_off[s + 1]) of K.
-    max_q, max_k: the most of a sequence, if the caller knows."""
+    max_q, max_k: the most of a sequence, if the caller knows (None: all of Q's, of K's).
+    ws: of these numbers, ps.workspace(ps.OP_ATTN, B=S, N=max_k, Hq=.., Hkv=.., dh=.., P=Tq,
+    k=max_q); one of others, larger ones too, may not be enough."""
     dh, dtype, index = Q.shape[-1], Q.dtype, Q.get_device()
     Tq, q_ld = _heads_ld(Q, None, dh, dtype, index)
     Hq = Q.shape[1]

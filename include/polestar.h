@@ -701,7 +701,9 @@ ps_status ps_rope(ps_handle h, const ps_rope_rows* r, const ps_rope_part* parts,
  * Sizes: S, Tq >= 0 (0: no-op), S <= 2^20, Tq * Hq <= 2^30, Tk < 2^31 - 2^16,
  *   Hkv <= 512, Hq / Hkv <= 4096, dh % 16 == 0, dh <= 256, max_q, max_k >= 1.
  * Workspace: ps_workspace_bytes(PS_OP_ATTN, B = S, N = max_k, Hq, Hkv, dh, P = Tq,
- * k = max_q); the call takes no more than that for these numbers. */
+ * k = max_q), of the numbers that the call gets: others, larger ones too, may give less,
+ * since they choose how the slots are shared out.  A caller whose lengths grow passes one
+ * max_k throughout. */
 typedef struct {
   const void* Q;
   const void* K;
