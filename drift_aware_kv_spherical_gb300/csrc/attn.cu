@@ -543,8 +543,8 @@ k_attn(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap t
   }
 }
 
-// Row number i of those that are joined: its sequence, token and head; false where there is
-// none.  For whole warps.
+// Row number i of those that are joined (its partial sums' too, attn_part): its sequence,
+// token and head; false where there is none.  For whole warps.
 __device__ __forceinline__ bool join_row(const AttnArgs& a, int i, AttnSeq* seq, int* t, int* h) {
   if (a.per_seq > 0) {  // numbers for the most rows that a sequence may have
     const int k = i / a.Hkv, hkv = i - k * a.Hkv, s = k / a.most, m = k - s * a.most;
@@ -581,7 +581,7 @@ k_attn_join(const __grid_constant__ AttnArgs a) {
   AttnSeq seq;
   if (!join_row(a, blockIdx.x, &seq, &t, &h)) return;
   const int r = seq.q0 + t, tid = threadIdx.x;
-  const long row = (long)r * a.Hq + h;
+  const long row = blockIdx.x;
   const int2 shares = join_shares(a, seq, t);
   const int from = shares.x, to = shares.y;
   const float* pml = a.pml + 2 * row * a.nsplit;
@@ -625,7 +625,7 @@ k_attn_join_rows(const __grid_constant__ AttnArgs a, int count) {
   int t, h;
   AttnSeq seq;
   if (i >= count || !join_row(a, i, &seq, &t, &h)) return;
-  const long row = (long)(seq.q0 + t) * a.Hq + h;
+  const long row = i;
   const int2 shares = join_shares(a, seq, t);
   const float* pml = a.pml + 2 * row * a.nsplit;
   const float* po = a.po + row * a.nsplit * a.dh;
@@ -731,9 +731,14 @@ Plan plan(int dtype, int S, int max_k, int Hq, int Hkv, int dh, int Tq, int max_
   }
   return p;
 }
-void parts(Carver& cv, const Part& p, int Tq, int Hq, int dh, float** po, float** pml) {
+// Rows whose shares are joined.
+long joined(const Part& p, int S, int Hq, int Hkv, int Tq) {
+  return p.per_seq > 0 ? (long)S * p.most * Hkv : (long)Tq * Hq;
+}
+void parts(Carver& cv, const Part& p, int S, int Hq, int Hkv, int dh, int Tq, float** po,
+           float** pml) {
   if (!p.on || p.nsplit == 1 || p.cluster) return;
-  const size_t rows = (size_t)Tq * Hq * p.nsplit;
+  const size_t rows = (size_t)joined(p, S, Hq, Hkv, Tq) * p.nsplit;
   *po = cv.take<float>(rows * dh);
   *pml = cv.take<float>(rows * 2);
 }
@@ -787,8 +792,8 @@ size_t ws_of(int dtype, int S, int max_k, int Hq, int Hkv, int dh, int Tq, int m
   const Plan p = plan(dtype, S, max_k, Hq, Hkv, dh, Tq, max_q);
   Carver cv(nullptr);
   float *po, *pml;
-  parts(cv, p.few, Tq, Hq, dh, &po, &pml);
-  parts(cv, p.tc, Tq, Hq, dh, &po, &pml);
+  parts(cv, p.few, S, Hq, Hkv, dh, Tq, &po, &pml);
+  parts(cv, p.tc, S, Hq, Hkv, dh, Tq, &po, &pml);
   return cv.bytes();
 }
 
@@ -815,12 +820,12 @@ cudaError_t attn_run(AttnArgs a, cudaStream_t s) {
     b.nsplit = x.nsplit;
     b.chunk = x.chunk;
     b.cluster = x.cluster;
-    parts(cv, x, a.Tq, a.Hq, a.dh, &b.po, &b.pml);
+    parts(cv, x, a.S, a.Hq, a.Hkv, a.dh, a.Tq, &b.po, &b.pml);
     cudaError_t e = tc ? attn_tc_launch(b, s)
                        : a.dtype == PS_F32 ? by_dh<float>(b, x.wide, s)
                                            : by_dh<__nv_bfloat16>(b, x.wide, s);
     if (e != cudaSuccess || x.nsplit == 1 || x.cluster) return e;
-    const long rows = x.per_seq > 0 ? (long)a.S * x.most * a.Hkv : (long)a.Tq * a.Hq;
+    const long rows = joined(x, a.S, a.Hq, a.Hkv, a.Tq);
     return a.dtype == PS_F32 ? join<float>(b, rows, s) : join<__nv_bfloat16>(b, rows, s);
   };
   const cudaError_t e = run(p.few, false);

@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 struct AttnTile {
   AttnSeq seq;
   long m0;             // first row
-  int num, hkv, split; // rows
+  int s, num, hkv, split; // sequence; rows
   int lo, hi, steps;   // slots that some row sees; stages of them
 
   // false: no work, or another kernel's sequence.  For whole warps.
@@ -123,7 +123,7 @@ struct AttnTile {
     auto first = [&](int s) {
       return a.per_seq > 0 ? (long)s * a.per_seq : (long)attn_q_off(a, s) * a.G / R + s;
     };
-    const int s = a.per_seq > 0 ? (int)(tile / a.per_seq) : attn_find(a.S, tile, first);
+    s = a.per_seq > 0 ? (int)(tile / a.per_seq) : attn_find(a.S, tile, first);
     seq = attn_seq(a, s);
     m0 = (tile - first(s)) * R;
     const long rows = (long)seq.n * a.G;
@@ -150,6 +150,14 @@ struct AttnTile {
     return true;
   }
 };
+
+// Which partial sums are those of row m of sequence s and KV head hkv, row `row` of Q and head
+// h: by row and head; where a kernel takes few rows of every sequence, by their numbers (a
+// long prompt beside a token has rows by the thousand that are not among them).
+__device__ __forceinline__ long attn_part(const AttnArgs& a, int s, int hkv, int m, int row,
+                                          int h) {
+  return a.per_seq > 0 ? ((long)s * a.most + m) * a.Hkv + hkv : (long)row * a.Hq + h;
+}
 
 constexpr float kAttnLog2e = 1.4426950408889634f;
 constexpr float kAttnLn2 = 0.6931471805599453f;
@@ -305,7 +313,8 @@ __device__ __forceinline__ void attn_join_warps(const AttnArgs& a, const AttnTil
         acc[kW * R * DH + 2 * r + 1] = sum;
       }
     } else if (part) {
-      const long at = ((long)row * a.Hq + h) * a.nsplit + tile.split;
+      const long at = attn_part(a, tile.s, tile.hkv, (int)tile.m0 + r, row, h) * a.nsplit +
+                      tile.split;
       *reinterpret_cast<float4*>(a.po + at * a.dh + d) = x;
       if (d == 0) {
         a.pml[2 * at] = top;

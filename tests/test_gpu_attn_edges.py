@@ -25,3 +25,14 @@ def test_keys_of_minus_infinity_have_no_weight(dtype, dh, T, n):
     O, lse = base._run(Q, K, V, *a)
     base._near(O, lse, Q, K, V, *a)
     assert torch.isfinite(O).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,dh", [(4, 4, 128), (28, 4, 64), (8, 8, 80), (4, 1, 128)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_few_rows_beside_a_prompt_on_long_caches(Hq, Hkv, dh, causal):
+    """Sequences of up to eight rows a KV head in more shares than a cluster holds, their
+    partial sums by sequence."""
+    q = [300, 1, 2, 0, 1, 1, 8, 40]
+    k = [4000, 30000, 9, 100, 20000, 0, 12345, 7000]
+    base._check(Hq + dh, q, k, Hq, Hkv, dh, BF, gap=2, pad=3, causal=causal)
+    base._check(Hq, [2000, 1], [2000, 33000], Hq, Hkv, dh, BF, causal=causal)
