@@ -750,13 +750,9 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem = SH::kBytes;
   static_assert(smem <= 227 * 1024 - 1024, "a CTA's shared memory");
   static_assert((size_t)kW * 16 * DH * 4 + 128 <= (size_t)SH::kStages * SH::kStage, "the warps' sums");
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = allow_smem(kern, smem, once);
+  if (e != cudaSuccess) return e;
   const long grid = a.tiles * a.Hkv * a.nsplit;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   CUtensorMap k{}, v{};

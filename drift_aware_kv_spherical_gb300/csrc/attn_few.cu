@@ -278,13 +278,9 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   auto kern = k_attn_few<DH, RT>;
   static_assert(F::kBytes <= 227 * 1024 - 1024, "a CTA's shared memory");
   static_assert(kW * F::kRows * DH * 4 + 8 * F::kRows <= F::kQ, "the warps' sums");
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)F::kBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = allow_smem(kern, F::kBytes, once);
+  if (e != cudaSuccess) return e;
   const long grid = a.tiles * a.Hkv * a.nsplit;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   CUtensorMap k, v;

@@ -806,13 +806,9 @@ k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMa
 template <int DH>
 cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
   auto kern = k_attn_tc<DH>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)TcSmem<DH>::kBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = allow_smem(kern, TcSmem<DH>::kBytes, once);
+  if (e != cudaSuccess) return e;
   const uintptr_t to = a.nsplit > 1 ? reinterpret_cast<uintptr_t>(a.po)
                                     : reinterpret_cast<uintptr_t>(a.O) | (uintptr_t)a.o_ld * 2;
   a.whole = to % 32 == 0;

@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "../../include/polestar.h"
+#include "device_once.h"
 
 namespace ps {
 struct TraceSink;
@@ -98,6 +99,18 @@ cudaError_t launch_ex(const cudaLaunchConfig_t& cfg, void (*kernel)(KArgs...), A
   trace_begin(cfg.stream);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
   trace_end(cfg.stream, reinterpret_cast<const void*>(kernel));
+  return e;
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current GPU (the limit is 48 KB
+// until then, and an attribute of the kernel on one GPU).  `once`: the instantiation's own.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, DeviceOnce& once) {
+  int device = -1;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess || once.done(device)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) once.set(device);
   return e;
 }
 

@@ -921,12 +921,10 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t o_bytes = (size_t)(kWarps + 1) * 8 * NB * DH * 4;
   constexpr size_t smem = q_bytes > o_bytes ? q_bytes : o_bytes;
   auto kern = k_kv4_attn<DH, NB, F32, KIND>;
-  static bool attr_set = false;
-  if (!attr_set && smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+  static DeviceOnce once;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = allow_smem(kern, smem, once);
     if (e != cudaSuccess) return e;
-    attr_set = true;
   }
   const unsigned grid = (unsigned)((long)a.B * a.Hkv * a.nsplit * a.ntile);
   if (a.cluster) {
@@ -953,12 +951,10 @@ cudaError_t launch_weight(const Kv4AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem =
       (size_t)(kWRows / 8) * (F32 ? 2 : 1) * (DH / 32) * 32 * 16 + kWarps * Ring<DH, false>::kBytes;
   auto kern = k_kv4_weight<DH, F32, GEN, ONE>;
-  static bool attr_set = false;
-  if (!attr_set && smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+  static DeviceOnce once;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = allow_smem(kern, smem, once);
     if (e != cudaSuccess) return e;
-    attr_set = true;
   }
   // rows that fit shared memory are staged once for all the slot groups of
   // a CTA, as many as leave five CTAs an SM, which is what its registers hold

@@ -929,13 +929,9 @@ k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
 template <int DH, int GEN>
 cudaError_t launch_tc(const Kv4AttnArgs& a, cudaStream_t s) {
   auto kern = k_kv4_attn_tc<DH, GEN>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)TcSmem<DH>::kBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = allow_smem(kern, TcSmem<DH>::kBytes, once);
+  if (e != cudaSuccess) return e;
   const unsigned items = (unsigned)(a.B * a.Hkv * a.ntile * a.nsplit);
   return launch_pdl(kern, dim3(items), dim3(kTcThreads), TcSmem<DH>::kBytes, s, a);
 }

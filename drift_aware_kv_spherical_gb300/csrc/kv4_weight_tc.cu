@@ -471,13 +471,9 @@ k_kv4_weight_tc(const __grid_constant__ Kv4AttnArgs a, const int blocks) {
 template <int DH, bool GEN>
 cudaError_t launch_weight_tc(Kv4AttnArgs a, cudaStream_t s) {
   auto kern = k_kv4_weight_tc<DH, GEN>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)WSmem<DH>::kBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = allow_smem(kern, WSmem<DH>::kBytes, once);
+  if (e != cudaSuccess) return e;
   // row splits: the fewest steps, the set-up and the join counted as four, of
   // the SM that takes the most CTAs
   const int blocks = ceil_div(a.Ncache, kSlots), tiles = ceil_div(a.M, kTile);

@@ -1285,13 +1285,9 @@ template <typename T, bool STAGED>
 cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
   auto kern = k_sample<T, STAGED>;
   const size_t smem = align_up(sizeof(Shared), 16) + (STAGED ? (size_t)a.slice * sizeof(T) : 0);
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         227 * 1024 - 256);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = allow_smem(kern, 227 * 1024 - 256, once);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.R * a.Z);
   cfg.blockDim = dim3(kST);

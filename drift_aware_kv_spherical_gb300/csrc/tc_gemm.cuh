@@ -509,13 +509,9 @@ cudaError_t launch_tc_gemm(const TcMaps& maps, const TcShape& sh, const Epi& epi
                            cudaStream_t s) {
   using Cfg = TcCfg<BN, NA, NB, B_MN>;
   auto kern = k_tc_gemm<BN, NA, NB, B_MN, Epi>;
-  static bool attr_set = false;  // per instantiation
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Cfg::kSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  const cudaError_t e = allow_smem(kern, Cfg::kSmem, once);
+  if (e != cudaSuccess) return e;
   TcShape shape = sh;
   shape.starve_loads = std::getenv("PS_TEST_STARVE_TMA") != nullptr ? 1 : 0;
   if constexpr (Epi::kClusterReduce) {
