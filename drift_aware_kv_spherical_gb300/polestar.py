@@ -775,13 +775,19 @@ def ps_sample(logits, u, token, prob=None, n=None, *, temperature=None, top_k=No
 
 def ps_commit_drawn(conf, role, undecided, D_blk, d_ld, d_sum, d_cnt, d_prev, suffix_sel, sel_ld,
                     params, commit, stream=None):
-    """ps_commit's rule on tokens that were drawn, conf [B][P] their confidences."""
-    lib = _lib()
+    """ps_commit's rule on tokens that were drawn, conf [B][P] their confidences, all on one
+    GPU."""
+    index = conf.get_device()
+    for t in (role, undecided, D_blk, d_sum, d_cnt, d_prev, suffix_sel, commit):
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"expected device tensors on GPU {index}, got one on {t.device}")
     B, P = conf.shape
+    at = _plain(conf, torch.float32, (B, P))
+    lib = _lib()
     st = lib.cdll.ps_commit_drawn(
-        lib.handle(), _plain(conf, torch.float32, (B, P)), B, P, _ptr(role), _ptr(undecided),
+        lib.handle(index), at, B, P, _ptr(role), _ptr(undecided),
         _ptr(D_blk), d_ld, _ptr(d_sum), _ptr(d_cnt), _ptr(d_prev), _ptr(suffix_sel), sel_ld,
-        params, _ptr(commit), _stream(stream))
+        params, _ptr(commit), raw_stream(stream, conf.device))
     _check(st, "ps_commit_drawn")
 
 
