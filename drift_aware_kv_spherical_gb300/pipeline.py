@@ -62,6 +62,12 @@ def _per_row(draw, B, P, device):
             for k, v in draw.items() if v is not None}
 
 
+def _at_one_stride(x):
+    """Whether the rows of x [B][T]... are B * T rows at one stride."""
+    B, T = x.shape[:2]
+    return B <= 1 or T <= 1 or x.stride(0) == T * x.stride(1)
+
+
 class LayerState:
     def __init__(self, w, device):
         B, N, C, d = w.B, w.N, w.C, w.d
@@ -232,13 +238,17 @@ class Pipeline:
     def attend(self, l, Q, O, lse=None, *, start=None, span=None, scale=None, stream=None):
         """Attention of Q [B][T][Hq][dh], window rows start (None: the block's first)
         and on, over layer l's cache into O; lse [B][T][Hq], span [B][T][2] as in
-        ps.ps_attn.  Q is not rotated yet (with rope: a rotated copy is read).  Calls
-        of one length on one stream share scratch, which the first one makes: graphs
-        captured on one stream must not run at the same time."""
+        ps.ps_attn.  Q is not rotated yet (with rope: a rotated copy is read).  Rows of Q may
+        lie anyhow (without rope too: those of a slice of a window's are copied), O's at one
+        stride over all windows.  Calls of one length on one stream share scratch, which the
+        first one makes: graphs captured on one stream must not run at the same time."""
         w, st = self.w, self.state[l]
         B, T = Q.shape[:2]
         if B != w.B:
             raise ValueError(f"expected queries of {w.B} windows, got {tuple(Q.shape)}")
+        if not _at_one_stride(O):
+            raise ValueError(f"the windows' rows of O must lie at one stride: got {tuple(O.shape)}, "
+                             f"strides {O.stride()}")
         start = w.blk_start if start is None else start
         if T not in self._spans:
             if Q.is_cuda and torch.cuda.is_current_stream_capturing():
@@ -263,6 +273,9 @@ class Pipeline:
                 torch.add(self.origin, start, out=at)
             ps.ps_rope(self.rope, Q, Q_out=turned, off=at, stream=stream)
             Q = turned
+        elif not _at_one_stride(Q):
+            with _on(stream, Q.device):
+                Q = turned.copy_(Q)
         rows = lambda x: x.view(-1, *x.shape[2:])
         ps.ps_attn(rows(Q), rows(st.Kc), rows(st.Vc), rows(O), None if lse is None else rows(lse),
                    span=None if span is None else rows(span), scale=scale, max_q=max(T, 1),
