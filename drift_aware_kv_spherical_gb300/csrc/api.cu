@@ -781,7 +781,7 @@ extern "C" ps_status ps_attn(ps_handle h, const ps_attn_rows* q, void* O, float*
   a.dtype = q->dtype; a.S = q->S; a.Tq = q->Tq; a.Tk = q->Tk;
   a.Hq = q->Hq; a.Hkv = q->Hkv; a.G = q->Hq / q->Hkv; a.dh = q->dh;
   a.causal = q->causal != 0; a.max_q = q->max_q; a.max_k = q->max_k; a.scale = q->scale;
-  a.O = O; a.lse = lse; a.ws = ws; a.status = h->status; a.num_sms = h->num_sms;
+  a.O = O; a.lse = lse; a.ws = ws; a.status = h->status;
   DeviceScope dev(h->device);
   if (dev.err != cudaSuccess) return launch_status(dev.err);
   return launch_status(attn_run(a, static_cast<cudaStream_t>(stream)));

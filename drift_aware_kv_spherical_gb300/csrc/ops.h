@@ -164,7 +164,7 @@ struct AttnArgs {
   const void* Q; const void* K; const void* V; long q_ld, k_ld, v_ld, o_ld;
   const int32_t* q_off; const int32_t* k_off; const int32_t* k_len; const int32_t* span;
   int dtype, S, Tq, Tk, Hq, Hkv, G, dh; bool causal; int max_q, max_k; float scale;
-  void* O; float* lse; void* ws; int* status; int num_sms;
+  void* O; float* lse; void* ws; int* status;
   // set by attn_run
   Quotient by_g;
   int least, most;      // query rows a KV head of the sequences that a kernel takes
