@@ -493,7 +493,7 @@ k_attn(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap t
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           acc[(warp * 16 + g + 8 * r) * DH + TL::column(d, i)] = o[d][2 * r + i];
-    attn_join_warps<T, DH, 16>(a, tile, acc, &s_m[0][0], &s_l[0][0], &s_bad);
+    attn_join_warps<T, DH, 16, true>(a, tile, acc, &s_m[0][0], &s_l[0][0], &s_bad);
   } else {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -537,7 +537,7 @@ k_attn(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap t
       for (int k = 0; k < 8; ++k)
         if (bad >> (4 * k) & 15) {
           const int tk = __shfl_sync(0xffffffffu, t, 4 * k), hk = __shfl_sync(0xffffffffu, h, 4 * k);
-          attn_redo<T>(a, seq, tk, hk);
+          attn_redo_call<T>(a, seq, tk, hk);
         }
     }
   }
@@ -613,7 +613,7 @@ k_attn_join(const __grid_constant__ AttnArgs a) {
       attn_add4(x, l, s_o[tid + k * lanes], s_l[tid + k * lanes], 1.f);
     fine = attn_store4<T>(a, r, h, d, x, top, l);
   }
-  if (__syncthreads_or(!fine) && tid < 32) attn_redo<T>(a, seq, t, h);
+  if (__syncthreads_or(!fine) && tid < 32) attn_redo_call<T>(a, seq, t, h);
 }
 
 // ... else a warp does (18800 rows of two shares 12 us, by a CTA of 128 threads each 38).
@@ -643,7 +643,7 @@ k_attn_join_rows(const __grid_constant__ AttnArgs a, int count) {
                 attn_exp2(pml[2 * k] - base));
     fine = attn_store4<T>(a, seq.q0 + t, h, d, x, top, l) && fine;
   }
-  if (__any_sync(0xffffffffu, !fine)) attn_redo<T>(a, seq, t, h);
+  if (__any_sync(0xffffffffu, !fine)) attn_redo_call<T>(a, seq, t, h);
 }
 
 // ---------------------------------------------------------------- host

@@ -269,7 +269,7 @@ k_attn_few(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorM
         acc[(warp * F::kRows + r) * DH + 16 * d + g + 8] = o[d][i][e + 2];
       }
     }
-  attn_join_warps<__nv_bfloat16, DH, F::kRows>(a, tile, acc, &s_m[0][0], &s_l[0][0], &s_bad);
+  attn_join_warps<__nv_bfloat16, DH, F::kRows, false>(a, tile, acc, &s_m[0][0], &s_l[0][0], &s_bad);
 }
 
 template <int DH, int RT>
