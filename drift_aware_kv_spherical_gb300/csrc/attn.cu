@@ -9,12 +9,14 @@
 //           their sums at the end (bf16 heads of 64 and more: k_attn_few, attn_few.cu)
 //   wide    64 rows or 128, 16 a warp; every warp takes all slots of a stage (fp32: 16 at a
 //           time, so that more products do not wait on one another)
-// bf16 products are exact (m16n8k16); fp32 operands are split into two tf32 terms,
-// three products (m16n8k8): the term left out is 2^-22 of a product.  The indices
+// bf16 products are exact (m16n8k16), the weights rounded to bf16 on their way to V (2^-8 of
+// one at most; their sum is of the unrounded ones); fp32 operands are split into two tf32 terms,
+// three products (m16n8k8): the term left out is 2^-22 of a product, and so is what
+// ex2.approx is off by.  The indices
 // of a contraction may be permuted freely, so fp32 fragments are loaded as vectors.
 // Rows of a stage lie an odd number of 16-byte units apart: no bank conflicts.
 // What bounds fp32: three products of mma.sync and the splitting of K and V, which every
-// warp repeats; 2048 x 2048 rows of 8 heads of 128 take 506 us, tensor cores 37 % busy,
+// warp repeats; 2048 x 2048 rows of 8 heads of 128 take 513 us, tensor cores 36 % busy,
 // issue slots 46 %, two CTAs an SM at 255 registers.  Leading terms are summed by adds that
 // round; low terms in accumulators of their own, so that no product waits on another.
 //
@@ -711,7 +713,7 @@ Plan plan(int dtype, int S, int max_k, int Hq, int Hkv, int dh, int Tq, int max_
       ctas = (long)S * Hkv;
     } else {
       // Wide tiles read K and V a quarter or an eighth as often, and leave SMs idle where
-      // there are few.  fp32: 2048^2 x 32 heads x 128 2509 -> 1857 us, 1024^2 x 8 x 64 (128
+      // there are few.  fp32: 2048^2 x 32 heads x 128 2509 -> 1878 us, 1024^2 x 8 x 64 (128
       // tiles) 116 -> 97, but 3 x 77 rows of 4 heads (16 tiles) 17.5 -> 28, and in shares
       // 4 x 32 x 8 (32 tiles) 69 -> 81.  bf16 gains with shares too, heads of 256:
       // 2 x 1024^2 x 8 292 -> 91, 71 x 32 on 16 K slots 583 -> 206, 6 x 100 x 4 on 900

@@ -6,15 +6,16 @@
 // turned round: slots are the 16 of the m16n8k16 tile and rows its 8, S^T = K Q^T and
 // O^T += V^T P^T, so that 7 rows of a group of heads fill a tile that rows on the 16
 // would leave half empty: half the products, and half of O's registers.  P^T comes out of
-// the accumulators of S^T by a transposing move of 8x8 halves.
+// the accumulators of S^T by a transposing move of 8x8 halves, rounded to bf16 (V's type: half
+// a step, 2^-8 at most, of a weight; the row's sum is of the unrounded ones).
 // The running maximum of a row is common to the warp and follows the scores only when one
 // passes it by 2^kGrow (P carries a factor up to that): most steps vote once and
 // exchange nothing.
 //
 // One token of 28/4 heads for each of 8 sequences of up to 32 K slots: 52 us, 75 % of the
 // memory's nominal rate (86 % of a copy's); with rows as the 16 it was 85 us for 8 tokens
-// where this takes 75.  What bounds it is the latency of a warp's own steps, 12 warps an SM
-// at three stages of two 16 KB tiles a CTA (two stages and a fourth CTA were no faster).
+// where this takes 75.  What bounds it is the latency of a warp's own steps, 12 warps an SM:
+// three CTAs of two stages of two 16 KB tiles each.
 #include <algorithm>
 
 #include "attn.cuh"

@@ -18,7 +18,10 @@
 // first one of the next item, whose queries are loaded as soon as the last S of this
 // one has read its own.  The commit that announces S(j+1) also says that P V(j) is
 // done, so O may be rescaled then.  It is rescaled only when a row's maximum has grown
-// by 2^kGrow or more: until then P just carries a factor up to that.
+// by 2^kGrow or more: until then P just carries a factor up to that.  P is rounded to bf16,
+// the type that V is multiplied in: half a step, 2^-8 at most, of a weight, the row's sum being
+// of the unrounded ones in fp32.  Of O that makes an error of 0.0023 of its norm where its own
+// rounding makes 0.0016; a second term of P would be half as many products again.
 //
 // What bounds it: the chain of a step, product, softmax, product; the other row tile hides
 // half of it.  2 x 4096 rows of 32 heads on 4096 slots: 338 us, 1.63 PFLOP/s, tensor

@@ -32,7 +32,8 @@ each KV head still holds.
 With rope (a ps.RopeTable) the keys that a refresh wrote are rotated where they
 lie in the cache, each as the position origin[b] + row, before the 4-bit cache
 takes them; `attend` rotates a block's queries and reads the cache with them
-(without rope it reads the cache as it is).
+(without rope it reads the cache as it is).  `self.kv4[l].attend` takes its queries
+as they come: for a 4-bit cache of rotated keys the caller rotates them.
 
 With draw (temperature, top_k, top_p, min_p as in ps.ps_sample, each a number or
 a [B, P] array) the commit step draws the tokens by `u` [B, P], which the caller

@@ -697,7 +697,7 @@ ps_status ps_rope(ps_handle h, const ps_rope_rows* r, const ps_rope_part* parts,
  * max_q, max_k: the most rows and slots of a sequence, as well as the caller knows
  *   them: they choose a launch and its workspace, never a result's rows or slots.
  * Sums and statistics in fp32.  bf16: products exact, the weights rounded to bf16 on
- * their way into the product with V.  f32: to some 2^-21 of the terms.  Deterministic.
+ * their way into the product with V (lse and the weights' sum are of the unrounded ones).  f32: to some 2^-21 of the terms.  Deterministic.
  * Sizes: S, Tq >= 0 (0: no-op), S <= 2^20, Tq * Hq <= 2^30, Tk < 2^31 - 2^16,
  *   Hkv <= 512, Hq / Hkv <= 4096, dh % 16 == 0, dh <= 256, max_q, max_k >= 1.
  * Workspace: ps_workspace_bytes(PS_OP_ATTN, B = S, N = max_k, Hq, Hkv, dh, P = Tq,
@@ -729,8 +729,8 @@ ps_status ps_attn(ps_handle h, const ps_attn_rows* a, void* O, float* lse, void*
  * the probability it was drawn with.
  *
  * Per row r, of V logits l (a NaN counts as -inf):
- *   w_i = exp((l_i - max l) / T)     T = temperature[r]; T <= 0 or NaN: 1, and the
- *                                    token is the first arg-max in place of a draw
+ *   w_i = exp((l_i - max l) / T)     T = temperature[r] (1e-30 at least); T <= 0 or NaN: 1,
+ *                                    and the token is the first arg-max in place of a draw
  * in descending order of l, ties to the lower index, what is left is
  *   the first top_k                  (top_k <= 0: all),
  *   of those the shortest prefix whose sum of w is at least top_p times theirs
