@@ -686,7 +686,7 @@ ps_status ps_rope(ps_handle h, const ps_rope_rows* r, const ps_rope_part* parts,
  *   j <= m - n + t           if causal (its rows are the last ones of the slots),
  *   span[0] <= j < span[1]   if span is given (for the row of Q).
  * s = scale * <q, k>;  O = softmax over the seen slots of s, times V;  lse = ln sum
- * exp s.  A row that sees nothing gives O = 0, lse = -inf.  Query head h reads KV head
+ * exp s.  A row that sees nothing, or no score above -inf, gives O = 0, lse = -inf.  Query head h reads KV head
  * h / (Hq / Hkv).  What a row does not see never reaches it, NaN or not.  Rows of
  * O and lse that belong to no sequence are left as they are.  Offsets outside the
  * tensors are cut to them; q_off must ascend.

@@ -36,3 +36,24 @@ def test_few_rows_beside_a_prompt_on_long_caches(Hq, Hkv, dh, causal):
     k = [4000, 30000, 9, 100, 20000, 0, 12345, 7000]
     base._check(Hq + dh, q, k, Hq, Hkv, dh, BF, gap=2, pad=3, causal=causal)
     base._check(Hq, [2000, 1], [2000, 33000], Hq, Hkv, dh, BF, causal=causal)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 1.0])
+def test_rows_without_a_score_above_minus_infinity(dtype, T, bad):
+    """All that they see has no weight: O is 0 whatever V holds, lse -inf."""
+    Q, K, V = base._data(T, T, 3, 4, 2, 64, dtype)
+    Q = torch.sign(Q)
+    Q[..., 3] = 0.5
+    K[1:, :, 3] = -float("inf")
+    V[1:, :, ::5] = bad
+    span = np.tile([[1, 3]], (T, 1))
+    span[::3] = [[0, 1]]              # these see the one slot that is like others
+    a = (np.array([0, T]), np.array([0]), np.array([3]))
+    O, lse = base._run(Q, K, V, *a, span=span)
+    rest = np.arange(T) % 3 != 0
+    assert not O[rest].any() and torch.isneginf(lse[rest]).all()
+    one = len(O[::3])
+    base._near(O[::3], lse[::3], Q[::3], K[:1], V[:1], np.array([0, one]), np.array([0]),
+               np.array([1]))         # (fp32: V's two tf32 terms leave 2^-22 of it)
