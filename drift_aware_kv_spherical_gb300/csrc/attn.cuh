@@ -242,12 +242,15 @@ __device__ __forceinline__ void attn_redo(const AttnArgs& a, const AttnSeq& s, i
   }
   T* to = static_cast<T*>(a.O) + (long)(s.q0 + t) * a.o_ld + (long)h * a.dh + 2 * lane;
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (l == 0.f) {  // no weight at all: nothing of V, infinite or not
+#pragma unroll
+    for (int e = 0; e < 2 * E; ++e) o[e] = 0.f;
+  }
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if (2 * lane + 64 * e < a.dh) {
-      // (no weight at all: nothing of V, infinite or not)
-      Store<T>::put(to + 64 * e, l == 0.f ? 0.f : o[2 * e] * inv);
-      Store<T>::put(to + 64 * e + 1, l == 0.f ? 0.f : o[2 * e + 1] * inv);
+      Store<T>::put(to + 64 * e, o[2 * e] * inv);
+      Store<T>::put(to + 64 * e + 1, o[2 * e + 1] * inv);
     }
   if (lane == 0 && a.lse != nullptr) a.lse[(long)(s.q0 + t) * a.Hq + h] = attn_lse(m, l);
 }
